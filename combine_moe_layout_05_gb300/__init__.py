@@ -11,11 +11,13 @@ from ._binding import (MOE_DEV_ERR_DUPLICATE, MOE_DEV_ERR_EXPERT_RANGE,
                        LayoutBuffers, MoeError, declared_functions,
                        library_path, load, moe_combine, moe_combine_fp8,
                        moe_combine_rank_partial,
-                       moe_dispatch, moe_dispatch_recv, moe_dispatch_send,
+                       moe_dispatch, moe_dispatch_int8, moe_dispatch_recv, moe_dispatch_send,
+                       moe_expert_matmul_int8,
                        moe_layout, moe_layout_dispatch,
                        moe_layout_dispatch_kernels, moe_layout_kernels, moe_layout_static,
                        moe_layout_workspace_bytes,
-                       moe_status_string)
+                       moe_route, moe_route_backward, moe_route_workspace_bytes,
+                       moe_status_string, RouteBuffers)
 
 __all__ = [
     "MOE_DEV_ERR_DUPLICATE", "MOE_DEV_ERR_EXPERT_RANGE", "MOE_DEV_ERR_REGION_OVERFLOW",
@@ -25,5 +27,6 @@ __all__ = [
     "moe_combine_fp8", "moe_combine_rank_partial",
     "moe_dispatch", "moe_dispatch_recv", "moe_dispatch_send", "moe_layout", "moe_layout_dispatch", "moe_layout_dispatch_kernels", "moe_layout_kernels", "moe_layout_static",
     "moe_layout_workspace_bytes",
-    "moe_status_string",
+    "moe_route", "moe_route_backward", "moe_route_workspace_bytes",
+    "moe_status_string", "RouteBuffers",
 ]

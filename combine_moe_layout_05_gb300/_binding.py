@@ -78,6 +78,17 @@ def load(path: str | None = None):
             lib.moe_dispatch_recv.restype = ctypes.c_int
             lib.moe_layout_static.argtypes = [P, i32, i32, i32, i32, P, P, P, P, P, P, P]
             lib.moe_layout_static.restype = ctypes.c_int
+            f32 = ctypes.c_float
+            lib.moe_route_workspace_bytes.argtypes = [i32, i32]
+            lib.moe_route_workspace_bytes.restype = sz
+            lib.moe_route.argtypes = [P, i32, i32, i32, i32, i32, f32, P, P, P, P, P, P, P, sz, P]
+            lib.moe_route.restype = ctypes.c_int
+            lib.moe_route_backward.argtypes = [P, i32, i32, i32, i32, i32, f32, P, P, P, P, P, P, P]
+            lib.moe_route_backward.restype = ctypes.c_int
+            lib.moe_dispatch_int8.argtypes = [P, i32, i32, i32, P, P, P, P]
+            lib.moe_dispatch_int8.restype = ctypes.c_int
+            lib.moe_expert_matmul_int8.argtypes = [P, P, P, P, P, i32, i32, i32, i32, P, P]
+            lib.moe_expert_matmul_int8.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -336,6 +347,136 @@ def moe_combine_fp8(expert_out, expert_scales, topk_weights, dst_row, out,
     st = load().moe_combine_fp8(_ptr(expert_out), _ptr(expert_scales), _ptr(topk_weights),
                                 _ptr(dst_row), T, H, K, _ptr(out), _stream(stream))
     _raise("moe_combine_fp8", st)
+
+
+def moe_dispatch_int8(tokens, dst_row, packed, scales, stream=None) -> None:
+    """Pack token rows into their K slots as int8 codes with one scale a row."""
+    T, H = tokens.shape
+    K = dst_row.shape[1] if dst_row.dim() == 2 else 1
+    _check("tokens", tokens, torch.bfloat16)
+    _check("dst_row", dst_row, torch.int32)
+    _check("packed", packed, torch.int8)
+    _check("scales", scales, torch.float32)
+    if dst_row.numel() != T * K or packed.numel() < T * K * H or scales.numel() < T * K:
+        raise ValueError("moe_dispatch_int8: dst_row/packed/scales have the wrong size")
+    st = load().moe_dispatch_int8(_ptr(tokens), T, H, K, _ptr(dst_row), _ptr(packed),
+                                  _ptr(scales), _stream(stream))
+    _raise("moe_dispatch_int8", st)
+
+
+def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
+                           stream=None) -> None:
+    """Packed int8 rows times their experts' int8 weights (see include/moe_layout.h)."""
+    rows, H = x.shape
+    E, N = weights.shape[0], weights.shape[1]
+    _check("x", x, torch.int8)
+    _check("x_scales", x_scales, torch.float32)
+    _check("weights", weights, torch.int8)
+    _check("w_scales", w_scales, torch.float32)
+    _check("expert_offsets", expert_offsets, torch.int32)
+    _check("out", out, torch.bfloat16)
+    if weights.dim() != 3 or weights.shape[2] != H or w_scales.numel() != E * N \
+            or x_scales.numel() < rows or expert_offsets.numel() < E + 1 \
+            or out.numel() < rows * N or out.shape[-1] != N:
+        raise ValueError("moe_expert_matmul_int8: argument sizes disagree")
+    st = load().moe_expert_matmul_int8(_ptr(x), _ptr(x_scales), _ptr(weights), _ptr(w_scales),
+                                       _ptr(expert_offsets), rows, H, N, E, _ptr(out),
+                                       _stream(stream))
+    _raise("moe_expert_matmul_int8", st)
+
+
+def moe_route_workspace_bytes(T: int, E: int) -> int:
+    return int(load().moe_route_workspace_bytes(T, E))
+
+
+def _logits_type(fn: str, logits) -> int:
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{fn}: logits must be float32 or bfloat16, got {logits.dtype}")
+    return int(logits.dtype == torch.bfloat16)
+
+
+def moe_route(logits, topk_ids, topk_weights, expert_counts, routed_tokens, loss,
+              renormalize: bool = True, loss_coef: float = 1.0, token_mask=None,
+              workspace=None, stream=None) -> None:
+    """Router logits to top-k ids, weights, counts and the balance loss (see
+    include/moe_layout.h)."""
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    bf16 = _logits_type("moe_route", logits)
+    _check("logits", logits, logits.dtype)
+    _check("topk_ids", topk_ids, torch.int32)
+    _check("topk_weights", topk_weights, torch.float32)
+    _check("expert_counts", expert_counts, torch.int32)
+    _check("routed_tokens", routed_tokens, torch.int32)
+    _check("loss", loss, torch.float32)
+    if token_mask is not None:
+        _check("token_mask", token_mask, torch.bool)
+        if token_mask.numel() != T:
+            raise ValueError("moe_route: token_mask has the wrong size")
+    if topk_ids.numel() != T * K or topk_weights.numel() != T * K or expert_counts.numel() < E \
+            or routed_tokens.numel() < 1 or loss.numel() < 1:
+        raise ValueError("moe_route: output arrays have the wrong size")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = load().moe_route(_ptr(logits), bf16, T, E, K, int(bool(renormalize)), float(loss_coef),
+                          _ptr(token_mask), _ptr(topk_ids), _ptr(topk_weights),
+                          _ptr(expert_counts), _ptr(routed_tokens), _ptr(loss),
+                          _ptr(workspace), ws_bytes, _stream(stream))
+    _raise("moe_route", st)
+
+
+def moe_route_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weights, grad_loss,
+                       grad_logits, renormalize: bool = True, loss_coef: float = 1.0,
+                       stream=None) -> None:
+    """Gradient of moe_route's weights and loss to the logits; grad_weights or
+    grad_loss may be None (zero)."""
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    bf16 = _logits_type("moe_route_backward", logits)
+    _check("logits", logits, logits.dtype)
+    _check("grad_logits", grad_logits, logits.dtype)
+    _check("topk_ids", topk_ids, torch.int32)
+    _check("expert_counts", expert_counts, torch.int32)
+    _check("routed_tokens", routed_tokens, torch.int32)
+    _check("grad_weights", grad_weights, torch.float32)
+    _check("grad_loss", grad_loss, torch.float32)
+    if topk_ids.numel() != T * K or expert_counts.numel() < E or routed_tokens.numel() < 1 \
+            or grad_logits.numel() != T * E \
+            or (grad_weights is not None and grad_weights.numel() != T * K) \
+            or (grad_loss is not None and grad_loss.numel() != 1):
+        raise ValueError("moe_route_backward: argument sizes disagree")
+    st = load().moe_route_backward(_ptr(logits), bf16, T, E, K, int(bool(renormalize)),
+                                   float(loss_coef), _ptr(topk_ids), _ptr(expert_counts),
+                                   _ptr(routed_tokens), _ptr(grad_weights), _ptr(grad_loss),
+                                   _ptr(grad_logits), _stream(stream))
+    _raise("moe_route_backward", st)
+
+
+class RouteBuffers:
+    """Device buffers for routing T tokens over E experts, K a token (allocated by torch)."""
+
+    def __init__(self, T: int, K: int, E: int, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.T, self.K, self.E = T, K, E
+        self.topk_ids = torch.empty((T, K), **i32)
+        self.topk_weights = torch.empty((T, K), dtype=torch.float32, device=device)
+        self.expert_counts = torch.empty(E, **i32)
+        self.routed_tokens = torch.empty(1, **i32)
+        self.loss = torch.empty(1, dtype=torch.float32, device=device)
+        self.workspace = torch.empty(moe_route_workspace_bytes(T, E), dtype=torch.uint8,
+                                     device=device)
+
+    def run(self, logits, renormalize: bool = True, loss_coef: float = 1.0, token_mask=None,
+            stream=None) -> "RouteBuffers":
+        moe_route(logits, self.topk_ids, self.topk_weights, self.expert_counts,
+                  self.routed_tokens, self.loss, renormalize, loss_coef, token_mask,
+                  self.workspace, stream)
+        return self
+
+    def backward(self, logits, grad_weights, grad_loss, grad_logits, renormalize: bool = True,
+                 loss_coef: float = 1.0, stream=None) -> None:
+        """Gradient to the logits of the run() before it."""
+        moe_route_backward(logits, self.topk_ids, self.expert_counts, self.routed_tokens,
+                           grad_weights, grad_loss, grad_logits, renormalize, loss_coef, stream)
 
 
 class LayoutBuffers:

@@ -38,6 +38,14 @@ moe_status_t rows_ok(int32_t T, int32_t H, int32_t K)
     return MOE_OK;
 }
 
+bool route_sizes_ok(int32_t T, int32_t E, int32_t K)
+{
+    return T >= 0 && E >= 1 && E <= MOE_MAX_EXPERTS && K >= 1 && K <= MOE_MAX_TOPK && K <= E &&
+           (int64_t)T * K <= (int64_t)INT32_MAX - 1;
+}
+
+bool flag(int32_t v) { return v == 0 || v == 1; }
+
 }  // namespace
 
 extern "C" {
@@ -262,6 +270,86 @@ int32_t moe_layout_kernels(int32_t T, int32_t K, int32_t E)
     if (!layout_sizes_ok(T, K, E)) return 0;
     if (moe::plan_layout(T, K, E).single_launch) return 1;
     return moe::layout_ranked(T, K, E) ? 2 : 3;
+}
+
+size_t moe_route_workspace_bytes(int32_t T, int32_t E)
+{
+    if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS) return 0;
+    return moe::route_workspace_bytes(T, E);
+}
+
+moe_status_t moe_route(const void *logits, int32_t bf16, int32_t T, int32_t E, int32_t K,
+                       int32_t renormalize, float loss_coef, const uint8_t *token_mask,
+                       int32_t *topk_ids, float *topk_weights, int32_t *expert_counts,
+                       int32_t *routed_tokens, float *loss, void *workspace,
+                       size_t workspace_bytes, cudaStream_t stream)
+{
+    const CallRange range("moe_route");
+    if (!route_sizes_ok(T, E, K) || !flag(bf16) || !flag(renormalize)) return MOE_ERR_INVALID_ARG;
+    if (!expert_counts || !routed_tokens || !loss) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!logits || !topk_ids || !topk_weights)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, bf16 ? 2 : 4)) return MOE_ERR_ALIGNMENT;
+    const void *p4[] = {topk_ids, topk_weights, expert_counts, routed_tokens, loss};
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return MOE_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < moe::route_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
+    return cuda_status(moe::launch_route(logits, bf16, T, E, K, renormalize, loss_coef, token_mask,
+                                         topk_ids, topk_weights, expert_counts, routed_tokens, loss,
+                                         workspace, stream));
+}
+
+moe_status_t moe_route_backward(const void *logits, int32_t bf16, int32_t T, int32_t E, int32_t K,
+                                int32_t renormalize, float loss_coef, const int32_t *topk_ids,
+                                const int32_t *expert_counts, const int32_t *routed_tokens,
+                                const float *grad_weights, const float *grad_loss,
+                                void *grad_logits, cudaStream_t stream)
+{
+    const CallRange range("moe_route_backward");
+    if (!route_sizes_ok(T, E, K) || !flag(bf16) || !flag(renormalize)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_ids || !expert_counts || !routed_tokens || !grad_logits)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, bf16 ? 2 : 4) || !aligned(grad_logits, bf16 ? 2 : 4)) return MOE_ERR_ALIGNMENT;
+    const void *p4[] = {topk_ids, expert_counts, routed_tokens, grad_weights, grad_loss};
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return MOE_ERR_ALIGNMENT;
+    return cuda_status(moe::launch_route_backward(logits, bf16, T, E, K, renormalize, loss_coef,
+                                                  topk_ids, expert_counts, routed_tokens,
+                                                  grad_weights, grad_loss, grad_logits, stream));
+}
+
+moe_status_t moe_dispatch_int8(const void *tokens, int32_t T, int32_t H, int32_t K,
+                               const int32_t *dst_row, void *packed, float *scales,
+                               cudaStream_t stream)
+{
+    const CallRange range("moe_dispatch_int8");
+    moe_status_t s = rows_ok(T, H, K);
+    if (s != MOE_OK) return s;
+    if (H % 16 != 0) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!tokens || !dst_row || !packed || !scales) return MOE_ERR_INVALID_ARG;
+    if (!aligned(tokens, 16) || !aligned(packed, 16) || !aligned(dst_row, 4) || !aligned(scales, 4))
+        return MOE_ERR_ALIGNMENT;
+    return cuda_status(moe::launch_dispatch_int8(tokens, T, H, K, dst_row, packed, scales, stream));
+}
+
+moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales, const void *weights,
+                                    const float *w_scales, const int32_t *expert_offsets,
+                                    int32_t rows, int32_t H, int32_t N, int32_t E, void *out,
+                                    cudaStream_t stream)
+{
+    const CallRange range("moe_expert_matmul_int8");
+    if (rows < 0 || H < 16 || H > 65536 || H % 16 != 0 || N < 1 || E < 1 || E > MOE_MAX_EXPERTS ||
+        (int64_t)E * N > (int64_t)INT32_MAX)
+        return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !x_scales || !weights || !w_scales || !expert_offsets || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(weights, 16) || !aligned(out, 16) || !aligned(x_scales, 4) ||
+        !aligned(w_scales, 4) || !aligned(expert_offsets, 4))
+        return MOE_ERR_ALIGNMENT;
+    return cuda_status(moe::launch_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets,
+                                                      rows, H, N, E, out, stream));
 }
 
 }  // extern "C"

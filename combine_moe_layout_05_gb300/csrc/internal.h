@@ -100,6 +100,26 @@ cudaError_t launch_dispatch_recv(const void *priv, const float *priv_scales, int
                                  const int32_t *rank_offsets, int R, int T, int H, int K,
                                  int fp8, void *packed, float *scales, cudaStream_t stream);
 
+// Token rows quantised to int8 (one scale a row) and packed into their slots.
+cudaError_t launch_dispatch_int8(const void *tokens, int T, int H, int K, const int32_t *dst_row,
+                                 void *packed, float *scales, cudaStream_t stream);
+
+// Packed int8 rows times their experts' int8 weights.
+cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, const void *w,
+                                      const float *w_scales, const int32_t *offsets, int rows,
+                                      int H, int N, int E, void *out, cudaStream_t stream);
+
+// Router logits (bf16 != 0: bf16, else fp32) to ids, weights, counts and the
+// balance loss; and the gradient back to the logits.
+size_t route_workspace_bytes(int T, int E);
+cudaError_t launch_route(const void *logits, int bf16, int T, int E, int K, int renorm, float coef,
+                         const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts,
+                         int32_t *routed, float *loss, void *workspace, cudaStream_t stream);
+cudaError_t launch_route_backward(const void *logits, int bf16, int T, int E, int K, int renorm,
+                                  float coef, const int32_t *ids, const int32_t *counts,
+                                  const int32_t *routed, const float *grad_weights,
+                                  const float *grad_loss, void *grad, cudaStream_t stream);
+
 // Layout and dispatch together: one fused kernel when
 // layout_dispatch_fused() says the batch is small enough, else the layout
 // kernels followed by the dispatch kernel.

@@ -357,6 +357,132 @@ MOE_API moe_status_t moe_layout_static(const int32_t *topk_ids, int32_t T, int32
                                        int32_t *src_token, int32_t *dst_row,
                                        uint32_t *dev_error, cudaStream_t stream);
 
+/*
+ * moe_route -- from router logits to the routing that the calls above take,
+ * with the per-expert counts and the balance loss, in one pass.
+ *
+ * An expert is open for a token when the token is not masked and its logit is
+ * above -inf; a token with an open expert is routed.  With x the logits:
+ *
+ *   p[t,e]  = exp(x[t,e] - m_t) / sum over open e' of exp(x[t,e'] - m_t),
+ *             0 for an expert that is not open
+ *   topk_ids[t,:]      the K open experts of largest logit, largest first, ties
+ *                      to the lowest index; -1 where fewer than K are open
+ *   topk_weights[t,k]  p at topk_ids[t,k], divided by the sum of the token's K
+ *                      when renormalize == 1; 0 where topk_ids is -1
+ *   expert_counts[e]   entries of topk_ids equal to e (moe_layout's counts)  [E]
+ *   routed_tokens      n, the number of routed tokens                        [1]
+ *   loss               coef * E * sum over e of (expert_counts[e] / (K n)) *
+ *                      (sum over t of p[t,e] / n); 0 when n == 0             [1]
+ *
+ * All sums are fp32 in an order that the sizes fix: the same inputs give the
+ * same bits.  A NaN logit is never chosen; a NaN or +inf logit of a token that
+ * is not masked makes the token's weights and the loss NaN.  A masked token's
+ * logits are not looked at.  An id of -1 is what moe_layout reports as
+ * MOE_DEV_ERR_EXPERT_RANGE and then skips.
+ *
+ * logits      [T,E], fp32 (bf16 == 0) or bf16 (bf16 == 1), aligned to their type.
+ * token_mask  [T] bytes or NULL; 0 masks the token (padding).
+ * topk_ids [T,K] int32, topk_weights [T,K] fp32, expert_counts [E] int32,
+ * routed_tokens [1] int32, loss [1] fp32: 4-byte aligned.
+ * workspace   moe_route_workspace_bytes(T,E) bytes (never 0 for valid sizes),
+ *             16-byte aligned; its contents on entry do not matter.
+ * T >= 0, 1 <= E <= MOE_MAX_EXPERTS, 1 <= K <= min(E, MOE_MAX_TOPK),
+ * T*K < 2^31.  T == 0 writes zero counts and loss.  Asynchronous on `stream`;
+ * may be captured.
+ */
+MOE_API size_t moe_route_workspace_bytes(int32_t T, int32_t E);
+
+MOE_API moe_status_t moe_route(const void *logits, int32_t bf16, int32_t T, int32_t E, int32_t K,
+                               int32_t renormalize, float loss_coef, const uint8_t *token_mask,
+                               int32_t *topk_ids, float *topk_weights, int32_t *expert_counts,
+                               int32_t *routed_tokens, float *loss, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * moe_route_backward -- the gradient of moe_route's weights and loss with
+ * respect to the logits.
+ *
+ * The choice of experts and the counts are constants.  With dw = grad_weights,
+ * w the weights, a[e] = grad_loss * coef * E * expert_counts[e] / (K n^2):
+ *
+ *   grad_logits[t,e] = p[t,e] (a[e] - sum over j of p[t,j] a[j])
+ *     + renormalize == 1:  w[t,k] (dw[t,k] - sum over j of w[t,j] dw[t,j])
+ *                          at e = topk_ids[t,k]
+ *     + renormalize == 0:  p[t,e] ([e == topk_ids[t,k]] dw[t,k]
+ *                          - sum over j of w[t,j] dw[t,j])
+ *
+ * computed in fp32 and rounded once to the logits' type.  The probabilities
+ * are computed again from the logits.  A token whose ids are all outside [0,E)
+ * gets zeros (so the mask need not be given again).
+ *
+ * topk_ids, expert_counts, routed_tokens: moe_route's outputs for the same
+ * logits.  grad_weights [T,K] fp32 or NULL (zeros); grad_loss [1] fp32 on the
+ * device or NULL (zero).  grad_logits [T,E] in the logits' type; must not
+ * overlap the logits.  Sizes as for moe_route; T == 0 is a no-op.
+ */
+MOE_API moe_status_t moe_route_backward(const void *logits, int32_t bf16, int32_t T, int32_t E,
+                                        int32_t K, int32_t renormalize, float loss_coef,
+                                        const int32_t *topk_ids, const int32_t *expert_counts,
+                                        const int32_t *routed_tokens, const float *grad_weights,
+                                        const float *grad_loss, void *grad_logits,
+                                        cudaStream_t stream);
+
+/*
+ * moe_dispatch_int8 -- moe_dispatch with rows quantised to int8.
+ *
+ * For every token t and k with 0 <= dst_row[t,k] < T*K:
+ *
+ *   scale = max |tokens[t, :]| * (1/127)                    (fp32 product with
+ *                                                           the fp32 nearest 1/127)
+ *   packed[dst_row[t,k], j] = rint(tokens[t, j] / scale)    (fp32 divide; ties
+ *                             to even; in [-127, 127])
+ *   scales[dst_row[t,k]] = scale
+ *
+ * A row of zeros stores scale 0 and codes 0.  A row that holds a NaN or an
+ * infinity stores scale NaN and codes 0, so that what is computed from it is
+ * NaN.  With K == 1 and dst_row[t] = t it quantises a matrix row by row.
+ *
+ * tokens  [T,H] bf16, 16-byte aligned.   dst_row [T,K] int32.
+ * packed  [T*K,H] int8, 16-byte aligned.  scales [T*K] fp32, 4-byte aligned.
+ * H >= 16 with H % 16 == 0.  T == 0 is a no-op.  Asynchronous on `stream`; may
+ * be captured.
+ */
+MOE_API moe_status_t moe_dispatch_int8(const void *tokens, int32_t T, int32_t H, int32_t K,
+                                       const int32_t *dst_row, void *packed, float *scales,
+                                       cudaStream_t stream);
+
+/*
+ * moe_expert_matmul_int8 -- the experts' matrix product on packed int8 rows.
+ *
+ * The page multiplies the packed rows with the experts' weights between
+ * dispatch and combine ("MoE all-to-all over EFA"); here both are 8-bit
+ * integers, with a scale for each row and for each expert's output channel.
+ * For the rows r of expert e, expert_offsets[e] <= r < expert_offsets[e+1]:
+ *
+ *   s = sum over h of x[r,h] * weights[e,n,h]
+ *   out[r,n] = bf16(float(s) * x_scales[r] * w_scales[e,n])      (RN, ties to even)
+ *
+ * s is exact while its partial sums stay below 2^24, else rounded to fp32 as
+ * it is summed.  Rows outside all experts' ranges are not written.  E == 1 with
+ * offsets {0, rows} is the plain matrix product.
+ *
+ * x              [rows,H] int8, 16-byte aligned.   x_scales [rows] fp32.
+ * weights        [E,N,H] int8, 16-byte aligned (a channel's H values together).
+ * w_scales       [E,N] fp32.
+ * expert_offsets [E+1] int32, moe_layout's; non-decreasing.  Offsets outside
+ *                [0, rows] are taken as the nearer end.
+ * out            [rows,N] bf16, 16-byte aligned; must not overlap the inputs.
+ * rows >= 0, 16 <= H <= 65536 with H % 16 == 0, N >= 1, E*N < 2^31,
+ * 1 <= E <= MOE_MAX_EXPERTS.  rows == 0 is a no-op.  Asynchronous on `stream`;
+ * may be captured.
+ */
+MOE_API moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales,
+                                            const void *weights, const float *w_scales,
+                                            const int32_t *expert_offsets, int32_t rows,
+                                            int32_t H, int32_t N, int32_t E, void *out,
+                                            cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,173 @@
+"""moe_expert_matmul_int8 against the integer sums.
+
+While no partial sum can reach 2^24 the kernel's sum is the integer, and the
+result is bf16(fp32(fp32(s * x_scale) * w_scale)): compared bit for bit.  Past
+2^24 each of the sum's steps may round or truncate to 24 bits: its error is
+held to 2^-23 of the magnitudes' sum for every 16 terms, and the output's
+rounding adds 2^-8 of the result."""
+import numpy as np
+import pytest
+import torch
+
+import combine_moe_layout_05_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from combine_moe_layout_05_gb300 import build
+    build.build()
+    moe.load()
+
+
+def codes(shape, seed, lo=-128, hi=128):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(lo, hi, shape, generator=g, device="cuda", dtype=torch.int8)
+
+
+def offsets_of(counts):
+    o = np.zeros(len(counts) + 1, np.int32)
+    o[1:] = np.cumsum(counts)
+    return o
+
+
+def sums(x, w, o):
+    """[rows, N] integer sums in float64 (exact), NaN where no expert owns the row."""
+    s = torch.full((x.shape[0], w.shape[1]), float("nan"), dtype=torch.float64, device="cuda")
+    for e in range(w.shape[0]):
+        a, b = int(o[e]), int(o[e + 1])
+        if b > a:
+            s[a:b] = x[a:b].double() @ w[e].double().t()
+    return s
+
+
+def scales(rows, E, N, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed + 1000)
+    return (torch.rand(rows, generator=g, device="cuda") * 0.1 + 0.001,
+            torch.rand((E, N), generator=g, device="cuda") * 0.02 + 1e-4)
+
+
+def run(x, xs, w, ws, o):
+    out = torch.full((x.shape[0], w.shape[1]), -77.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_matmul_int8(x, xs, w, ws, torch.from_numpy(np.asarray(o, np.int32)).cuda(), out)
+    return out
+
+
+def check(counts, H, N, seed=0, spare=0, lim=None):
+    E, rows = len(counts), int(sum(counts)) + spare
+    o = offsets_of(counts)
+    # magnitudes that keep H products' sum below 2^24
+    lim = lim or max(1, min(127, int((2 ** 24 / H) ** 0.5)))
+    x, w = codes((rows, H), seed, -lim, lim + 1), codes((E, N, H), seed + 1, -lim, lim + 1)
+    xs, ws = scales(rows, E, N, seed)
+    out = run(x, xs, w, ws, o)
+    s = sums(x, w, o)
+    owned = ~torch.isnan(s[:, 0])
+    per_row = torch.zeros((rows, N), device="cuda")
+    for e in range(E):
+        per_row[int(o[e]):int(o[e + 1])] = ws[e]
+    want = (s.float() * xs[:, None] * per_row).to(torch.bfloat16)
+    assert torch.equal(out[owned], want[owned])
+    assert bool((out[~owned] == -77.0).all())            # rows of no expert are left alone
+
+
+@pytest.mark.parametrize("H", [16, 64, 128, 144, 1040])
+@pytest.mark.parametrize("N", [1, 7, 64, 129, 250, 256])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 17, 1], [16, 33, 250, 0]])
+def test_small(counts, H, N):
+    check(counts, H, N, seed=H + N)
+
+
+@pytest.mark.parametrize("counts,H,N", [
+    ([1] * 8 + [0] * 24, 7168, 256),                     # one token's experts
+    ([4] * 256, 1024, 264),                              # a decode batch
+    ([1000, 0, 3, 515, 64, 127, 128, 129], 512, 520),    # rows around every tile edge
+    ([0, 0, 0], 64, 64),                                 # nobody
+    ([4097], 256, 1000),                                 # one expert: the plain product
+    ([0] * 1023 + [5], 32, 16),                          # the most experts
+    ([31, 32, 33, 63, 64, 65, 255, 256, 257, 511, 513], 192, 384),
+])
+def test_groups(counts, H, N):
+    check(counts, H, N, seed=len(counts), spare=5)
+
+
+def test_full_codes_below_the_exact_bound():
+    """All 256 codes, -128 among them: 1008 * 128 * 128 < 2^24."""
+    o = offsets_of([40, 0, 90])
+    x, w = codes((130, 1008), 3), codes((3, 200, 1008), 4)
+    assert int(x.min()) == -128 == int(w.min())
+    xs, ws = scales(130, 3, 200, 5)
+    out = run(x, xs, w, ws, o)
+    per_row = torch.cat([ws[0].expand(40, -1), ws[2].expand(90, -1)])
+    assert torch.equal(out, (sums(x, w, o).float() * xs[:, None] * per_row).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("kind", ["random", "all_127", "up_then_down"])
+def test_sums_past_24_bits(kind):
+    rows, H, N = 70, 7168, 136
+    x, w = codes((rows, H), 1, -127, 128), codes((1, N, H), 2, -127, 128)
+    if kind != "random":
+        x.fill_(127)
+        w.fill_(127)
+    if kind == "up_then_down":
+        w[..., H // 2:] = -126
+    xs, ws = torch.ones(rows, device="cuda"), torch.ones(1, N, device="cuda")
+    out = run(x, xs, w, ws, [0, rows]).double()
+    s = x.double() @ w[0].double().t()
+    big = x.double().abs() @ w[0].double().abs().t()
+    tol = (H / 16) * 2.0 ** -23 * big + 2.0 ** -8 * s.abs()
+    assert bool(((out - s).abs() <= tol).all())
+
+
+def test_scales_pass_through():
+    x, w = codes((20, 64), 1), codes((2, 24, 64), 2)
+    xs, ws = scales(20, 2, 24, 3)
+    xs[4], xs[5] = float("nan"), 0.0
+    ws[1, 3] = float("inf")
+    out = run(x, xs, w, ws, [0, 10, 20]).float()
+    assert bool(torch.isnan(out[4]).all()) and torch.count_nonzero(out[5]) == 0
+    assert not bool(torch.isfinite(out[10:, 3]).any()) and bool(torch.isfinite(out[10:, 4]).all())
+
+
+def test_offsets_outside_the_rows_are_cut():
+    x, w = codes((10, 32), 1), codes((3, 16, 32), 2)
+    xs, ws = scales(10, 3, 16, 3)
+    good = run(x, xs, w, ws, [0, 4, 4, 10])
+    assert torch.equal(run(x, xs, w, ws, [-3, 4, 4, 1000]), good)
+
+
+def test_long_weights_pass_32_bit_offsets():
+    """More than 2^31 weight bytes: the last experts' addresses need 64 bits."""
+    E, N, H = 40, 4096, 14336
+    counts = [0] * E
+    counts[0], counts[E - 1] = 3, 5
+    check(counts, H, N, seed=9)
+
+
+def test_side_stream_graph_and_repeat():
+    x, w = codes((300, 512), 1, -60, 61), codes((4, 512, 512), 2, -60, 61)
+    xs, ws = scales(300, 4, 512, 3)
+    o = torch.tensor([0, 100, 101, 290, 300], dtype=torch.int32, device="cuda")
+    a = run(x, xs, w, ws, o.cpu().numpy())
+    b = torch.zeros_like(a)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        moe.moe_expert_matmul_int8(x, xs, w, ws, o, b)
+    side.synchronize()
+    assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_expert_matmul_int8(x, xs, w, ws, o, b)
+    for n in range(3):
+        b.zero_()
+        if n == 2:                                       # a replay sees new rows and new ranges
+            x.copy_(codes((300, 512), 7, -60, 61))
+            o.copy_(torch.tensor([0, 0, 290, 290, 300], dtype=torch.int32))
+            a = run(x, xs, w, ws, o.cpu().numpy())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, b)
