@@ -87,7 +87,7 @@ def load(path: str | None = None):
             lib.moe_route_backward.restype = ctypes.c_int
             lib.moe_dispatch_int8.argtypes = [P, i32, i32, i32, P, P, P, P]
             lib.moe_dispatch_int8.restype = ctypes.c_int
-            lib.moe_expert_matmul_int8.argtypes = [P, P, P, P, P, i32, i32, i32, i32, P, P]
+            lib.moe_expert_matmul_int8.argtypes = [P, P, P, P, P, i32, i32, i32, i32, P, P, P]
             lib.moe_expert_matmul_int8.restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -365,7 +365,7 @@ def moe_dispatch_int8(tokens, dst_row, packed, scales, stream=None) -> None:
 
 
 def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
-                           stream=None) -> None:
+                           dev_error=None, stream=None) -> None:
     """Packed int8 rows times their experts' int8 weights (see include/moe_layout.h)."""
     rows, H = x.shape
     E, N = weights.shape[0], weights.shape[1]
@@ -375,13 +375,14 @@ def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
     _check("w_scales", w_scales, torch.float32)
     _check("expert_offsets", expert_offsets, torch.int32)
     _check("out", out, torch.bfloat16)
+    _check("dev_error", dev_error, torch.int32)
     if weights.dim() != 3 or weights.shape[2] != H or w_scales.numel() != E * N \
             or x_scales.numel() < rows or expert_offsets.numel() < E + 1 \
             or out.numel() < rows * N or out.shape[-1] != N:
         raise ValueError("moe_expert_matmul_int8: argument sizes disagree")
     st = load().moe_expert_matmul_int8(_ptr(x), _ptr(x_scales), _ptr(weights), _ptr(w_scales),
                                        _ptr(expert_offsets), rows, H, N, E, _ptr(out),
-                                       _stream(stream))
+                                       _ptr(dev_error), _stream(stream))
     _raise("moe_expert_matmul_int8", st)
 
 

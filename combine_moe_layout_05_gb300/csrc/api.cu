@@ -337,7 +337,7 @@ moe_status_t moe_dispatch_int8(const void *tokens, int32_t T, int32_t H, int32_t
 moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales, const void *weights,
                                     const float *w_scales, const int32_t *expert_offsets,
                                     int32_t rows, int32_t H, int32_t N, int32_t E, void *out,
-                                    cudaStream_t stream)
+                                    uint32_t *dev_error, cudaStream_t stream)
 {
     const CallRange range("moe_expert_matmul_int8");
     if (rows < 0 || H < 16 || H > 65536 || H % 16 != 0 || N < 1 || E < 1 || E > MOE_MAX_EXPERTS ||
@@ -346,10 +346,10 @@ moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales, const 
     if (rows == 0) return MOE_OK;
     if (!x || !x_scales || !weights || !w_scales || !expert_offsets || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(weights, 16) || !aligned(out, 16) || !aligned(x_scales, 4) ||
-        !aligned(w_scales, 4) || !aligned(expert_offsets, 4))
+        !aligned(w_scales, 4) || !aligned(expert_offsets, 4) || !aligned(dev_error, 4))
         return MOE_ERR_ALIGNMENT;
     return cuda_status(moe::launch_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets,
-                                                      rows, H, N, E, out, stream));
+                                                      rows, H, N, E, out, dev_error, stream));
 }
 
 }  // extern "C"

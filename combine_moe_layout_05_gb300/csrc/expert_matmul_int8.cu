@@ -4,83 +4,439 @@
 //   out[r, n] = bf16((sum_h x[r, h] * w[e, n, h]) * x_scale[r] * w_scale[e, n])
 //   for the rows r of expert e, [offsets[e], offsets[e+1])
 //
-// A block owns 64 channels of one expert and walks that expert's rows 64 at a
-// time; the sums are int32 and exact.
+// sm_103a has no 8-bit integer matrix instruction of the tcgen05 kind, and an
+// int8 value is exactly a fp16 value: the codes travel as bytes through HBM,
+// L2 and the copies into shared memory, and are widened on the way to the
+// fp16 tensor cores.  A product is below 2^14 and the fp32 accumulator exact
+// up to 2^24, so the sum is the integer's while partial sums stay below that.
+//
+// A tile is 128 channels a CTA (256 a pair of CTAs) by up to NT rows of one
+// expert.  Channels are the instruction's M, so that a tile with few rows
+// still feeds it 128 lanes; the row count is its N and is what the expert has
+// left, rounded up.  Warps of a CTA:
+//
+//   0       copies 128-byte-wide tiles of weights and rows into a ring
+//   1       issues the matrix instructions (the pair's first CTA)
+//   4..7    widen the weights into TMEM (operand A), one channel a thread
+//   8..11   widen the rows into shared memory (operand B), one row a thread
+//   12..15  scale the sums and store them, one channel a thread
+//
+// A pair shares each other's widened rows: every CTA widens half of the tile's
+// rows, which is what keeps shared memory from being the bound (a 128-wide
+// step of a full tile moves 16 KB in, 32 KB through the widening warps and
+// 32 KB into the tensor core, in 1024 cycles of the instruction).
 #include "common.cuh"
 #include "internal.h"
 #include "moe_layout.h"
+#include "tensor.cuh"
+
+#include <mutex>
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64;        // rows and channels of a tile
-constexpr int kStepWords = 16;   // 64 bytes of the contraction a step
-constexpr int kPad = 1;
+constexpr int kStep = 128;                 // bytes of the contraction a ring slot holds
+constexpr int kChannels = 128;             // channels a CTA
+constexpr int kThreads = 512;
+constexpr int kTmemColumns = 512;
 
-__global__ void __launch_bounds__(256)
-expert_matmul_int8_kernel(const uint8_t *__restrict__ x, const float *__restrict__ xs,
-                          const uint8_t *__restrict__ w, const float *__restrict__ ws,
-                          const int32_t *__restrict__ offsets, int rows, int H, int N,
-                          __nv_bfloat16 *__restrict__ out)
+// CG: CTAs a tile.  NT: rows a tile at most.  N8: ring slots of int8 tiles.
+// NC: slots of widened operands.  ND: accumulators.
+template <int CG_, int NT_, int N8_, int NC_, int ND_>
+struct Shape {
+    static constexpr int CG = CG_, NT = NT_, N8 = N8_, NC = NC_, ND = ND_;
+    static constexpr int BR = NT / CG;                 // rows a CTA widens at most
+    static constexpr int BOX = CG == 2 ? 32 : 16;      // rows a copy
+    static constexpr int QUANTUM = CG == 2 ? 32 : 16;  // rows of a tile are a multiple of
+    static constexpr int A8 = kChannels * kStep, B8 = BR * kStep, B16 = BR * kStep * 2;
+    static constexpr int SLOT8 = A8 + B8;
+    static constexpr int ACOL = kStep / 2;             // TMEM columns of a widened slot
+    static_assert(ND * NT + NC * ACOL <= kTmemColumns);
+    static constexpr int BARS = 2 * N8 + 2 * NC + 2 * ND + 1;
+    // ring, widened rows, row scales, barriers, flags, expert table
+    static constexpr int OFF16 = N8 * SLOT8;
+    static constexpr int OFFS = OFF16 + NC * B16;
+    static constexpr int OFFBAR = OFFS + 4 * NT * 4;   // a copy of the row scales for each storing warp
+    static constexpr int OFFTAB = OFFBAR + (BARS * 8 + 15) / 16 * 16 + 32;
+    static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4 + 1024; }
+};
+using Wide = Shape<2, 256, 3, 3, 1>;
+using Narrow = Shape<1, 32, 8, 4, 2>;
+
+// One tile: the rows [row, row + valid) of expert e, `n` of them after
+// rounding up, and the channels from `channel`.
+struct Tile {
+    int e, row, valid, n, channel;
+};
+
+// Experts' first rows and first tiles, in shared memory.
+struct Table {
+    const int *first_row;      // [E + 1]
+    const int *first_tile;     // [E + 1]
+};
+
+template <typename S>
+__device__ __forceinline__ Tile tile_of(const Table &t, int E, int channel_tiles, int i)
 {
-    __shared__ uint32_t sx[kTile][kStepWords + kPad], sw[kTile][kStepWords + kPad];
+    const int tt = i / channel_tiles;
+    int lo = 0, hi = E;                                // first_tile[lo] <= tt < first_tile[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.first_tile[mid] <= tt) lo = mid;
+        else hi = mid;
+    }
+    const int base = t.first_tile[lo], tiles = t.first_tile[lo + 1] - base;
+    const int rows = t.first_row[lo + 1] - t.first_row[lo];
+    // an expert's rows are split evenly; a share is at most NT, so no tile is empty
+    const int share = ceil_div(ceil_div(rows, tiles), S::QUANTUM) * S::QUANTUM;
+    Tile r;
+    r.e = lo;
+    r.row = t.first_row[lo] + (tt - base) * share;
+    r.valid = min(share, rows - (tt - base) * share);
+    r.n = ceil_div(r.valid, S::QUANTUM) * S::QUANTUM;
+    r.channel = (i - tt * channel_tiles) * kChannels * S::CG;
+    return r;
+}
+
+// Four int8 codes to four fp16: with its sign bit flipped a code is b + 128,
+// which below 0x64 is the fp16 1024 + (b + 128); 1152 off is exact.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 c = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), c);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), c);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <typename S>
+__global__ void __launch_bounds__(kThreads, 1)
+expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                          const float *__restrict__ x_scales, const float *__restrict__ w_scales,
+                          const int32_t *__restrict__ offsets, int rows, int H, int N, int E,
+                          __nv_bfloat16 *__restrict__ out, uint32_t *__restrict__ dev_error)
+{
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    uint8_t *const generic = raw + (base - smem_addr(raw));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = S::CG == 2 ? cluster_rank() : 0;
+
+    const uint32_t bar0 = base + S::OFFBAR;
+    auto full8 = [&](int i) { return bar0 + 8 * i; };
+    auto empty8 = [&](int i) { return bar0 + 8 * (S::N8 + i); };
+    auto full16 = [&](int i) { return bar0 + 8 * (2 * S::N8 + i); };
+    auto empty16 = [&](int i) { return bar0 + 8 * (2 * S::N8 + S::NC + i); };
+    auto full_d = [&](int i) { return bar0 + 8 * (2 * S::N8 + 2 * S::NC + i); };
+    auto empty_d = [&](int i) { return bar0 + 8 * (2 * S::N8 + 2 * S::NC + S::ND + i); };
+    const uint32_t drained = bar0 + 8 * (S::BARS - 1);
+    uint32_t *const flags = reinterpret_cast<uint32_t *>(generic + S::OFFBAR + (S::BARS * 8 + 15) / 16 * 16);
+    volatile int *const abort = reinterpret_cast<volatile int *>(flags + 1);
+    int *const first_row = reinterpret_cast<int *>(generic + S::OFFTAB);
+    int *const first_tile = first_row + E + 1;
+
+    if (tid == 0) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_x);
+        uint64_t *b = reinterpret_cast<uint64_t *>(generic + S::OFFBAR);
+        for (int i = 0; i < S::N8; ++i) mbar_init(b + i, 1), mbar_init(b + S::N8 + i, 8);
+        b += 2 * S::N8;
+        for (int i = 0; i < S::NC; ++i) mbar_init(b + i, 8 * S::CG), mbar_init(b + S::NC + i, 1);
+        b += 2 * S::NC;
+        for (int i = 0; i < S::ND; ++i) mbar_init(b + i, 1), mbar_init(b + S::ND + i, 4 * S::CG);
+        mbar_init(b + 2 * S::ND, 1);
+        *abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc<S::CG>(smem_addr(flags), kTmemColumns);
     pdl_wait();
     pdl_trigger();
-    const int e = blockIdx.y, n0 = blockIdx.x * kTile;
-    const int lo = max(0, min(rows, offsets[e])), hi = max(lo, min(rows, offsets[e + 1]));
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 16;    // 16 bytes of a tile row each
-    for (int r0 = lo; r0 < hi; r0 += kTile) {
-        int acc[4][4] = {};
-        for (int h0 = 0; h0 < H; h0 += kStepWords * 4) {
-            uint4 vx = make_uint4(0, 0, 0, 0), vw = vx;
-            if (h0 + lc < H) {
-                if (r0 + lr < hi) vx = *reinterpret_cast<const uint4 *>(x + (size_t)(r0 + lr) * H + h0 + lc);
-                if (n0 + lr < N)
-                    vw = *reinterpret_cast<const uint4 *>(w + ((size_t)e * N + n0 + lr) * H + h0 + lc);
-            }
-            __syncthreads();
-            const int c = lc / 4;
-            sx[lr][c] = vx.x, sx[lr][c + 1] = vx.y, sx[lr][c + 2] = vx.z, sx[lr][c + 3] = vx.w;
-            sw[lr][c] = vw.x, sw[lr][c + 1] = vw.y, sw[lr][c + 2] = vw.z, sw[lr][c + 3] = vw.w;
-            __syncthreads();
+
+    // Tiles an expert, then their running sum: thread t has experts 2t, 2t + 1.
+    {
+        __shared__ int warp_tiles[kThreads / 32];
+        int tiles[2], before = 0;
 #pragma unroll
-            for (int c2 = 0; c2 < kStepWords; ++c2) {
-                int a[4], b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[i] = (int)sx[ty * 4 + i][c2];
-                    b[i] = (int)sw[tx + 16 * i][c2];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(a[i], b[j], acc[i][j]);
+        for (int j = 0; j < 2; ++j) {
+            const int e = 2 * tid + j;
+            tiles[j] = 0;
+            if (e <= E) {
+                const int lo = max(0, min(rows, offsets[e]));
+                first_row[e] = lo;
+                if (e < E) tiles[j] = ceil_div(max(0, min(rows, offsets[e + 1]) - lo), S::NT);
             }
         }
+        int sum = tiles[0] + tiles[1];
+        const int mine = sum;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + ty * 4 + i;
-            if (r >= hi) continue;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFullMask, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) warp_tiles[warp] = sum;
+        tc_fence_before();
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) before += warp_tiles[w];
+        before += sum - mine;
+        if (2 * tid <= E) first_tile[2 * tid] = before;
+        if (2 * tid + 1 <= E) first_tile[2 * tid + 1] = before + tiles[0];
+        if (E == 2 * kThreads && tid == kThreads - 1) {
+            first_row[E] = max(0, min(rows, offsets[E]));
+            first_tile[E] = before + mine;
+        }
+    }
+    if (dev_error && blockIdx.x == 0 && tid == 0) *dev_error = 0;
+    __syncthreads();
+    if constexpr (S::CG == 2) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = flags[0];
+
+    const Table table{first_row, first_tile};
+    const int channel_tiles = ceil_div(N, kChannels * S::CG);
+    const int items = first_tile[E] * channel_tiles;
+    const int steps = ceil_div(H, kStep);
+    const int group = blockIdx.x / S::CG, groups = gridDim.x / S::CG;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            bool ok = true;
+            for (int i = group; i < items && ok; i += groups) {
+                const Tile t = tile_of<S>(table, E, channel_tiles, i);
+                const int half = t.n / S::CG, boxes = ceil_div(half, S::BOX);
+                const int wr = t.e * N + t.channel + (int)rank * kChannels, xr = t.row + (int)rank * half;
+                const uint32_t bytes = S::A8 + boxes * S::BOX * kStep;
+                for (int k = 0; k < steps; ++k, ++issued) {
+                    const int s = issued % S::N8;
+                    ok = mbar_wait_bounded(empty8(s), (issued / S::N8 & 1) ^ 1, abort);
+                    if (!ok) break;
+                    const uint32_t slot = base + s * S::SLOT8;
+                    mbar_arrive_expect(reinterpret_cast<uint64_t *>(generic + S::OFFBAR) + s, bytes);
+                    tile_load_2d(slot, &map_w, k * kStep, wr, full8(s));
+                    for (int b = 0; b < boxes; ++b)
+                        tile_load_2d(slot + S::A8 + b * S::BOX * kStep, &map_x, k * kStep, xr + b * S::BOX, full8(s));
+                }
+            }
+            if (!ok)                                   // the copies in flight land first
+                for (int j = max(0, issued - S::N8); j < issued; ++j) {
+                    const uint64_t deadline = global_ns() + kWaitLimitNs;
+                    while (!mbar_test_cluster(full8(j % S::N8), j / S::N8 & 1))
+                        if (global_ns() > deadline) break;
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int c = 0, d = 0;
+            bool ok = true;
+            for (int i = group; i < items && ok; i += groups, ++d) {
+                const Tile t = tile_of<S>(table, E, channel_tiles, i);
+                const uint32_t idesc = instruction_desc_f16(kChannels * S::CG, t.n);
+                const uint32_t acc = tmem + d % S::ND * S::NT;
+                ok = mbar_wait_bounded(empty_d(d % S::ND), (d / S::ND & 1) ^ 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = 0; k < steps; ++k, ++c) {
+                    const int s = c % S::NC;
+                    ok = mbar_wait_bounded(full16(s), c / S::NC & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = tmem + S::ND * S::NT + s * S::ACOL;
+                    const uint32_t b = base + S::OFF16 + s * S::B16;
+                    const int subs = min(8, (H - k * kStep) >> 4);
+                    for (int j = 0; j < subs; ++j)
+                        mma_f16_ts<S::CG>(acc, a + 8 * j, operand_desc(b + (j >> 2) * S::BR * 128 + (j & 3) * 32),
+                                          idesc, (k | j) != 0);
+                    mma_commit<S::CG>(empty16(s));
+                }
+                if (ok) mma_commit<S::CG>(full_d(d % S::ND));
+            }
+            if (!ok) {                                 // what was issued finishes first
+                mma_commit<S::CG>(drained);
+                const uint64_t deadline = global_ns() + kWaitLimitNs;
+                while (!mbar_test_cluster(drained, 0))
+                    if (global_ns() > deadline) break;
+            }
+        }
+    } else if (warp >= 4 && warp < 12) {
+        const bool weights = warp < 8;
+        const int r = (warp & 3) * 32 + lane;          // channel, or row, of the tile
+        int n = 0;
+        bool ok = true;
+        for (int i = group; i < items && ok; i += groups) {
+            const Tile t = tile_of<S>(table, E, channel_tiles, i);
+            const bool live = weights || r < t.n / S::CG;
+            for (int k = 0; k < steps; ++k, ++n) {
+                const int s = n % S::N8, c = n % S::NC;
+                ok = mbar_wait_bounded(full8(s), n / S::N8 & 1, abort);
+                ok = ok && mbar_wait_bounded(empty16(c), (n / S::NC & 1) ^ 1, abort);
+                ok = __all_sync(kFullMask, ok);
+                if (!ok) break;
+                const uint32_t src = base + s * S::SLOT8 + (weights ? 0 : S::A8) + r * kStep;
+                if (weights) {
+                    tc_fence_after();
+                    const uint32_t dst = tmem + S::ND * S::NT + c * S::ACOL + ((uint32_t)(warp & 3) << 21);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx + 16 * j;
-                if (n < N)
-                    out[(size_t)r * N + n] = __float2bfloat16_rn((float)acc[i][j] * xs[r] * ws[(size_t)e * N + n]);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint4 x = lds128(src + (((4 * h + q) ^ (r & 7)) << 4));
+                            widen4(x.x, v[8 * q], v[8 * q + 1]);
+                            widen4(x.y, v[8 * q + 2], v[8 * q + 3]);
+                            widen4(x.z, v[8 * q + 4], v[8 * q + 5]);
+                            widen4(x.w, v[8 * q + 6], v[8 * q + 7]);
+                        }
+                        tmem_store_x32(dst + 32 * h, v);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                } else if (live) {
+                    const uint32_t dst = base + S::OFF16 + c * S::B16 + r * 128;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint4 x = lds128(src + ((q ^ (r & 7)) << 4));
+                        uint32_t v[8];
+                        widen4(x.x, v[0], v[1]);
+                        widen4(x.y, v[2], v[3]);
+                        widen4(x.z, v[4], v[5]);
+                        widen4(x.w, v[6], v[7]);
+                        const uint32_t at = dst + (q >> 2) * S::BR * 128;
+                        const int g = 2 * q & 7;
+                        sts128(at + ((g ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
+                        sts128(at + (((g + 1) ^ (r & 7)) << 4), v[4], v[5], v[6], v[7]);
+                    }
+                    fence_async_shared();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(reinterpret_cast<uint64_t *>(generic + S::OFFBAR) + S::N8 + s);
+                    mbar_arrive_cluster(S::CG == 2 ? cluster_addr(full16(c), 0) : full16(c));
+                }
+            }
+        }
+        for (int j = max(0, n - S::NC); j < n && ok; ++j)     // the last slots' arrivals are in
+            ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(j % S::NC), j / S::NC & 1, abort));
+    } else if (warp >= 12) {
+        const int quarter = warp & 3;
+        float *const row_scale = reinterpret_cast<float *>(generic + S::OFFS) + quarter * S::NT;
+        int d = 0;
+        bool ok = true;
+        for (int i = group; i < items && ok; i += groups, ++d) {
+            const Tile t = tile_of<S>(table, E, channel_tiles, i);
+            const int ch = t.channel + (int)rank * kChannels + quarter * 32 + lane;
+            __syncwarp();                              // the last tile's scales have been read
+            for (int j = lane; j < t.valid; j += 32) row_scale[j] = x_scales[t.row + j];
+            const float ws = ch < N ? w_scales[(size_t)t.e * N + ch] : 0.0f;
+            ok = __all_sync(kFullMask, mbar_wait_bounded(full_d(d % S::ND), d / S::ND & 1, abort));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + d % S::ND * S::NT + ((uint32_t)quarter << 21);
+            __nv_bfloat16 *o = out + (size_t)t.row * N + ch;
+            for (int c0 = 0; c0 < t.n; c0 += 16) {
+                uint32_t v[16];
+                tmem_load_x16(acc + c0, v);
+                tmem_wait_ld();
+                if (c0 + 16 >= t.n) {                  // all read: the accumulator is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(S::CG == 2 ? cluster_addr(empty_d(d % S::ND), 0) : empty_d(d % S::ND));
+                }
+                if (ch < N) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c0 + j < t.valid)
+                            o[(size_t)(c0 + j) * N] =
+                                __float2bfloat16_rn(__uint_as_float(v[j]) * row_scale[c0 + j] * ws);
+                }
             }
         }
     }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (S::CG == 2) cluster_sync_all();      // the peer is done with this CTA's memory
+    tc_fence_after();
+    if (tid == 0 && *abort && dev_error) atomicOr(dev_error, MOE_DEV_ERR_TIMEOUT);
+    if (warp == 1) tmem_free<S::CG>(tmem, kTmemColumns);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static std::once_flag once;
+    static EncodeFn fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+    });
+    return fn;
+}
+
+// [rows, H] bytes, in boxes of kStep bytes by `box` rows, 128-byte swizzle.
+bool byte_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t H, uint32_t box)
+{
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {H, rows}, strides[1] = {H};
+    const cuuint32_t boxes[2] = {kStep, box}, ones[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, boxes, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename S>
+cudaError_t run(const void *x, const float *x_scales, const void *w, const float *w_scales,
+                const int32_t *offsets, int rows, int H, int N, int E, void *out, uint32_t *dev_error,
+                cudaStream_t stream)
+{
+    CUtensorMap map_w, map_x;
+    if (!byte_map(&map_w, w, (uint64_t)E * N, H, kChannels) || !byte_map(&map_x, x, rows, H, S::BOX))
+        return cudaErrorInvalidValue;
+    const size_t smem = S::bytes(E);
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(&expert_matmul_int8_kernel<S>), smem);
+    if (e != cudaSuccess) return e;
+    int sms = 0;
+    e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    // tiles there can be at most: every expert's last one may be short
+    const int64_t most = ((int64_t)(rows < E ? rows : E) + rows / S::NT) * ceil_div(N, kChannels * S::CG);
+    const int64_t groups = most < sms / S::CG ? most : sms / S::CG;
+    return launch_pdl_clusters(expert_matmul_int8_kernel<S>, dim3((unsigned)groups * S::CG), dim3(kThreads), smem,
+                               stream, S::CG, map_w, map_x, x_scales, w_scales, offsets, rows, H, N, E,
+                               static_cast<__nv_bfloat16 *>(out), dev_error);
 }
 
 }  // namespace
 
 cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, const void *w,
                                       const float *w_scales, const int32_t *offsets, int rows,
-                                      int H, int N, int E, void *out, cudaStream_t stream)
+                                      int H, int N, int E, void *out, uint32_t *dev_error,
+                                      cudaStream_t stream)
 {
-    return launch_pdl(expert_matmul_int8_kernel, dim3(ceil_div(N, kTile), E), dim3(256), 0, stream,
-                      static_cast<const uint8_t *>(x), x_scales, static_cast<const uint8_t *>(w),
-                      w_scales, offsets, rows, H, N, static_cast<__nv_bfloat16 *>(out));
+    if (rows <= (int64_t)Narrow::NT * E)
+        return run<Narrow>(x, x_scales, w, w_scales, offsets, rows, H, N, E, out, dev_error, stream);
+    return run<Wide>(x, x_scales, w, w_scales, offsets, rows, H, N, E, out, dev_error, stream);
 }
 
 }  // namespace moe

@@ -107,7 +107,8 @@ cudaError_t launch_dispatch_int8(const void *tokens, int T, int H, int K, const 
 // Packed int8 rows times their experts' int8 weights.
 cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, const void *w,
                                       const float *w_scales, const int32_t *offsets, int rows,
-                                      int H, int N, int E, void *out, cudaStream_t stream);
+                                      int H, int N, int E, void *out, uint32_t *dev_error,
+                                      cudaStream_t stream);
 
 // Router logits (bf16 != 0: bf16, else fp32) to ids, weights, counts and the
 // balance loss; and the gradient back to the logits.

@@ -63,9 +63,10 @@ typedef enum moe_status {
 #define MOE_DEV_ERR_DUPLICATE    2u  /* some token lists one expert twice       */
 #define MOE_DEV_ERR_REGION_OVERFLOW 4u /* moe_dispatch_send: a rank's rows exceed
                                           its private + bulk capacity          */
-#define MOE_DEV_ERR_TIMEOUT 8u       /* moe_layout_dispatch: a bounded wait
-                                        between its blocks expired; outputs
-                                        unspecified                            */
+#define MOE_DEV_ERR_TIMEOUT 8u       /* moe_layout_dispatch,
+                                        moe_expert_matmul_int8: a bounded wait
+                                        between its blocks or warps expired;
+                                        outputs unspecified                    */
 
 /* Limits of this implementation. */
 #define MOE_MAX_EXPERTS 1024
@@ -473,6 +474,9 @@ MOE_API moe_status_t moe_dispatch_int8(const void *tokens, int32_t T, int32_t H,
  * expert_offsets [E+1] int32, moe_layout's; non-decreasing.  Offsets outside
  *                [0, rows] are taken as the nearer end.
  * out            [rows,N] bf16, 16-byte aligned; must not overlap the inputs.
+ * dev_error      [1] uint32 or NULL.  Overwritten with 0, or with
+ *                MOE_DEV_ERR_TIMEOUT when a bounded wait (2 s) between the
+ *                kernel's warps expired; the outputs are then unspecified.
  * rows >= 0, 16 <= H <= 65536 with H % 16 == 0, N >= 1, E*N < 2^31,
  * 1 <= E <= MOE_MAX_EXPERTS.  rows == 0 is a no-op.  Asynchronous on `stream`;
  * may be captured.
@@ -481,7 +485,7 @@ MOE_API moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales
                                             const void *weights, const float *w_scales,
                                             const int32_t *expert_offsets, int32_t rows,
                                             int32_t H, int32_t N, int32_t E, void *out,
-                                            cudaStream_t stream);
+                                            uint32_t *dev_error, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -63,13 +63,13 @@ def test_dispatch_int8(lib):
 
 
 def test_expert_matmul_int8(lib):
-    def f(x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, off=FAKE, rows=4, H=32, N=8, E=2, out=FAKE):
-        return lib.moe_expert_matmul_int8(P(x), P(xs), P(w), P(ws), P(off), rows, H, N, E, P(out), None)
+    def f(x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, off=FAKE, rows=4, H=32, N=8, E=2, out=FAKE, err=0):
+        return lib.moe_expert_matmul_int8(P(x), P(xs), P(w), P(ws), P(off), rows, H, N, E, P(out), P(err), None)
     for kw in (dict(rows=-1), dict(H=0), dict(H=24), dict(H=65552), dict(N=0), dict(E=0), dict(E=1025),
                dict(E=1024, N=2 ** 21), dict(x=0), dict(xs=0), dict(w=0), dict(ws=0), dict(off=0), dict(out=0)):
         assert f(**kw) == INVALID, kw
     for kw in (dict(x=FAKE + 8), dict(w=FAKE + 8), dict(out=FAKE + 8), dict(xs=FAKE + 2), dict(ws=FAKE + 2),
-               dict(off=FAKE + 2)):
+               dict(off=FAKE + 2), dict(err=FAKE + 2)):
         assert f(**kw) == ALIGNMENT, kw
     assert f(rows=0, x=0, out=0) == 0
 
