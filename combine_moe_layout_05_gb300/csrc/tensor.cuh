@@ -13,7 +13,9 @@
 
 namespace moe {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;    // 2 s; the longest tile takes well under 1 ms
+// About 2 s; the longest tile takes well under 1 ms.  Counted in clock cycles:
+// a read of the nanosecond timer takes long enough to delay every wait.
+constexpr long long kWaitLimitCycles = 4000000000ll;
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -36,9 +38,24 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
     return r;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
+// One arrival on a barrier of the pair.  What it announces is read by the
+// tensor cores alone, each from its own CTA's memory, and was handed to them
+// by fence.proxy.async or tcgen05.wait before: no cluster-wide release of
+// ordinary writes is asked for (it costs a memory barrier, 0.4 us, each time).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
+}
+
+// True in one lane of a converged warp.  Instructions of the copy engine and
+// the tensor core are issued behind it, in code the whole warp runs: behind a
+// test of the lane number the compiler loops over the lanes to make their
+// operands uniform, 150 cycles an instruction.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
@@ -56,13 +73,21 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort)
 {
     if (mbar_test_cluster(bar, parity)) return true;
-    const uint64_t deadline = global_ns() + kWaitLimitNs;
+    const long long start = clock64();
     while (!mbar_test_cluster(bar, parity))
-        if (*abort || global_ns() > deadline) {
+        if (*abort || clock64() - start > kWaitLimitCycles) {
             *abort = 1;
             return false;
         }
     return true;
+}
+
+// The same for a copy or a matrix instruction in flight while giving up.
+__device__ __forceinline__ void mbar_drain_bounded(uint32_t bar, uint32_t parity)
+{
+    const long long start = clock64();
+    while (!mbar_test_cluster(bar, parity))
+        if (clock64() - start > kWaitLimitCycles) return;
 }
 
 // Tile of a two-dimensional tensor at (column c, row r) to shared memory;
