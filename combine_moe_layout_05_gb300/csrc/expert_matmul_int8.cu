@@ -36,32 +36,37 @@ namespace moe {
 namespace {
 
 constexpr int kStep = 128;                 // bytes of the contraction a ring slot holds
-constexpr int kHalf = 64;                  // of them in a slot of widened operands
 constexpr int kChannels = 128;             // channels a CTA
 constexpr int kTmemColumns = 512;
 
-// CG: CTAs a tile.  NT: rows a tile at most.  N8: ring slots of int8 tiles.
-// NC: slots of widened operands.  ND: accumulators.  GA, GB: groups of warps
-// that widen the weights and the rows; a group takes every GA-th (GB-th) step,
-// since one step's latency (barrier, loads, stores and their wait) is several
-// times its issue slots.
-template <int CG_, int NT_, int N8_, int NC_, int ND_, int GA_, int GB_>
+// CG: CTAs a tile.  NT: rows a tile at most.  PARTS: parts a tile's rows are
+// summed in, each with its accumulator.  KS: the contraction's share of a slot
+// of widened operands.  N8, NC: slots of int8 tiles and of widened operands.
+// GA, GB: groups of warps that widen the weights and the rows; a group takes
+// every GA-th (GB-th) step, since one step's latency (barrier, loads, stores
+// and their wait) is several times its issue slots.
+template <int CG_, int NT_, int PARTS_, int KS_, int N8_, int NC_, int GA_, int GB_>
 struct Shape {
-    static constexpr int CG = CG_, NT = NT_, N8 = N8_, NC = NC_, ND = ND_, GA = GA_, GB = GB_;
+    static constexpr int CG = CG_, NT = NT_, PARTS = PARTS_, KS = KS_, N8 = N8_, NC = NC_, GA = GA_, GB = GB_;
     static constexpr int BR = NT / CG;                 // rows a CTA widens at most
-    static constexpr int BOX = CG == 2 ? 32 : 16;      // rows a copy
-    static constexpr int QUANTUM = CG == 2 ? 32 : 16;  // rows of a tile are a multiple of
-    static constexpr int A8 = kChannels * kStep, B8 = BR * kStep, B16 = BR * kHalf * 2;
+    static constexpr int QUANTUM = 16 * CG;            // rows of a part are a multiple of
+    static constexpr int PER = kStep / KS;             // widened slots a step
+    static constexpr int BURST = 3;                    // slots a part runs ahead at a tile's ends
+    static constexpr int A8 = kChannels * kStep, B8 = BR * kStep, B16 = BR * KS * 2;
     static constexpr int SLOT8 = A8 + B8;
-    static constexpr int ACOL = kHalf / 2;             // TMEM columns of a widened slot
-    static_assert(ND * NT + NC * ACOL <= kTmemColumns);
+    static constexpr int UNIT = NT / PARTS;            // TMEM columns of an accumulator
+    static constexpr int ACOL0 = 2 * UNIT, ACOL = KS / 2;   // and of the widened weights
+    static_assert(ACOL0 + NC * ACOL <= kTmemColumns && BURST <= NC);
+    // a barrier's parity tells a use from the one before, not from the one
+    // before that: no group may be two rounds of its ring ahead
+    static_assert(GA * PER <= NC && GB * PER <= NC && GA <= N8 && GB <= N8);
     // warps: 0 copies, 1 issues, then those that widen and those that store;
     // the TMEM lanes a warp reaches are those of its number modulo 4
     static constexpr int WB = BR / 32;                 // warps of a group that widens rows
     static constexpr int A0 = 4, E0 = A0 + 4 * GA, B0 = WB * GB <= 2 ? 2 : E0 + 4;
     static constexpr int WARPS = B0 == 2 ? E0 + 4 : B0 + WB * GB;
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int BARS = 2 * N8 + 2 * NC + 2 * ND + 1;
+    static constexpr int BARS = 2 * N8 + 2 * NC + 4 + 1;
     // ring, widened rows, 16 x 32 outputs and the row scales of each storing
     // warp, barriers, flags, expert table
     static constexpr int OFF16 = N8 * SLOT8;
@@ -71,13 +76,23 @@ struct Shape {
     static constexpr int OFFTAB = OFFBAR + (BARS * 8 + 15) / 16 * 16 + 32;
     static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4 + 1024; }
 };
-using Wide = Shape<2, 256, 3, 6, 1, 2, 2>;
-using Narrow = Shape<1, 32, 8, 12, 2, 4, 2>;
+using Wide = Shape<2, 256, 2, 64, 3, 6, 2, 2>;
+using Narrow = Shape<1, 32, 1, 128, 8, 6, 4, 2>;
 
-// One tile: the rows [row, row + valid) of expert e, `n` of them after
-// rounding up, and the channels from `channel`.
+// Copies of rows come in these heights; a tile takes the one that covers its
+// share (an instruction of the copy engine costs its issuing thread 150 to 200
+// cycles, so a copy too high is cheaper than several that fit).
+constexpr int kBoxes = 4, kLeastBox = 16;
+struct RowMaps {
+    CUtensorMap box[kBoxes];    // 16, 32, 64, 128 rows
+};
+
+// One tile: the rows [row, row + valid) of expert e and the channels from
+// `channel`.  CTA r of a pair widens the rows from r * share; the share is
+// split into parts (a sum with an accumulator of its own), and n[p] counts the
+// pair's rows in part p: part 0 is the first n[0] / CG of each share.
 struct Tile {
-    int e, row, valid, n, channel;
+    int e, row, valid, n[2], channel;
 };
 
 // Experts' first rows and first tiles, in shared memory.
@@ -101,10 +116,12 @@ __device__ __forceinline__ Tile tile_of(const Table &t, int E, int channel_tiles
     // an expert's rows are split evenly; a share is at most NT, so no tile is empty
     const int share = ceil_div(ceil_div(rows, tiles), S::QUANTUM) * S::QUANTUM;
     Tile r;
-    r.e = lo;
-    r.row = t.first_row[lo] + (tt - base) * share;
-    r.valid = min(share, rows - (tt - base) * share);
-    r.n = ceil_div(r.valid, S::QUANTUM) * S::QUANTUM;
+    r.e = uniform(lo);
+    r.row = uniform(t.first_row[lo] + (tt - base) * share);
+    r.valid = uniform(min(share, rows - (tt - base) * share));
+    const int n = ceil_div(r.valid, S::QUANTUM) * S::QUANTUM;
+    r.n[0] = S::PARTS == 1 ? n : ceil_div(n, 2 * S::QUANTUM) * S::QUANTUM;
+    r.n[1] = n - r.n[0];
     r.channel = (i - tt * channel_tiles) * kChannels * S::CG;
     return r;
 }
@@ -122,6 +139,14 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
     hi = *reinterpret_cast<const uint32_t *>(&y);
 }
 
+__device__ __forceinline__ void widen16(const uint4 &x, uint32_t *v)
+{
+    widen4(x.x, v[0], v[1]);
+    widen4(x.y, v[2], v[3]);
+    widen4(x.z, v[4], v[5]);
+    widen4(x.w, v[6], v[7]);
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t addr)
 {
     uint4 v;
@@ -134,9 +159,26 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// The instructions of one slot of widened operands: B's 64-wide blocks follow
+// each other, 128 bytes a row.
+template <typename S, int COUNT>
+__device__ __forceinline__ void mma_slot(uint32_t acc, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+#pragma unroll
+    for (int q = 0; q < COUNT; ++q)
+        mma_f16_ts<S::CG>(acc, a + 8 * q, b + (q >> 2) * (S::BR * 128 / 16) + (q & 3) * 2, idesc, accumulate || q > 0);
+}
+
+template <typename S>
+__device__ __forceinline__ void mma_slot_n(uint32_t acc, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, int count)
+{
+    for (int q = 0; q < count; ++q)
+        mma_f16_ts<S::CG>(acc, a + 8 * q, b + (q >> 2) * (S::BR * 128 / 16) + (q & 3) * 2, idesc, accumulate || q > 0);
+}
+
 template <typename S>
 __global__ void __launch_bounds__(S::THREADS, 1)
-expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x,
                           const float *__restrict__ x_scales, const float *__restrict__ w_scales,
                           const int32_t *__restrict__ offsets, int rows, int H, int N, int E,
                           __nv_bfloat16 *__restrict__ out, uint32_t *__restrict__ dev_error)
@@ -144,8 +186,8 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
     uint8_t *const generic = raw + (base - smem_addr(raw));
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = S::CG == 2 ? cluster_rank() : 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
+    const uint32_t rank = S::CG == 2 ? uniform(cluster_rank()) : 0;
 
     const uint32_t bar0 = base + S::OFFBAR;
     auto full8 = [&](int i) { return bar0 + 8 * i; };
@@ -153,7 +195,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     auto full16 = [&](int i) { return bar0 + 8 * (2 * S::N8 + i); };
     auto empty16 = [&](int i) { return bar0 + 8 * (2 * S::N8 + S::NC + i); };
     auto full_d = [&](int i) { return bar0 + 8 * (2 * S::N8 + 2 * S::NC + i); };
-    auto empty_d = [&](int i) { return bar0 + 8 * (2 * S::N8 + 2 * S::NC + S::ND + i); };
+    auto empty_d = [&](int i) { return bar0 + 8 * (2 * S::N8 + 2 * S::NC + 2 + i); };
     const uint32_t drained = bar0 + 8 * (S::BARS - 1);
     uint32_t *const flags = reinterpret_cast<uint32_t *>(generic + S::OFFBAR + (S::BARS * 8 + 15) / 16 * 16);
     volatile int *const abort = reinterpret_cast<volatile int *>(flags + 1);
@@ -162,14 +204,14 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
 
     if (tid == 0) {
         prefetch_map(&map_w);
-        prefetch_map(&map_x);
+        for (int m = 0; kLeastBox << m <= S::BR; ++m) prefetch_map(&map_x.box[m]);
         uint64_t *b = reinterpret_cast<uint64_t *>(generic + S::OFFBAR);
         for (int i = 0; i < S::N8; ++i) mbar_init(b + i, 1), mbar_init(b + S::N8 + i, 4 + S::WB);
         b += 2 * S::N8;
         for (int i = 0; i < S::NC; ++i) mbar_init(b + i, (4 + S::WB) * S::CG), mbar_init(b + S::NC + i, 1);
         b += 2 * S::NC;
-        for (int i = 0; i < S::ND; ++i) mbar_init(b + i, 1), mbar_init(b + S::ND + i, 4 * S::CG);
-        mbar_init(b + 2 * S::ND, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(b + i, 1), mbar_init(b + 2 + i, 4 * S::CG);
+        mbar_init(b + 4, 1);
         *abort = 0;
         fence_barrier_init();
     }
@@ -211,12 +253,12 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     __syncthreads();
     if constexpr (S::CG == 2) cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem = flags[0];
+    const uint32_t tmem = uniform(flags[0]);
 
     const Table table{first_row, first_tile};
     const int channel_tiles = ceil_div(N, kChannels * S::CG);
-    const int items = first_tile[E] * channel_tiles;
-    const int steps = ceil_div(H, kStep), halves = 2 * steps;
+    const int items = uniform(first_tile[E]) * channel_tiles;
+    const int steps = ceil_div(H, kStep), slots = ceil_div(H, S::KS);
     uint64_t *const bars = reinterpret_cast<uint64_t *>(generic + S::OFFBAR);
     const int group = blockIdx.x / S::CG, groups = gridDim.x / S::CG;
 
@@ -225,9 +267,11 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         bool ok = true;
         for (int i = group; i < items && ok; i += groups) {
             const Tile t = tile_of<S>(table, E, channel_tiles, i);
-            const int half = t.n / S::CG, boxes = ceil_div(half, S::BOX);
-            const int wr = t.e * N + t.channel + (int)rank * kChannels, xr = t.row + (int)rank * half;
-            const uint32_t bytes = S::A8 + boxes * S::BOX * kStep;
+            const int share = (t.n[0] + t.n[1]) / S::CG;
+            int m = 0;
+            while (kLeastBox << m < share) ++m;
+            const int wr = t.e * N + t.channel + (int)rank * kChannels, xr = t.row + (int)rank * share;
+            const uint32_t bytes = S::A8 + (kLeastBox << m) * kStep;
             for (int k = 0; k < steps; ++k, ++issued) {
                 const int s = issued % S::N8;
                 ok = __all_sync(kFullMask, mbar_wait_bounded(empty8(s), (issued / S::N8 & 1) ^ 1, abort));
@@ -236,8 +280,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 if (elect_one()) {
                     mbar_arrive_expect(bars + s, bytes);
                     tile_load_2d(slot, &map_w, k * kStep, wr, full8(s));
-                    for (int b = 0; b < boxes; ++b)
-                        tile_load_2d(slot + S::A8 + b * S::BOX * kStep, &map_x, k * kStep, xr + b * S::BOX, full8(s));
+                    tile_load_2d(slot + S::A8, &map_x.box[m], k * kStep, xr, full8(s));
                 }
                 __syncwarp();
             }
@@ -247,32 +290,109 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 mbar_drain_bounded(full8(j % S::N8), j / S::N8 & 1);
     } else if (warp == 1) {
         if (rank == 0) {
-            int c = 0, d = 0;
+            int c = 0, cphase = 0;                     // slot of widened operands
+            int u = 0;                                 // accumulators used so far
+            const uint64_t b_first = operand_desc(base + S::OFF16);
+            constexpr int kFull = S::KS / 16;          // instructions a slot
+            const int last = (H - (slots - 1) * S::KS) >> 4;     // and in the last one
             bool ok = true;
-            for (int i = group; i < items && ok; i += groups, ++d) {
-                const Tile t = tile_of<S>(table, E, channel_tiles, i);
-                const uint32_t idesc = instruction_desc_f16(kChannels * S::CG, t.n);
-                const uint32_t acc = tmem + d % S::ND * S::NT;
-                ok = __all_sync(kFullMask, mbar_wait_bounded(empty_d(d % S::ND), (d / S::ND & 1) ^ 1, abort));
-                if (!ok) break;
+            auto wait_free = [&](int v) {
+                ok = __all_sync(kFullMask, mbar_wait_bounded(empty_d(v & 1), (v >> 1 & 1) ^ 1, abort));
                 tc_fence_after();
-                for (int k = 0; k < halves; ++k, ++c) {
-                    const int s = c % S::NC;
-                    ok = __all_sync(kFullMask, mbar_wait_bounded(full16(s), c / S::NC & 1, abort));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t a = tmem + S::ND * S::NT + s * S::ACOL;
-                    const uint64_t b = operand_desc(base + S::OFF16 + s * S::B16);
-                    const int subs = min(4, (H - k * kHalf) >> 4);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (j < subs) mma_f16_ts<S::CG>(acc, a + 8 * j, b + 2 * j, idesc, (k | j) != 0);
-                        mma_commit<S::CG>(empty16(s));
-                        if (k == halves - 1) mma_commit<S::CG>(full_d(d % S::ND));
+            };
+            auto wait_slot = [&](int s, int phase) {
+                ok = __all_sync(kFullMask, mbar_wait_bounded(full16(s), phase, abort));
+                tc_fence_after();
+            };
+            for (int i = group; i < items && ok; i += groups) {
+                const Tile t = tile_of<S>(table, E, channel_tiles, i);
+                const uint32_t idesc0 = instruction_desc_f16(kChannels * S::CG, t.n[0]);
+                const uint32_t idesc1 = instruction_desc_f16(kChannels * S::CG, t.n[1]);
+                const uint32_t b_part = t.n[0] / S::CG * (128 / 16);       // part 1's rows follow part 0's
+                const uint32_t acc0 = tmem + (u & 1) * S::UNIT, acc1 = tmem + (u + 1 & 1) * S::UNIT;
+                // slots by turns between the parts, but the first and the last
+                // few one part after the other: one accumulator is drained
+                // while the other is summed
+                if constexpr (S::PARTS == 2) {
+                    const bool two = t.n[1] > 0;
+                    int k = 0;
+                    bool ready = false;                // the next slot has been seen full
+                    while (k < slots && ok) {
+                        const int left = slots - k;
+                        int s = c, ph = cphase;
+                        if (k > 0 && left > S::BURST) {
+                            if (!ready) wait_slot(s, ph);
+                            if (!ok) break;
+                            const uint32_t a = tmem + S::ACOL0 + s * S::ACOL;
+                            const uint64_t b0 = b_first + s * (S::B16 / 16), b1 = b0 + b_part;
+                            const uint32_t empty = empty16(s);
+                            if (elect_one()) mma_slot<S, kFull>(acc0, a, b0, idesc0, true);
+                            __syncwarp();
+                            // the next slot is asked for while instructions wait in the queue
+                            if (++s == S::NC) s = 0, ph ^= 1;
+                            ready = __all_sync(kFullMask, mbar_test_cluster(full16(s), ph));
+                            if (elect_one()) {
+                                if (two) mma_slot<S, kFull>(acc1, a, b1, idesc1, true);
+                                mma_commit<S::CG>(empty);
+                            }
+                            __syncwarp();
+                            if (ready) tc_fence_after();
+                            ++k;
+                        } else {
+                            const int count = min(S::BURST, left);
+                            if (k == 0) wait_free(u);
+                            for (int j = 0; j < count && ok; ++j) {
+                                if (!ready) wait_slot(s, ph);
+                                ready = false;
+                                if (!ok) break;
+                                if (elect_one()) {
+                                    mma_slot_n<S>(acc0, tmem + S::ACOL0 + s * S::ACOL, b_first + s * (S::B16 / 16), idesc0,
+                                                  k + j > 0, k + j == slots - 1 ? last : kFull);
+                                    if (k + j == slots - 1) mma_commit<S::CG>(full_d(u & 1));
+                                }
+                                __syncwarp();
+                                if (++s == S::NC) s = 0, ph ^= 1;
+                            }
+                            if (k == 0 && ok) wait_free(u + 1);
+                            if (!ok) break;
+                            s = c, ph = cphase;
+                            for (int j = 0; j < count; ++j) {
+                                if (elect_one()) {
+                                    if (two)
+                                        mma_slot_n<S>(acc1, tmem + S::ACOL0 + s * S::ACOL, b_first + s * (S::B16 / 16) + b_part,
+                                                      idesc1, k + j > 0, k + j == slots - 1 ? last : kFull);
+                                    mma_commit<S::CG>(empty16(s));
+                                    if (k + j == slots - 1) mma_commit<S::CG>(full_d(u + 1 & 1));
+                                }
+                                __syncwarp();
+                                if (++s == S::NC) s = 0, ph ^= 1;
+                            }
+                            k += count;
+                        }
+                        c = s, cphase = ph;
                     }
-                    __syncwarp();
+                } else {
+                    wait_free(u);
+                    for (int k = 0; k < slots && ok; ++k) {
+                        wait_slot(c, cphase);
+                        if (!ok) break;
+                        const uint32_t a = tmem + S::ACOL0 + c * S::ACOL;
+                        const uint64_t b = b_first + c * (S::B16 / 16);
+                        if (elect_one()) {
+                            if (k < slots - 1) {
+                                mma_slot<S, kFull>(acc0, a, b, idesc0, k > 0);
+                                mma_commit<S::CG>(empty16(c));
+                            } else {
+                                mma_slot_n<S>(acc0, a, b, idesc0, k > 0, last);
+                                mma_commit<S::CG>(empty16(c));
+                                mma_commit<S::CG>(full_d(u & 1));
+                            }
+                        }
+                        __syncwarp();
+                        if (++c == S::NC) c = 0, cphase ^= 1;
+                    }
                 }
+                u += S::PARTS;
             }
             if (!ok) {                                 // what was issued finishes first
                 if (elect_one()) mma_commit<S::CG>(drained);
@@ -283,141 +403,166 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     } else if (warp >= S::E0 && warp < S::E0 + 4) {
         const int quarter = warp & 3;
         float *const row_scale = reinterpret_cast<float *>(generic + S::OFFS) + quarter * S::NT;
-        __nv_bfloat16 *const turned = reinterpret_cast<__nv_bfloat16 *>(generic + S::OFFTURN) + quarter * 512;
-        const bool vector_out = N % 8 == 0;
-        int d = 0;
+        const uint32_t turned = base + S::OFFTURN + quarter * 1024;
+        int u = 0;
         bool ok = true;
-        for (int i = group; i < items && ok; i += groups, ++d) {
+        for (int i = group; i < items && ok; i += groups) {
             const Tile t = tile_of<S>(table, E, channel_tiles, i);
-            const int ch = t.channel + (int)rank * kChannels + quarter * 32 + lane;
+            const int ch0 = t.channel + (int)rank * kChannels + quarter * 32;
             __syncwarp();                              // the last tile's scales have been read
-            float xs[S::NT / 32];
+            float xs[S::NT / 32], ws[4];
 #pragma unroll
             for (int j = 0; j < S::NT / 32; ++j)
                 xs[j] = j * 32 + lane < t.valid ? x_scales[t.row + j * 32 + lane] : 0.0f;
-            const float ws = ch < N ? w_scales[(size_t)t.e * N + ch] : 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int ch = ch0 + 8 * q + (lane >> 2);
+                ws[q] = ch < N ? w_scales[(size_t)t.e * N + ch] : 0.0f;
+            }
 #pragma unroll
             for (int j = 0; j < S::NT / 32; ++j) row_scale[j * 32 + lane] = xs[j];
             __syncwarp();
-            ok = __all_sync(kFullMask, mbar_wait_bounded(full_d(d % S::ND), d / S::ND & 1, abort));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + d % S::ND * S::NT + ((uint32_t)quarter << 21);
-            const int ch0 = ch - lane;
-            const bool vectors = vector_out && ch0 + 32 <= N;
-            for (int c0 = 0; c0 < t.n; c0 += 16) {
-                uint32_t v[16];
-                tmem_load_x16(acc + c0, v);
-                tmem_wait_ld();
-                if (c0 + 16 >= t.n) {                  // all read: the accumulator is free
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_pair(S::CG == 2 ? cluster_addr(empty_d(d % S::ND), 0) : empty_d(d % S::ND));
+            const bool vectors = N % 8 == 0 && ch0 + 32 <= N;
+            for (int p = 0; p < S::PARTS && ok; ++p, ++u) {
+                const int d = u & 1, n = t.n[p], mine = n / S::CG;
+                ok = __all_sync(kFullMask, mbar_wait_bounded(full_d(d), u >> 1 & 1, abort));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + d * S::UNIT + ((uint32_t)quarter << 21);
+                uint32_t next[16];
+                if (n > 0) {
+                    tmem_load_16x16(acc, next);
+                    tmem_load_16x16(acc + (16u << 16), next + 8);
                 }
-                __nv_bfloat16 y[16];
+                for (int c0 = 0; c0 < n; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    y[j] = __float2bfloat16_rn(__uint_as_float(v[j]) * row_scale[c0 + j] * ws);
-                if (vectors) {
-                    // 16 rows of 32 channels turned in shared memory, then 16 bytes a lane
+                    for (int j = 0; j < 16; ++j) v[j] = next[j];
+                    if (c0 + 16 < n) {
+                        tmem_load_16x16(acc + c0 + 16, next);
+                        tmem_load_16x16(acc + c0 + 16 + (16u << 16), next + 8);
+                    }
+                    // the tile's row of column c0: the second CTA's share follows the first's
+                    const int second = S::CG == 2 && c0 >= mine;
+                    const int r0 = c0 + (p ? t.n[0] / S::CG : 0) + (second ? (t.n[0] + t.n[1]) / 2 - mine : 0);
+                    const float *rs = row_scale + r0 + 2 * (lane & 3);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) turned[j * 32 + lane] = y[j];
-                    __syncwarp();
+                    for (int b = 0; b < 2; ++b) {      // 8 rows, of 4 times 8 channels
+                        const float2 r = *reinterpret_cast<const float2 *>(rs + 8 * b);
+                        uint32_t y[4];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int r = c0 + j * 8 + (lane >> 2);
-                        const uint4 q = reinterpret_cast<const uint4 *>(turned)[j * 32 + lane];
-                        if (r < t.valid) st_v4(out + (size_t)(t.row + r) * N + ch0 + (lane & 3) * 8, q);
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t *w = v + 8 * (q >> 1) + 4 * b + 2 * (q & 1);
+                            y[q] = pack_bf16x2_rn(__uint_as_float(w[0]) * r.x * ws[q], __uint_as_float(w[1]) * r.y * ws[q]);
+                        }
+                        const int j = lane & 7;        // a row of 64 bytes, its 16-byte pieces permuted
+                        store_turned_x4(turned + (8 * b + j) * 64 + (((lane >> 3) ^ (j >> 1 & 3)) << 4),
+                                        y[0], y[1], y[2], y[3]);
                     }
                     __syncwarp();
-                } else if (ch < N) {
-                    __nv_bfloat16 *o = out + (size_t)(t.row + c0) * N + ch;
+                    if (vectors) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c0 + j < t.valid) o[(size_t)j * N] = y[j];
+                        for (int j = 0; j < 2; ++j) {
+                            const int r = 8 * j + (lane >> 2);
+                            const uint4 q = lds128(turned + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4));
+                            if (r0 + r < t.valid)
+                                st_v4(out + (size_t)(t.row + r0 + r) * N + ch0 + (lane & 3) * 8, q);
+                        }
+                    } else if (ch0 + lane < N) {
+                        const int rows_left = min(16, t.valid - r0);
+                        for (int r = 0; r < rows_left; ++r) {
+                            uint16_t q;
+                            asm volatile("ld.shared.u16 %0, [%1];"
+                                         : "=h"(q) : "r"(turned + r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4) + (lane & 7) * 2));
+                            out[(size_t)(t.row + r0 + r) * N + ch0 + lane] = __ushort_as_bfloat16(q);
+                        }
+                    }
+                    __syncwarp();
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(S::CG == 2 ? cluster_addr(empty_d(d), 0) : empty_d(d));
             }
         }
     } else if (warp >= S::A0 && warp < S::E0) {
         // weights: group `g` has every GA-th step, and in it a thread one channel
         const int g = (warp - S::A0) >> 2, r = (warp & 3) * 32 + lane;
-        int n = 0;
+        int n = 0, m0 = 0;                             // steps, and widened slots, so far
         bool ok = true;
-        for (int i = group; i < items && ok; i += groups)
+        for (int i = group; i < items && ok; i += groups, m0 += slots)
             for (int k = 0; k < steps && ok; ++k, ++n) {
                 if (n % S::GA != g) continue;
                 const int s = n % S::N8;
                 ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, abort));
                 const uint32_t src = base + s * S::SLOT8 + r * kStep;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int m = 2 * n + h, c = m % S::NC;
-                    if (!ok) break;
+#pragma unroll 1
+                for (int h = 0; h < S::PER; ++h) {
+                    if (!ok || k * S::PER + h >= slots) break;
+                    const int m = m0 + k * S::PER + h, c = m % S::NC;
                     uint32_t v[32];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 x = lds128(src + (((4 * h + q) ^ (r & 7)) << 4));
-                        widen4(x.x, v[8 * q], v[8 * q + 1]);
-                        widen4(x.y, v[8 * q + 2], v[8 * q + 3]);
-                        widen4(x.z, v[8 * q + 4], v[8 * q + 5]);
-                        widen4(x.w, v[8 * q + 6], v[8 * q + 7]);
+                    for (int w = 0; w < S::KS / 64; ++w) {
+                        const int q0 = 4 * (h + w);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            widen16(lds128(src + (((q0 + q) ^ (r & 7)) << 4)), v + 8 * q);
+                        if (w == 0) {
+                            ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, abort));
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        tmem_store_x32(tmem + S::ACOL0 + c * S::ACOL + 32 * w + ((uint32_t)(warp & 3) << 21), v);
                     }
-                    ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, abort));
                     if (!ok) break;
-                    tc_fence_after();
-                    tmem_store_x32(tmem + S::ND * S::NT + c * S::ACOL + ((uint32_t)(warp & 3) << 21), v);
-                    if (h == 1 && lane == 0) mbar_arrive(bars + S::N8 + s);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_pair(S::CG == 2 ? cluster_addr(full16(c), 0) : full16(c));
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + S::N8 + s);
             }
-        for (int j = max(0, 2 * n - S::NC); j < 2 * n && ok; ++j)     // the last slots' arrivals are in
+        for (int j = max(0, m0 - S::NC); j < m0 && ok; ++j)           // the last slots' arrivals are in
             ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(j % S::NC), j / S::NC & 1, abort));
     } else if (warp >= S::B0 && warp < S::B0 + S::WB * S::GB) {
         // rows: group `g` has every GB-th step, and in it a thread one row
         const int g = (warp - S::B0) / S::WB, r = (warp - S::B0) % S::WB * 32 + lane;
-        int n = 0;
+        int n = 0, m0 = 0;
         bool ok = true;
-        for (int i = group; i < items && ok; i += groups) {
-            const bool live = r < tile_of<S>(table, E, channel_tiles, i).n / S::CG;
+        for (int i = group; i < items && ok; i += groups, m0 += slots) {
+            const Tile t = tile_of<S>(table, E, channel_tiles, i);
+            const bool live = r < (t.n[0] + t.n[1]) / S::CG;
             for (int k = 0; k < steps && ok; ++k, ++n) {
                 if (n % S::GB != g) continue;
                 const int s = n % S::N8;
                 ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, abort));
                 const uint32_t src = base + s * S::SLOT8 + S::A8 + r * kStep;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int m = 2 * n + h, c = m % S::NC;
-                    if (!ok) break;
-                    uint32_t v[32];
-                    if (live) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint4 x = lds128(src + (((4 * h + q) ^ (r & 7)) << 4));
-                            widen4(x.x, v[8 * q], v[8 * q + 1]);
-                            widen4(x.y, v[8 * q + 2], v[8 * q + 3]);
-                            widen4(x.z, v[8 * q + 4], v[8 * q + 5]);
-                            widen4(x.w, v[8 * q + 6], v[8 * q + 7]);
-                        }
-                    }
+#pragma unroll 1
+                for (int h = 0; h < S::PER; ++h) {
+                    if (!ok || k * S::PER + h >= slots) break;
+                    const int m = m0 + k * S::PER + h, c = m % S::NC;
                     ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, abort));
                     if (!ok) break;
                     if (live) {
-                        const uint32_t dst = base + S::OFF16 + c * S::B16 + r * 128;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            sts128(dst + ((q ^ (r & 7)) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        for (int w = 0; w < S::KS / 64; ++w) {
+                            const uint32_t dst = base + S::OFF16 + c * S::B16 + w * S::BR * 128 + r * 128;
+                            uint32_t v[32];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                widen16(lds128(src + (((4 * (h + w) + q) ^ (r & 7)) << 4)), v + 8 * q);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                sts128(dst + ((q ^ (r & 7)) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        }
                         fence_async_shared();
                     }
                     __syncwarp();
-                    if (lane == 0) {
-                        if (h == 1) mbar_arrive(bars + S::N8 + s);
-                        mbar_arrive_pair(S::CG == 2 ? cluster_addr(full16(c), 0) : full16(c));
-                    }
+                    if (lane == 0) mbar_arrive_pair(S::CG == 2 ? cluster_addr(full16(c), 0) : full16(c));
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + S::N8 + s);
             }
         }
     }
@@ -465,9 +610,11 @@ cudaError_t run(const void *x, const float *x_scales, const void *w, const float
                 const int32_t *offsets, int rows, int H, int N, int E, void *out, uint32_t *dev_error,
                 cudaStream_t stream)
 {
-    CUtensorMap map_w, map_x;
-    if (!byte_map(&map_w, w, (uint64_t)E * N, H, kChannels) || !byte_map(&map_x, x, rows, H, S::BOX))
-        return cudaErrorInvalidValue;
+    CUtensorMap map_w;
+    RowMaps map_x;
+    if (!byte_map(&map_w, w, (uint64_t)E * N, H, kChannels)) return cudaErrorInvalidValue;
+    for (int m = 0; m < kBoxes; ++m)
+        if (!byte_map(&map_x.box[m], x, rows, H, min(kLeastBox << m, S::BR))) return cudaErrorInvalidValue;
     const size_t smem = S::bytes(E);
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(&expert_matmul_int8_kernel<S>), smem);
     if (e != cudaSuccess) return e;

@@ -47,6 +47,14 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
 }
 
+// Lane 0's value, which the compiler then knows to be the warp's: branches on
+// it do not diverge, and operands made from it stay in uniform registers.
+template <typename T>
+__device__ __forceinline__ T uniform(T v)
+{
+    return __shfl_sync(kFullMask, v, 0);
+}
+
 // True in one lane of a converged warp.  Instructions of the copy engine and
 // the tensor core are issued behind it, in code the whole warp runs: behind a
 // test of the lane number the compiler loops over the lanes to make their
@@ -69,10 +77,11 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
 }
 
 // Waits for the phase of `bar` with the given parity; false, and *abort set,
-// when the limit passed or another thread of the block gave up.
-__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort)
+// when the limit passed or another thread of the block gave up.  Once, not
+// inline: the kernel's warps run different loops, which together have to stay
+// in the instruction cache.
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort)
 {
-    if (mbar_test_cluster(bar, parity)) return true;
     const long long start = clock64();
     while (!mbar_test_cluster(bar, parity))
         if (*abort || clock64() - start > kWaitLimitCycles) {
@@ -80,6 +89,11 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
             return false;
         }
     return true;
+}
+
+__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort)
+{
+    return mbar_test_cluster(bar, parity) || mbar_wait_long(bar, parity, abort);
 }
 
 // The same for a copy or a matrix instruction in flight while giving up.
@@ -187,14 +201,23 @@ __device__ __forceinline__ void tmem_store_x32(uint32_t addr, const uint32_t (&v
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_load_x16(uint32_t addr, uint32_t (&v)[16])
+// 16 columns of 16 TMEM lanes, spread over the warp as the matrix
+// instructions' 8 x 8 blocks: thread t has columns 2(t%4), 2(t%4) + 1 (and 8
+// more) of lanes t/4 (words 0, 1; 4, 5) and t/4 + 8 (words 2, 3; 6, 7).
+__device__ __forceinline__ void tmem_load_16x16(uint32_t addr, uint32_t *v)
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
-                   "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
-                   "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                   "=r"(v[6]), "=r"(v[7])
                  : "r"(addr) : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit words, turned: block q's word (i, j), held by
+// thread 4i + j/2, goes to word i of the row that thread 8q + j points at.
+__device__ __forceinline__ void store_turned_x4(uint32_t row, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 :: "r"(row), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 }  // namespace moe
