@@ -76,7 +76,7 @@ struct Shape {
     static constexpr int OFFTAB = OFFBAR + (BARS * 8 + 15) / 16 * 16 + 32;
     static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4 + 1024; }
 };
-using Wide = Shape<2, 256, 2, 64, 3, 6, 2, 2>;
+using Wide = Shape<2, 256, 2, 64, 4, 4, 2, 2>;
 using Narrow = Shape<1, 32, 1, 128, 8, 6, 4, 2>;
 
 // Copies of rows come in these heights; a tile takes the one that covers its
@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x,
                           const float *__restrict__ x_scales, const float *__restrict__ w_scales,
                           const int32_t *__restrict__ offsets, int rows, int H, int N, int E,
-                          __nv_bfloat16 *__restrict__ out, uint32_t *__restrict__ dev_error)
+                          int least, int most, int second, __nv_bfloat16 *__restrict__ out,
+                          uint32_t *__restrict__ dev_error)
 {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
@@ -216,10 +217,13 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc<S::CG>(smem_addr(flags), kTmemColumns);
-    pdl_wait();
+    // The second of two launches starts as the first one's blocks leave: its
+    // inputs were there when the first one started, and it writes other rows.
+    if (!second) pdl_wait();
     pdl_trigger();
 
-    // Tiles an expert, then their running sum: thread t has experts 2t, 2t + 1.
+    // Tiles an expert (none where its rows are not in [least, most]), then
+    // their running sum: thread t has experts 2t, 2t + 1.
     {
         static_assert(2 * S::THREADS > MOE_MAX_EXPERTS);
         __shared__ int warp_tiles[S::WARPS];
@@ -231,7 +235,10 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
             if (e <= E) {
                 const int lo = max(0, min(rows, offsets[e]));
                 first_row[e] = lo;
-                if (e < E) tiles[j] = ceil_div(max(0, min(rows, offsets[e + 1]) - lo), S::NT);
+                if (e < E) {
+                    const int m = max(0, min(rows, offsets[e + 1])) - lo;
+                    if (m >= least && m <= most) tiles[j] = ceil_div(m, S::NT);
+                }
             }
         }
         int sum = tiles[0] + tiles[1];
@@ -249,7 +256,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         if (2 * tid <= E) first_tile[2 * tid] = before;
         if (2 * tid + 1 <= E) first_tile[2 * tid + 1] = before + tiles[0];
     }
-    if (dev_error && blockIdx.x == 0 && tid == 0) *dev_error = 0;
+    if (dev_error && !second && blockIdx.x == 0 && tid == 0) *dev_error = 0;
     __syncthreads();
     if constexpr (S::CG == 2) cluster_sync_all();
     tc_fence_after();
@@ -573,6 +580,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     tc_fence_after();
     if (tid == 0 && *abort && dev_error) atomicOr(dev_error, MOE_DEV_ERR_TIMEOUT);
     if (warp == 1) tmem_free<S::CG>(tmem, kTmemColumns);
+    if (second) pdl_wait();                            // what follows waits for both launches
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -607,8 +615,8 @@ bool byte_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t H, uint32
 
 template <typename S>
 cudaError_t run(const void *x, const float *x_scales, const void *w, const float *w_scales,
-                const int32_t *offsets, int rows, int H, int N, int E, void *out, uint32_t *dev_error,
-                cudaStream_t stream)
+                const int32_t *offsets, int rows, int H, int N, int E, int least, int most, int second,
+                void *out, uint32_t *dev_error, cudaStream_t stream)
 {
     CUtensorMap map_w;
     RowMaps map_x;
@@ -622,11 +630,11 @@ cudaError_t run(const void *x, const float *x_scales, const void *w, const float
     e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
     // tiles there can be at most: every expert's last one may be short
-    const int64_t most = ((int64_t)(rows < E ? rows : E) + rows / S::NT) * ceil_div(N, kChannels * S::CG);
-    const int64_t groups = most < sms / S::CG ? most : sms / S::CG;
+    const int64_t tiles = ((int64_t)(rows < E ? rows : E) + rows / S::NT) * ceil_div(N, kChannels * S::CG);
+    const int64_t groups = tiles < sms / S::CG ? tiles : sms / S::CG;
     return launch_pdl_clusters(expert_matmul_int8_kernel<S>, dim3((unsigned)groups * S::CG), dim3(S::THREADS), smem,
                                stream, S::CG, map_w, map_x, x_scales, w_scales, offsets, rows, H, N, E,
-                               static_cast<__nv_bfloat16 *>(out), dev_error);
+                               least, most, second, static_cast<__nv_bfloat16 *>(out), dev_error);
 }
 
 }  // namespace
@@ -636,9 +644,17 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
                                       int H, int N, int E, void *out, uint32_t *dev_error,
                                       cudaStream_t stream)
 {
-    if (rows <= (int64_t)Narrow::NT * E)
-        return run<Narrow>(x, x_scales, w, w_scales, offsets, rows, H, N, E, out, dev_error, stream);
-    return run<Wide>(x, x_scales, w, w_scales, offsets, rows, H, N, E, out, dev_error, stream);
+    auto go = [&](auto shape, int least, int most, int second) {
+        return run<decltype(shape)>(x, x_scales, w, w_scales, offsets, rows, H, N, E, least, most, second, out,
+                                    dev_error, stream);
+    };
+#ifndef LIGHT
+#define LIGHT 32
+#endif
+    if (rows <= 16 * E) return go(Narrow{}, 1, INT32_MAX, 0);
+    if (rows >= 512 * E) return go(Wide{}, 1, INT32_MAX, 0);
+    const cudaError_t e = go(Wide{}, LIGHT + 1, INT32_MAX, 0);
+    return e != cudaSuccess ? e : go(Narrow{}, 1, LIGHT, 1);
 }
 
 }  // namespace moe
