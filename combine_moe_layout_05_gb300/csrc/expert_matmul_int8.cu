@@ -31,6 +31,7 @@
 #include "tensor.cuh"
 
 #include <mutex>
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -62,9 +63,9 @@ struct Shape {
     static_assert(GA * PER <= NC && GB * PER <= NC && GA <= N8 && GB <= N8);
     // warps: 0 copies, 1 issues, then those that widen and those that store;
     // the TMEM lanes a warp reaches are those of its number modulo 4
-    static constexpr int WB = BR / 32;                 // warps of a group that widens rows
-    static constexpr int A0 = 4, E0 = A0 + 4 * GA, B0 = WB * GB <= 2 ? 2 : E0 + 4;
-    static constexpr int WARPS = B0 == 2 ? E0 + 4 : B0 + WB * GB;
+    static constexpr int WB = 4;                       // warps of a group that widens rows
+    static_assert(BR * (KS / 64) <= 8 * WB * 4);
+    static constexpr int A0 = 4, E0 = A0 + 4 * GA, B0 = E0 + 4, WARPS = B0 + WB * GB;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int BARS = 2 * N8 + 2 * NC + 4 + 1;
     // ring, widened rows, 16 x 32 outputs and the row scales of each storing
@@ -533,38 +534,52 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         for (int j = max(0, m0 - S::NC); j < m0 && ok; ++j)           // the last slots' arrivals are in
             ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(j % S::NC), j / S::NC & 1, abort));
     } else if (warp >= S::B0 && warp < S::B0 + S::WB * S::GB) {
-        // rows: group `g` has every GB-th step, and in it a thread one row
-        const int g = (warp - S::B0) / S::WB, r = (warp - S::B0) % S::WB * 32 + lane;
+        // rows: group `g` has every GB-th step; a warp takes 8 rows by 64 bytes at
+        // a time, a thread 16 bytes, so that few rows are spread over all warps
+        const int g = (warp - S::B0) / S::WB, w = (warp - S::B0) % S::WB;
         int n = 0, m0 = 0;
         bool ok = true;
         for (int i = group; i < items && ok; i += groups, m0 += slots) {
             const Tile t = tile_of<S>(table, E, channel_tiles, i);
-            const bool live = r < (t.n[0] + t.n[1]) / S::CG;
+            const int blocks = (t.n[0] + t.n[1]) / (8 * S::CG);
             for (int k = 0; k < steps && ok; ++k, ++n) {
                 if (n % S::GB != g) continue;
                 const int s = n % S::N8;
                 ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, abort));
-                const uint32_t src = base + s * S::SLOT8 + S::A8 + r * kStep;
+                const uint32_t src = base + s * S::SLOT8 + S::A8;
 #pragma unroll 1
                 for (int h = 0; h < S::PER; ++h) {
                     if (!ok || k * S::PER + h >= slots) break;
                     const int m = m0 + k * S::PER + h, c = m % S::NC;
-                    ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, abort));
-                    if (!ok) break;
-                    if (live) {
+                    // pieces a warp, rounded up to 1, 2 or 4: the rows past the tile's
+                    // are in the slot's memory, and no instruction reads them
+                    auto widen = [&](auto pieces) {
+                        constexpr int U = decltype(pieces)::value;
+                        uint32_t v[U][8];
 #pragma unroll
-                        for (int w = 0; w < S::KS / 64; ++w) {
-                            const uint32_t dst = base + S::OFF16 + c * S::B16 + w * S::BR * 128 + r * 128;
-                            uint32_t v[32];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                widen16(lds128(src + (((4 * (h + w) + q) ^ (r & 7)) << 4)), v + 8 * q);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                sts128(dst + ((q ^ (r & 7)) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        for (int j = 0; j < U; ++j) {
+                            const int at = w + S::WB * j, half = S::KS > 64 && at >= blocks, block = at - half * blocks;
+                            const int r = 8 * block + (lane & 7), q = 4 * (h + half) + (lane >> 3);
+                            widen16(lds128(src + r * kStep + ((q ^ (r & 7)) << 4)), v[j]);
                         }
-                        fence_async_shared();
-                    }
+                        ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, abort));
+                        if (!ok) return;
+#pragma unroll
+                        for (int j = 0; j < U; ++j) {
+                            const int at = w + S::WB * j, half = S::KS > 64 && at >= blocks, block = at - half * blocks;
+                            const int r = 8 * block + (lane & 7), q = 2 * (lane >> 3);
+                            const uint32_t row = base + S::OFF16 + c * S::B16 + half * S::BR * 128 + r * 128;
+                            sts128(row + ((q ^ (r & 7)) << 4), v[j][0], v[j][1], v[j][2], v[j][3]);
+                            sts128(row + (((q + 1) ^ (r & 7)) << 4), v[j][4], v[j][5], v[j][6], v[j][7]);
+                        }
+                    };
+                    constexpr int kMost = S::BR / 8 * (S::KS / 64) / S::WB;
+                    const int pieces = ceil_div(blocks * (S::KS / 64), S::WB);
+                    if (pieces == 1) widen(std::integral_constant<int, 1>());
+                    else if (kMost <= 2 || pieces == 2) widen(std::integral_constant<int, 2>());
+                    else widen(std::integral_constant<int, kMost <= 2 ? 2 : 4>());
+                    if (!ok) break;
+                    fence_async_shared();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_pair(S::CG == 2 ? cluster_addr(full16(c), 0) : full16(c));
                 }
@@ -648,13 +663,17 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
         return run<decltype(shape)>(x, x_scales, w, w_scales, offsets, rows, H, N, E, least, most, second, out,
                                     dev_error, stream);
     };
-#ifndef LIGHT
-#define LIGHT 32
-#endif
+    // Few rows an expert: the weights' bytes are the work, and the narrow form
+    // moves them at 6.8 TB/s where the wide one reaches 5.2 (decode, 256 experts
+    // of 2048 x 7168: 547 and 723 us).  Many: the wide form alone (1.4 ms at 1024
+    // rows an expert, against 1.6 PFLOP/s).  Between them each expert goes by
+    // its own rows, in two launches (16384 skewed rows over 384 experts: 1257 us;
+    // wide alone 1450, narrow alone 2560).
+    constexpr int kLight = Narrow::NT;
     if (rows <= 16 * E) return go(Narrow{}, 1, INT32_MAX, 0);
     if (rows >= 512 * E) return go(Wide{}, 1, INT32_MAX, 0);
-    const cudaError_t e = go(Wide{}, LIGHT + 1, INT32_MAX, 0);
-    return e != cudaSuccess ? e : go(Narrow{}, 1, LIGHT, 1);
+    const cudaError_t e = go(Wide{}, kLight + 1, INT32_MAX, 0);
+    return e != cudaSuccess ? e : go(Narrow{}, 1, kLight, 1);
 }
 
 }  // namespace moe
