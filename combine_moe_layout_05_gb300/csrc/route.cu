@@ -7,26 +7,41 @@
 //
 //   loss = coef * E * sum_e (c_e / (K n)) * (sum_t p_te / n)
 //
-// One warp owns a token: lane l holds logits l, l + 32, ... in registers, so
-// the row is read once; its maximum, sum and the K picks are warp reductions.
-// Sums of p over tokens stay in registers (fp32) while a warp walks its
-// tokens, then are added warp by warp and block by block in a fixed order,
-// so a call's results do not depend on timing.
+// One warp owns a token: lane l holds the NV logits from l * NV, so the row is
+// read once, in 16-byte loads where its alignment allows, and a lower lane
+// always has lower expert numbers: among equal logits the lowest lane, and in
+// it the lowest place, is the lowest expert.  The maximum and each pick are
+// one warp-wide maximum; the lane that has it strikes it out and finds its
+// next.  Sums of p over tokens stay in registers (fp32) while a warp walks its
+// tokens, are added warp by warp in a block, block by block in a cluster
+// (distributed shared memory) and cluster by cluster at the end, always in
+// that order, so a call's results do not depend on timing.
 #include "common.cuh"
 #include "internal.h"
 #include "moe_layout.h"
+#include "tensor.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kRouteThreads = 256;
-constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteMaxBlocks = 304;      // two a multiprocessor
+constexpr int kRouteWarps = 16;
+constexpr int kRouteThreads = kRouteWarps * 32;
+constexpr int kRouteCluster = 4;                    // blocks that add their sums up together
+constexpr int kRouteClusters = 76;                  // at most: two blocks a multiprocessor
+constexpr int kSingleCluster = 8;                   // blocks of the form that needs one launch
+constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float load_logit(const float *p) { return __ldg(p); }
-__device__ __forceinline__ float load_logit(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_logit(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_logit(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float from_float(float v, float) { return v; }
+__device__ __forceinline__ __nv_bfloat16 from_float(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -35,67 +50,89 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// Largest of the warp's values that are numbers (NaN if none is).
 __device__ __forceinline__ float warp_max(float v)
 {
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// Lane's NV logits of a row of E (-inf past E).  VEC: rows start on 16 bytes
+// and E is a multiple of a 16-byte load's values.
+template <int NV, bool VEC, typename L>
+__device__ __forceinline__ void load_row(const L *row, int E, int lane, float (&x)[NV])
+{
+    constexpr int W = 16 / sizeof(L);
+    if constexpr (VEC) {
+        static_assert(NV % W == 0);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
+        for (int j = 0; j < NV; j += W) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            const bool in = lane * NV + j < E;
+            if (in) v = ld_stream_v4(row + lane * NV + j);
+            const L *q = reinterpret_cast<const L *>(&v);
+#pragma unroll
+            for (int i = 0; i < W; ++i) x[j + i] = in ? to_float(q[i]) : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x[j] = lane * NV + j < E ? to_float(row[lane * NV + j]) : -INFINITY;
+    }
+}
+
+template <int NV>
+__device__ __forceinline__ float lane_max(const float (&x)[NV])
+{
+    float m = x[0];
+#pragma unroll
+    for (int j = 1; j < NV; ++j) m = fmaxf(m, x[j]);
+    return m;
+}
+
+// The probability of logit x before the division by the row's sum: exactly 0
+// at -inf, and NaN for NaN or +inf, which then reaches the whole row.
+__device__ __forceinline__ float weight_of(float x, float m)
+{
+    return x == -INFINITY ? 0.0f : exp2_approx((x - m) * kLog2e);
+}
+
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
 
-// An unsigned key in the order of the floats (-0 and +0 alike); 0 for -inf
-// and NaN, which are never chosen.
-__device__ __forceinline__ uint32_t order_key(float x)
+// The call's last sums, thread e for expert e: p and c are expert e's totals.
+__device__ __forceinline__ float loss_term(float p, int c, int n, int K)
 {
-    if (!(x > -INFINITY)) return 0u;
-    const uint32_t u = __float_as_uint(x + 0.0f);
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+    const float fn = (float)max(n, 1);
+    return ((float)c / ((float)K * fn)) * (p / fn);
 }
 
-// A token's logits in registers (-inf past E and in a masked row), with the
-// maximum over its open experts (0 when there is none).
-template <int NV, typename L>
-__device__ __forceinline__ float load_row(const L *row, int E, bool masked, int lane, float (&x)[NV])
-{
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = j * 32 + lane;
-        x[j] = e < E && !masked ? load_logit(row + e) : -INFINITY;
-        m = fmaxf(m, x[j]);
-    }
-    m = warp_max(m);
-    return m == -INFINITY ? 0.0f : m;
-}
+struct RouteOut {
+    int32_t *counts, *routed;
+    float *loss;
+    float coef;
+};
 
-// x becomes exp(x - m), exactly 0 at -inf; returns the row's sum.  A NaN or
-// +inf logit makes the sum NaN, and with it every probability of the row.
-template <int NV>
-__device__ __forceinline__ float exp_row(float (&x)[NV], float m)
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        x[j] = x[j] == -INFINITY ? 0.0f : expf(x[j] - m);
-        s += x[j];
-    }
-    return warp_sum(s);
-}
-
-template <int NV, typename L>
-__global__ void __launch_bounds__(kRouteThreads)
+// SINGLE: the grid is one cluster, which writes the results; otherwise every
+// cluster writes its totals to part[cluster]: E probability sums, E counts and
+// the routed tokens.
+template <int NV, bool VEC, bool SINGLE, typename L>
+__global__ void __launch_bounds__(kRouteThreads, NV > 16 ? 1 : 2)
 route_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm,
              const uint8_t *__restrict__ mask, int32_t *__restrict__ ids,
-             float *__restrict__ weights, float *__restrict__ part_p, int32_t *__restrict__ part_c,
-             int32_t *__restrict__ part_n)
+             float *__restrict__ weights, uint32_t *__restrict__ part, RouteOut o)
 {
     extern __shared__ float sm[];
-    float *sum_p = sm;                                   // [E]
-    int32_t *cnt = reinterpret_cast<int32_t *>(sm + E);  // [E], then the routed tokens
+    float *const sums = sm;                              // [kRouteWarps][E], then [E]
+    int32_t *const cnt = reinterpret_cast<int32_t *>(sm + (size_t)kRouteWarps * E);     // [E] and the routed tokens
+    __shared__ int32_t picks[kRouteWarps][MOE_MAX_TOPK];
+    __shared__ float terms[kSingleCluster];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e <= E; e += kRouteThreads) {
-        if (e < E) sum_p[e] = 0.0f;
-        cnt[e] = 0;
-    }
+    for (int e = threadIdx.x; e <= E; e += kRouteThreads) cnt[e] = 0;
     pdl_wait();
     pdl_trigger();
     __syncthreads();
@@ -106,108 +143,170 @@ route_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm,
 
     for (int t = blockIdx.x * kRouteWarps + warp; t < T; t += gridDim.x * kRouteWarps) {
         float x[NV];
-        uint32_t key[NV];
-        const bool masked = mask && !mask[t];
-        const float m = load_row<NV>(logits + (size_t)t * E, E, masked, lane, x);
+        load_row<NV, VEC>(logits + (size_t)t * E, E, lane, x);
+        if (mask && !mask[t]) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) key[j] = order_key(x[j]);
-        const float s = exp_row<NV>(x, m);
-        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+            for (int j = 0; j < NV; ++j) x[j] = -INFINITY;
+        }
+        float best = lane_max<NV>(x);
+        float m = warp_max(best);
+        if (!(m > -INFINITY)) m = 0.0f;
+        float p[NV], s = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            x[j] *= inv;
-            acc[j] += x[j];
+            p[j] = weight_of(x[j], m);
+            s += p[j];
         }
-        int my_id = -1;
-        float my_w = 0.0f, total = 0.0f;
-        for (int k = 0; k < K; ++k) {
-            uint32_t best = 0;
-            int bj = 0;
-            float bp = 0.0f;
+        s = warp_sum(s);
+        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (key[j] > best) {
-                    best = key[j];
-                    bj = j;
-                    bp = x[j];
-                }
-            const uint32_t top = __reduce_max_sync(kFullMask, best);
-            if (top == 0) break;                         // no open expert is left
-            const int e = __reduce_min_sync(kFullMask, best == top ? bj * 32 + lane : INT32_MAX);
-            const float p = __shfl_sync(kFullMask, bp, e & 31);
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (j * 32 + lane == e) key[j] = 0;
-            if (lane == k) {
-                my_id = e;
-                my_w = p;
-            }
-            total += p;
-        }
-        if (renorm && total != 0.0f) my_w /= total;
-        if (lane < K) {
-            ids[(size_t)t * K + lane] = my_id;
-            weights[(size_t)t * K + lane] = my_w;
-            if (my_id >= 0) atomicAdd(&cnt[my_id], 1);
-            if (lane == 0 && my_id >= 0) atomicAdd(&cnt[E], 1);
-        }
-    }
-    for (int w = 0; w < kRouteWarps; ++w) {              // warp by warp: a fixed order
-        if (warp == w) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (j * 32 + lane < E) sum_p[j * 32 + lane] += acc[j];
-        }
-        __syncthreads();
-    }
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
-        part_p[(size_t)blockIdx.x * E + e] = sum_p[e];
-        part_c[(size_t)blockIdx.x * E + e] = cnt[e];
-    }
-    if (threadIdx.x == 0) part_n[blockIdx.x] = cnt[E];
-}
+        for (int j = 0; j < NV; ++j) acc[j] += p[j] * inv;
 
-// The blocks' parts in block order: counts, routed tokens and the loss.
-__global__ void __launch_bounds__(1024)
-route_finish_kernel(const float *__restrict__ part_p, const int32_t *__restrict__ part_c,
-                    const int32_t *__restrict__ part_n, int blocks, int E, int K, float coef,
-                    int32_t *__restrict__ counts, int32_t *__restrict__ routed,
-                    float *__restrict__ loss)
-{
-    __shared__ float red[32];
-    pdl_wait();
-    pdl_trigger();
-    const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+        float mine = -INFINITY;                          // pick number `lane`
+        for (int k = 0; k < K; ++k) {
+            const float top = warp_max(best);
+            if (!(top > -INFINITY)) break;               // no open expert is left
+            if (lane == k) mine = top;
+            const unsigned tied = __ballot_sync(kFullMask, best == top);
+            if (lane == __ffs(tied) - 1) {
+                int at = 0;
+                bool struck = false;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const bool here = !struck && x[j] == top;
+                    if (here) {
+                        at = j;
+                        x[j] = -INFINITY;
+                    }
+                    struck |= here;
+                }
+                picks[warp][k] = lane * NV + at;
+                best = lane_max<NV>(x);
+            }
+        }
+        __syncwarp();
+        const bool taken = lane < K && mine > -INFINITY;
+        float w = taken ? weight_of(mine, m) * inv : 0.0f;
+        if (renorm) {
+            const float total = warp_sum(w);
+            if (total != 0.0f) w /= total;
+        }
+        const int id = taken ? picks[warp][lane] : -1;
+        if (lane < K) {
+            ids[(size_t)t * K + lane] = id;
+            weights[(size_t)t * K + lane] = w;
+        }
+        if (taken) {
+            atomicAdd(&cnt[id], 1);
+            if (lane == 0) atomicAdd(&cnt[E], 1);
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (lane * NV + j < E) sums[warp * E + lane * NV + j] = acc[j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+        float v = sums[e];
+#pragma unroll
+        for (int w = 1; w < kRouteWarps; ++w) v += sums[w * E + e];
+        sums[e] = v;
+    }
+    const uint32_t rank = cluster_rank();
+    const int blocks = SINGLE ? (int)gridDim.x : kRouteCluster;
+    cluster_sync_all();
+
+    // experts rank, rank + blocks, ... are this block's to add up
+    const uint32_t sums_at = smem_addr(sums), cnt_at = smem_addr(cnt);
     int n = 0;
-    for (int b = 0; b < blocks; ++b) n += part_n[b];
-    float v = 0.0f;
-    if (e < E) {
-        float p = 0.0f;
+    for (int b = 0; b < blocks; ++b) n += (int)ld_cluster(cluster_addr(cnt_at + 4 * E, b));
+    float term = 0.0f;
+    for (int e = threadIdx.x * blocks + rank; e < E; e += kRouteThreads * blocks) {
+        float v = 0.0f;
         int c = 0;
         for (int b = 0; b < blocks; ++b) {
-            p += part_p[(size_t)b * E + e];
-            c += part_c[(size_t)b * E + e];
+            v += __uint_as_float(ld_cluster(cluster_addr(sums_at + 4 * e, b)));
+            c += (int)ld_cluster(cluster_addr(cnt_at + 4 * e, b));
         }
-        counts[e] = c;
-        const float fn = (float)max(n, 1);
-        v = ((float)c / ((float)K * fn)) * (p / fn);
+        if constexpr (SINGLE) {
+            o.counts[e] = c;
+            term += loss_term(v, c, n, K);
+        } else {
+            uint32_t *q = part + (size_t)(blockIdx.x / kRouteCluster) * (2 * E + 1);
+            q[e] = __float_as_uint(v);
+            q[E + e] = (uint32_t)c;
+        }
     }
-    v = warp_sum(v);
+    if constexpr (SINGLE) {
+        __syncthreads();                                 // picks is free: warp sums go there
+        float *const warp_terms = reinterpret_cast<float *>(&picks[0][0]);
+        term = warp_sum(term);
+        if (lane == 0) warp_terms[warp] = term;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float v = 0.0f;
+            for (int w = 0; w < kRouteWarps; ++w) v += warp_terms[w];
+            const uint32_t to = cluster_addr(smem_addr(&terms[rank]), 0);
+            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(to), "f"(v) : "memory");
+        }
+        cluster_sync_all();
+        if (rank == 0 && threadIdx.x == 0) {
+            float v = 0.0f;
+            for (int b = 0; b < blocks; ++b) v += terms[b];
+            *o.loss = o.coef * (float)E * v;
+            *o.routed = n;
+        }
+    } else {
+        if (rank == 0 && threadIdx.x == 0) part[(size_t)(blockIdx.x / kRouteCluster) * (2 * E + 1) + 2 * E] = (uint32_t)n;
+        cluster_sync_all();                              // the others have read this block's memory
+    }
+}
+
+// The clusters' totals in order: counts, routed tokens and the loss.
+__global__ void __launch_bounds__(1024)
+route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int K, RouteOut o)
+{
+    __shared__ float red[32];
+    __shared__ int total;
+    const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+    if (threadIdx.x == 0) total = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const size_t row = 2 * (size_t)E + 1;
+    for (int b = threadIdx.x; b < clusters; b += blockDim.x) atomicAdd(&total, (int)part[b * row + 2 * E]);
+    float p = 0.0f;
+    int c = 0;
+    if (e < E) {
+#pragma unroll 20
+        for (int b = 0; b < clusters; ++b) {
+            p += __uint_as_float(part[b * row + e]);
+            c += (int)part[b * row + E + e];
+        }
+        o.counts[e] = c;
+    }
+    __syncthreads();
+    const int n = total;
+    float v = warp_sum(e < E ? loss_term(p, c, n, K) : 0.0f);
     if (lane == 0) red[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        v = warp_sum(red[lane]);
+        v = warp_sum(lane < (int)blockDim.x / 32 ? red[lane] : 0.0f);
         if (lane == 0) {
-            *loss = coef * (float)E * v;
-            *routed = n;
+            *o.loss = o.coef * (float)E * v;
+            *o.routed = n;
         }
     }
 }
 
+constexpr int kBackWarps = 8;
+constexpr int kBackThreads = kBackWarps * 32;
+constexpr int kBackBlocks = 152 * 5;
+
 // grad_te = p_te (a_e - sum_j p_tj a_j) with a_e = dL coef E c_e / (K n^2),
 // plus the weights' part at (renormalised) or around (not) the chosen ids.
-template <int NV, typename L>
-__global__ void __launch_bounds__(kRouteThreads)
+template <int NV, bool VEC, typename L>
+__global__ void __launch_bounds__(kBackThreads)
 route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm, float coef,
                       const int32_t *__restrict__ ids, const int32_t *__restrict__ counts,
                       const int32_t *__restrict__ routed, const float *__restrict__ grad_weights,
@@ -215,8 +314,9 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
 {
     extern __shared__ float sm[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *add = sm + (size_t)warp * E;                  // this warp's row of additions
-    for (int e = lane; e < E; e += 32) add[e] = 0.0f;
+    float *add = sm + (size_t)warp * 32 * NV;            // this warp's row of additions
+#pragma unroll
+    for (int j = 0; j < NV; ++j) add[j * 32 + lane] = 0.0f;
     __syncwarp();
     pdl_wait();
     pdl_trigger();
@@ -225,31 +325,40 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
     float a[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int e = j * 32 + lane;
+        const int e = lane * NV + j;
         a[j] = e < E && unit != 0.0f ? unit * (float)counts[e] : 0.0f;
     }
-    for (int t = blockIdx.x * kRouteWarps + warp; t < T; t += gridDim.x * kRouteWarps) {
+    for (int t = blockIdx.x * kBackWarps + warp; t < T; t += gridDim.x * kBackWarps) {
         const L *row = logits + (size_t)t * E;
-        int id = lane < K ? ids[(size_t)t * K + lane] : -1;
-        if ((unsigned)id >= (unsigned)E) id = -1;
-        const bool masked = __ballot_sync(kFullMask, id >= 0) == 0;
         float x[NV];
-        const float m = load_row<NV>(row, E, masked, lane, x);
-        const float s = exp_row<NV>(x, m);
-        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-        float dot = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            x[j] *= inv;
-            dot += x[j] * a[j];
-        }
-        dot = warp_sum(dot);
-        float w = 0.0f, dw = 0.0f;
-        if (id >= 0) {
-            const float l = load_logit(row + id);
-            w = l == -INFINITY ? 0.0f : expf(l - m) * inv;
+        load_row<NV, VEC>(row, E, lane, x);
+        int id = -1;
+        float dw = 0.0f;
+        if (lane < K) {
+            id = ids[(size_t)t * K + lane];
             if (grad_weights) dw = grad_weights[(size_t)t * K + lane];
         }
+        if ((unsigned)id >= (unsigned)E) id = -1;
+        float chosen = id >= 0 ? to_float(row[id]) : -INFINITY;
+        const bool masked = __ballot_sync(kFullMask, id >= 0) == 0;
+        if (masked) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) x[j] = -INFINITY;
+        }
+        float m = warp_max(lane_max<NV>(x));
+        if (!(m > -INFINITY)) m = 0.0f;
+        float s = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            x[j] = weight_of(x[j], m);
+            s += x[j];
+            dot += x[j] * a[j];
+        }
+        s = warp_sum(s);
+        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+        dot = warp_sum(dot) * inv;
+        float w = id >= 0 ? weight_of(chosen, m) * inv : 0.0f;
+        if (id < 0) dw = 0.0f;
         if (renorm) {
             const float total = warp_sum(w);
             if (total != 0.0f) w /= total;
@@ -262,18 +371,32 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
         if (__any_sync(kFullMask, id >= 0 && (same & (same - 1)))) {
             float sum = 0.0f;
             for (int k = 0; k < K; ++k) {
-                const float o = __shfl_sync(kFullMask, v, k);
-                if (same >> k & 1) sum += o;
+                const float other = __shfl_sync(kFullMask, v, k);
+                if (same >> k & 1) sum += other;
             }
             v = sum;
             if (lane != __ffs(same) - 1) id = -1;
         }
         if (id >= 0) add[id] = v;
         __syncwarp();
+        float y[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int e = j * 32 + lane;
-            if (e < E) store_logit(grad + (size_t)t * E + e, x[j] * (a[j] - dot) + add[e]);
+        for (int j = 0; j < NV; ++j) y[j] = x[j] * inv * (a[j] - dot) + add[lane * NV + j];
+        L *to = grad + (size_t)t * E + lane * NV;
+        if constexpr (VEC) {
+            constexpr int W = 16 / sizeof(L);
+#pragma unroll
+            for (int j = 0; j < NV; j += W) {
+                uint4 q;
+                L *z = reinterpret_cast<L *>(&q);
+#pragma unroll
+                for (int i = 0; i < W; ++i) z[i] = from_float(y[j + i], L());
+                if (lane * NV + j < E) st_v4(to + j, q);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (lane * NV + j < E) to[j] = from_float(y[j], L());
         }
         __syncwarp();
         if (id >= 0) add[id] = 0.0f;
@@ -281,72 +404,99 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
     }
 }
 
-int route_blocks(int T)
+// Blocks of one cluster that writes the results itself, or 0: up to four
+// tokens a warp one launch is quicker than two.
+int single_blocks(int T)
 {
     const int need = ceil_div(T, kRouteWarps);
-    return need < 1 ? 1 : need < kRouteMaxBlocks ? need : kRouteMaxBlocks;
+    for (int b = 1; b <= kSingleCluster; b *= 2)
+        if (need <= b) return b;
+    return need <= 4 * kSingleCluster ? kSingleCluster : 0;
 }
 
-template <int NV, typename L>
+int route_clusters(int T)
+{
+    const int need = ceil_div(ceil_div(T, kRouteWarps), kRouteCluster);
+    return need < kRouteClusters ? need : kRouteClusters;
+}
+
+template <int NV, bool VEC, typename L>
 cudaError_t run_forward(const void *logits, int T, int E, int K, int renorm, float coef,
                         const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts,
                         int32_t *routed, float *loss, void *workspace, cudaStream_t s)
 {
-    const int blocks = route_blocks(T);
-    float *part_p = static_cast<float *>(workspace);
-    int32_t *part_c = reinterpret_cast<int32_t *>(part_p + (size_t)blocks * E);
-    int32_t *part_n = part_c + (size_t)blocks * E;
-    cudaError_t e = launch_pdl(route_kernel<NV, L>, dim3(blocks), dim3(kRouteThreads),
-                               (2 * (size_t)E + 1) * 4, s, static_cast<const L *>(logits), T, E,
-                               K, renorm, mask, ids, weights, part_p, part_c, part_n);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(route_finish_kernel, dim3(1), dim3(1024), 0, s, part_p, part_c, part_n,
-                      blocks, E, K, coef, counts, routed, loss);
+    const size_t smem = ((size_t)(kRouteWarps + 1) * E + 1) * 4;
+    const RouteOut o{counts, routed, loss, coef};
+    const int single = single_blocks(T);
+    auto *const kernel = single ? route_kernel<NV, VEC, true, L> : route_kernel<NV, VEC, false, L>;
+    if (smem > 40 << 10) {
+        const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int blocks = single ? single : route_clusters(T) * kRouteCluster;
+    uint32_t *part = static_cast<uint32_t *>(workspace);
+    cudaError_t e = launch_pdl_clusters(kernel, dim3(blocks), dim3(kRouteThreads), smem, s,
+                                        single ? single : kRouteCluster, static_cast<const L *>(logits),
+                                        T, E, K, renorm, mask, ids, weights, part, o);
+    if (e != cudaSuccess || single) return e;
+    return launch_pdl(route_finish_kernel, dim3(1), dim3(ceil_div(E, 32) * 32), 0, s, part,
+                      blocks / kRouteCluster, E, K, o);
 }
 
-template <int NV, typename L>
+template <int NV, bool VEC, typename L>
 cudaError_t run_backward(const void *logits, int T, int E, int K, int renorm, float coef,
                          const int32_t *ids, const int32_t *counts, const int32_t *routed,
                          const float *grad_weights, const float *grad_loss, void *grad,
                          cudaStream_t s)
 {
-    return launch_pdl(route_backward_kernel<NV, L>, dim3(route_blocks(T)), dim3(kRouteThreads),
-                      (size_t)kRouteWarps * E * 4, s, static_cast<const L *>(logits), T, E, K,
-                      renorm, coef, ids, counts, routed, grad_weights, grad_loss,
+    const int need = ceil_div(T, kBackWarps);
+    return launch_pdl(route_backward_kernel<NV, VEC, L>, dim3(need < kBackBlocks ? need : kBackBlocks),
+                      dim3(kBackThreads), (size_t)kBackThreads * NV * 4, s, static_cast<const L *>(logits),
+                      T, E, K, renorm, coef, ids, counts, routed, grad_weights, grad_loss,
                       static_cast<L *>(grad));
+}
+
+bool rows_aligned(const void *p, const void *q, int E, int size)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15) == 0 && E * size % 16 == 0;
 }
 
 }  // namespace
 
 size_t route_workspace_bytes(int T, int E)
 {
-    const size_t blocks = route_blocks(T);
-    return (blocks * ((size_t)E * 8 + 4) + 255) / 256 * 256;
+    const size_t clusters = single_blocks(T) ? 1 : route_clusters(T);
+    return (clusters * (2 * (size_t)E + 1) * 4 + 255) / 256 * 256;
 }
 
-// Values a lane holds: the smallest of these that covers E.
-#define MOE_ROUTE_CASES(CALL)                                                   \
+// Values a lane holds: the smallest of these that covers E.  Rows that 16-byte
+// loads cannot read (a length or an address off the grid) go value by value.
+#define MOE_ROUTE_WIDTHS(CALL, VEC, L)                                          \
+    do {                                                                        \
+        if (E <= 256) return CALL(8, VEC, L);                                   \
+        if (E <= 512) return CALL(16, VEC, L);                                  \
+        return CALL(32, VEC, L);                                                \
+    } while (0)
+#define MOE_ROUTE_CASES(CALL, OTHER)                                            \
     if (bf16) {                                                                 \
-        if (E <= 64) return CALL(2, __nv_bfloat16);                             \
-        if (E <= 128) return CALL(4, __nv_bfloat16);                            \
-        if (E <= 256) return CALL(8, __nv_bfloat16);                            \
-        if (E <= 512) return CALL(16, __nv_bfloat16);                           \
-        return CALL(32, __nv_bfloat16);                                         \
+        if (rows_aligned(logits, OTHER, E, 2)) MOE_ROUTE_WIDTHS(CALL, true, __nv_bfloat16); \
+        MOE_ROUTE_WIDTHS(CALL, false, __nv_bfloat16);                           \
     }                                                                           \
-    if (E <= 64) return CALL(2, float);                                         \
-    if (E <= 128) return CALL(4, float);                                        \
-    if (E <= 256) return CALL(8, float);                                        \
-    if (E <= 512) return CALL(16, float);                                       \
-    return CALL(32, float);
+    if (rows_aligned(logits, OTHER, E, 4)) {                                    \
+        if (E <= 128) return CALL(4, true, float);                              \
+        if (E > 256 && E <= 384) return CALL(12, true, float);                  \
+        MOE_ROUTE_WIDTHS(CALL, true, float);                                    \
+    }                                                                           \
+    MOE_ROUTE_WIDTHS(CALL, false, float)
 
 cudaError_t launch_route(const void *logits, int bf16, int T, int E, int K, int renorm, float coef,
                          const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts,
                          int32_t *routed, float *loss, void *workspace, cudaStream_t stream)
 {
-#define CALL(NV, L)                                                                           \
-    run_forward<NV, L>(logits, T, E, K, renorm, coef, mask, ids, weights, counts, routed, loss, \
-                       workspace, stream)
-    MOE_ROUTE_CASES(CALL)
+#define CALL(NV, VEC, L)                                                                       \
+    run_forward<NV, VEC, L>(logits, T, E, K, renorm, coef, mask, ids, weights, counts, routed, \
+                            loss, workspace, stream)
+    MOE_ROUTE_CASES(CALL, logits);
 #undef CALL
 }
 
@@ -355,10 +505,10 @@ cudaError_t launch_route_backward(const void *logits, int bf16, int T, int E, in
                                   const int32_t *routed, const float *grad_weights,
                                   const float *grad_loss, void *grad, cudaStream_t stream)
 {
-#define CALL(NV, L)                                                                         \
-    run_backward<NV, L>(logits, T, E, K, renorm, coef, ids, counts, routed, grad_weights,   \
-                        grad_loss, grad, stream)
-    MOE_ROUTE_CASES(CALL)
+#define CALL(NV, VEC, L)                                                                          \
+    run_backward<NV, VEC, L>(logits, T, E, K, renorm, coef, ids, counts, routed, grad_weights,    \
+                             grad_loss, grad, stream)
+    MOE_ROUTE_CASES(CALL, grad);
 #undef CALL
 }
 
