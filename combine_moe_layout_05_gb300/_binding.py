@@ -103,9 +103,7 @@ def declared_functions(header: str | None = None) -> list[str]:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    return t.data_ptr() if t.numel() > 0 else None
+    return None if t is None else t.data_ptr()          # 0 for an empty tensor
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)

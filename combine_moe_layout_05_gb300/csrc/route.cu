@@ -11,8 +11,9 @@
 // read once, in 16-byte loads where its alignment allows, and a lower lane
 // always has lower expert numbers: among equal logits the lowest lane, and in
 // it the lowest place, is the lowest expert.  The maximum and each pick are
-// one warp-wide maximum; the lane that has it strikes it out and finds its
-// next.  Sums of p over tokens stay in registers (fp32) while a warp walks its
+// one warp-wide maximum over the lanes' next largest: a lane keeps its logits
+// sorted as well and steps on by predicated moves when its own is picked; which
+// expert a pick was is looked up for all K at once, after the last.  Sums of p over tokens stay in registers (fp32) while a warp walks its
 // tokens, are added warp by warp in a block, block by block in a cluster
 // (distributed shared memory) and cluster by cluster at the end, always in
 // that order, so a call's results do not depend on timing.
@@ -26,8 +27,8 @@ namespace {
 
 constexpr int kRouteWarps = 16;
 constexpr int kRouteThreads = kRouteWarps * 32;
-constexpr int kRouteCluster = 4;                    // blocks that add their sums up together
-constexpr int kRouteClusters = 76;                  // at most: two blocks a multiprocessor
+constexpr int kRouteCluster = 8;                    // blocks that add their sums up together
+constexpr int kRouteClusters = 38;                  // at most: two blocks a multiprocessor
 constexpr int kSingleCluster = 8;                   // blocks of the form that needs one launch
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -41,6 +42,13 @@ __device__ __forceinline__ float exp2_approx(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Sum over the first `lanes` lanes, a power of two (the others get other sums).
+__device__ __forceinline__ float lanes_sum(float v, int lanes)
+{
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -58,27 +66,65 @@ __device__ __forceinline__ float warp_max(float v)
     return m;
 }
 
-// Lane's NV logits of a row of E (-inf past E).  VEC: rows start on 16 bytes
-// and E is a multiple of a 16-byte load's values.
-template <int NV, bool VEC, typename L>
+// 4, 8 or 16 bytes read once, as W values.
+template <int W, typename L>
+__device__ __forceinline__ void load_values(const L *p, float *x)
+{
+    union {
+        uint4 v4;
+        uint2 v2;
+        uint32_t v1;
+        L one[16 / sizeof(L)];
+    } u;
+    if constexpr (W * sizeof(L) == 16) u.v4 = ld_stream_v4(p);
+    else if constexpr (W * sizeof(L) == 8) u.v2 = ld_stream_v2(p);
+    else if constexpr (W * sizeof(L) == 4) u.v1 = __ldg(reinterpret_cast<const uint32_t *>(p));
+    else u.one[0] = *p;
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = to_float(u.one[i]);
+}
+
+template <int W, typename L>
+__device__ __forceinline__ void store_values(L *p, const float *x)
+{
+    union {
+        uint4 v4;
+        uint2 v2;
+        uint32_t v1;
+        L one[16 / sizeof(L)];
+    } u;
+#pragma unroll
+    for (int i = 0; i < W; ++i) u.one[i] = from_float(x[i], L());
+    if constexpr (W * sizeof(L) == 16) st_v4(p, u.v4);
+    else if constexpr (W * sizeof(L) == 8) st_v2(p, u.v2);
+    else if constexpr (W * sizeof(L) == 4) *reinterpret_cast<uint32_t *>(p) = u.v1;
+    else *p = u.one[0];
+}
+
+// Lane's NV logits of a row of E (-inf past E), W at a time: rows start on
+// that many values' bytes, and E is a multiple of W.
+template <int NV, int W, typename L>
 __device__ __forceinline__ void load_row(const L *row, int E, int lane, float (&x)[NV])
 {
-    constexpr int W = 16 / sizeof(L);
-    if constexpr (VEC) {
-        static_assert(NV % W == 0);
 #pragma unroll
-        for (int j = 0; j < NV; j += W) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            const bool in = lane * NV + j < E;
-            if (in) v = ld_stream_v4(row + lane * NV + j);
-            const L *q = reinterpret_cast<const L *>(&v);
+    for (int j = 0; j < NV; ++j) x[j] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < W; ++i) x[j + i] = in ? to_float(q[i]) : -INFINITY;
+    for (int j = 0; j < NV; j += W)
+        if (lane * NV + j < E) load_values<W>(row + lane * NV + j, x + j);
+}
+
+// Descending, by a network of odd and even transpositions (no NaN among them).
+template <int NV>
+__device__ __forceinline__ void sort_values(float (&v)[NV])
+{
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = i & 1; j + 1 < NV; j += 2) {
+            const float hi = fmaxf(v[j], v[j + 1]), lo = fminf(v[j], v[j + 1]);
+            v[j] = hi;
+            v[j + 1] = lo;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) x[j] = lane * NV + j < E ? to_float(row[lane * NV + j]) : -INFINITY;
-    }
 }
 
 template <int NV>
@@ -120,16 +166,17 @@ struct RouteOut {
 // SINGLE: the grid is one cluster, which writes the results; otherwise every
 // cluster writes its totals to part[cluster]: E probability sums, E counts and
 // the routed tokens.
-template <int NV, bool VEC, bool SINGLE, typename L>
+template <int NV, int W, int KT, bool SINGLE, typename L>
 __global__ void __launch_bounds__(kRouteThreads, NV > 16 ? 1 : 2)
-route_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm,
+route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
              const uint8_t *__restrict__ mask, int32_t *__restrict__ ids,
              float *__restrict__ weights, uint32_t *__restrict__ part, RouteOut o)
 {
+    const int K = KT > 0 ? KT : any_k;
     extern __shared__ float sm[];
     float *const sums = sm;                              // [kRouteWarps][E], then [E]
     int32_t *const cnt = reinterpret_cast<int32_t *>(sm + (size_t)kRouteWarps * E);     // [E] and the routed tokens
-    __shared__ int32_t picks[kRouteWarps][MOE_MAX_TOPK];
+    __shared__ float warp_terms[kRouteWarps];
     __shared__ float terms[kSingleCluster];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int e = threadIdx.x; e <= E; e += kRouteThreads) cnt[e] = 0;
@@ -137,19 +184,20 @@ route_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm,
     pdl_trigger();
     __syncthreads();
 
+    const int k_lanes = 1 << (32 - __clz(K - 1));        // K, rounded up to a power of two
+    int routed = 0;                                      // tokens with a first pick (lane 0)
     float acc[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) acc[j] = 0.0f;
 
     for (int t = blockIdx.x * kRouteWarps + warp; t < T; t += gridDim.x * kRouteWarps) {
         float x[NV];
-        load_row<NV, VEC>(logits + (size_t)t * E, E, lane, x);
+        load_row<NV, W>(logits + (size_t)t * E, E, lane, x);
         if (mask && !mask[t]) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) x[j] = -INFINITY;
         }
-        float best = lane_max<NV>(x);
-        float m = warp_max(best);
+        float m = warp_max(lane_max<NV>(x));
         if (!(m > -INFINITY)) m = 0.0f;
         float p[NV], s = 0.0f;
 #pragma unroll
@@ -158,50 +206,72 @@ route_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm,
             s += p[j];
         }
         s = warp_sum(s);
-        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
 #pragma unroll
         for (int j = 0; j < NV; ++j) acc[j] += p[j] * inv;
 
-        float mine = -INFINITY;                          // pick number `lane`
-        for (int k = 0; k < K; ++k) {
-            const float top = warp_max(best);
-            if (!(top > -INFINITY)) break;               // no open expert is left
-            if (lane == k) mine = top;
-            const unsigned tied = __ballot_sync(kFullMask, best == top);
-            if (lane == __ffs(tied) - 1) {
-                int at = 0;
-                bool struck = false;
+        // Pick number `lane`: its logit, and the lane that holds it.  Past the
+        // last open expert the picks are -inf, and not taken below.
+        float mine = -INFINITY;
+        int from = 0;
+        float next[NV];
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const bool here = !struck && x[j] == top;
-                    if (here) {
-                        at = j;
-                        x[j] = -INFINITY;
-                    }
-                    struck |= here;
-                }
-                picks[warp][k] = lane * NV + at;
-                best = lane_max<NV>(x);
+        for (int j = 0; j < NV; ++j) next[j] = x[j] > -INFINITY ? x[j] + 0.0f : -INFINITY;  // no NaN, one zero
+        if constexpr (NV <= 12) sort_values<NV>(next);
+        float best = NV <= 12 ? next[0] : lane_max<NV>(next);
+        auto pick = [&](int k) {
+            const float top = warp_max(best);
+            const int owner = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+            if (lane == k) {
+                mine = top;
+                from = owner;
             }
+            if constexpr (NV <= 12) {
+#pragma unroll
+                for (int j = 0; j + 1 < NV; ++j) next[j] = lane == owner ? next[j + 1] : next[j];
+                next[NV - 1] = lane == owner ? -INFINITY : next[NV - 1];
+                best = next[0];
+            } else if (lane == owner) {
+                int at = 0;
+#pragma unroll
+                for (int j = NV - 1; j >= 0; --j)
+                    if (next[j] == top) at = j;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    if (j == at) next[j] = -INFINITY;
+                best = lane_max<NV>(next);
+            }
+        };
+        if constexpr (KT > 0) {
+#pragma unroll
+            for (int k = 0; k < KT; ++k) pick(k);
+        } else {
+            for (int k = 0; k < K; ++k) pick(k);
         }
-        __syncwarp();
+        // Its place among the owner's logits: equal ones were picked in order.
+        const unsigned alike = __match_any_sync(kFullMask, __float_as_int(mine)) & __match_any_sync(kFullMask, from);
+        int before = __popc(alike & ((1u << lane) - 1)), place = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const bool same = __shfl_sync(kFullMask, x[j], from) == mine;
+            if (same && before == 0) place = j;
+            before -= same;
+        }
         const bool taken = lane < K && mine > -INFINITY;
         float w = taken ? weight_of(mine, m) * inv : 0.0f;
         if (renorm) {
-            const float total = warp_sum(w);
-            if (total != 0.0f) w /= total;
+            const float total = lanes_sum(w, k_lanes);
+            if (total != 0.0f) w = __fdividef(w, total);
         }
-        const int id = taken ? picks[warp][lane] : -1;
+        const int id = taken ? from * NV + place : -1;
         if (lane < K) {
             ids[(size_t)t * K + lane] = id;
             weights[(size_t)t * K + lane] = w;
         }
-        if (taken) {
-            atomicAdd(&cnt[id], 1);
-            if (lane == 0) atomicAdd(&cnt[E], 1);
-        }
-        __syncwarp();
+        if (taken) atomicAdd(&cnt[id], 1);
+        routed += taken;
     }
+    if (lane == 0) atomicAdd(&cnt[E], routed);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         if (lane * NV + j < E) sums[warp * E + lane * NV + j] = acc[j];
@@ -238,8 +308,6 @@ route_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm,
         }
     }
     if constexpr (SINGLE) {
-        __syncthreads();                                 // picks is free: warp sums go there
-        float *const warp_terms = reinterpret_cast<float *>(&picks[0][0]);
         term = warp_sum(term);
         if (lane == 0) warp_terms[warp] = term;
         __syncthreads();
@@ -262,37 +330,53 @@ route_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm,
     }
 }
 
-// The clusters' totals in order: counts, routed tokens and the loss.
+// The clusters' totals in order: counts, routed tokens and the loss.  `lanes`
+// threads (E rounded up to a warp) take each a share of the clusters, whose
+// sums are then added in order.
 __global__ void __launch_bounds__(1024)
-route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int K, RouteOut o)
+route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int K, int lanes, RouteOut o)
 {
+    __shared__ float share_p[1024];
+    __shared__ int32_t share_c[1024];
     __shared__ float red[32];
     __shared__ int total;
-    const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+    const int groups = blockDim.x / lanes, g = threadIdx.x / lanes, e = threadIdx.x - g * lanes;
+    const int each = ceil_div(clusters, groups);
     if (threadIdx.x == 0) total = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
     const size_t row = 2 * (size_t)E + 1;
-    for (int b = threadIdx.x; b < clusters; b += blockDim.x) atomicAdd(&total, (int)part[b * row + 2 * E]);
+    if (threadIdx.x < clusters) atomicAdd(&total, (int)part[threadIdx.x * row + 2 * E]);
     float p = 0.0f;
     int c = 0;
     if (e < E) {
-#pragma unroll 20
-        for (int b = 0; b < clusters; ++b) {
+        const int last = min(clusters, (g + 1) * each);
+#pragma unroll 10
+        for (int b = g * each; b < last; ++b) {
             p += __uint_as_float(part[b * row + e]);
             c += (int)part[b * row + E + e];
         }
-        o.counts[e] = c;
     }
+    share_p[threadIdx.x] = p;
+    share_c[threadIdx.x] = c;
     __syncthreads();
     const int n = total;
-    float v = warp_sum(e < E ? loss_term(p, c, n, K) : 0.0f);
-    if (lane == 0) red[warp] = v;
+    float v = 0.0f;
+    if (threadIdx.x < E) {
+        for (int i = 1; i < groups; ++i) {
+            p += share_p[i * lanes + e];
+            c += share_c[i * lanes + e];
+        }
+        o.counts[e] = c;
+        v = loss_term(p, c, n, K);
+    }
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (warp == 0) {
-        v = warp_sum(lane < (int)blockDim.x / 32 ? red[lane] : 0.0f);
-        if (lane == 0) {
+    if (threadIdx.x < 32) {
+        v = warp_sum(threadIdx.x < blockDim.x / 32 ? red[threadIdx.x] : 0.0f);
+        if (threadIdx.x == 0) {
             *o.loss = o.coef * (float)E * v;
             *o.routed = n;
         }
@@ -305,7 +389,7 @@ constexpr int kBackBlocks = 152 * 5;
 
 // grad_te = p_te (a_e - sum_j p_tj a_j) with a_e = dL coef E c_e / (K n^2),
 // plus the weights' part at (renormalised) or around (not) the chosen ids.
-template <int NV, bool VEC, typename L>
+template <int NV, int W, typename L>
 __global__ void __launch_bounds__(kBackThreads)
 route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm, float coef,
                       const int32_t *__restrict__ ids, const int32_t *__restrict__ counts,
@@ -320,6 +404,7 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
     __syncwarp();
     pdl_wait();
     pdl_trigger();
+    const int k_lanes = 1 << (32 - __clz(K - 1));
     const float n = (float)max(*routed, 1);
     const float unit = grad_loss ? *grad_loss * coef * (float)E / ((float)K * n) / n : 0.0f;
     float a[NV];
@@ -331,7 +416,7 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
     for (int t = blockIdx.x * kBackWarps + warp; t < T; t += gridDim.x * kBackWarps) {
         const L *row = logits + (size_t)t * E;
         float x[NV];
-        load_row<NV, VEC>(row, E, lane, x);
+        load_row<NV, W>(row, E, lane, x);
         int id = -1;
         float dw = 0.0f;
         if (lane < K) {
@@ -355,15 +440,16 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
             dot += x[j] * a[j];
         }
         s = warp_sum(s);
-        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
         dot = warp_sum(dot) * inv;
         float w = id >= 0 ? weight_of(chosen, m) * inv : 0.0f;
         if (id < 0) dw = 0.0f;
         if (renorm) {
-            const float total = warp_sum(w);
-            if (total != 0.0f) w /= total;
+            const float total = lanes_sum(w, k_lanes);
+            if (total != 0.0f) w = __fdividef(w, total);
         }
-        const float inner = warp_sum(w * dw);
+        float inner = lanes_sum(w * dw, k_lanes);
+        inner = __shfl_sync(kFullMask, inner, 0);
         float v = renorm ? w * (dw - inner) : w * dw;
         if (!renorm) dot += inner;
         // one id listed twice: its first lane adds them all, in k order
@@ -383,21 +469,9 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
 #pragma unroll
         for (int j = 0; j < NV; ++j) y[j] = x[j] * inv * (a[j] - dot) + add[lane * NV + j];
         L *to = grad + (size_t)t * E + lane * NV;
-        if constexpr (VEC) {
-            constexpr int W = 16 / sizeof(L);
 #pragma unroll
-            for (int j = 0; j < NV; j += W) {
-                uint4 q;
-                L *z = reinterpret_cast<L *>(&q);
-#pragma unroll
-                for (int i = 0; i < W; ++i) z[i] = from_float(y[j + i], L());
-                if (lane * NV + j < E) st_v4(to + j, q);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (lane * NV + j < E) to[j] = from_float(y[j], L());
-        }
+        for (int j = 0; j < NV; j += W)
+            if (lane * NV + j < E) store_values<W>(to + j, y + j);
         __syncwarp();
         if (id >= 0) add[id] = 0.0f;
         __syncwarp();
@@ -420,7 +494,7 @@ int route_clusters(int T)
     return need < kRouteClusters ? need : kRouteClusters;
 }
 
-template <int NV, bool VEC, typename L>
+template <int NV, int W, typename L>
 cudaError_t run_forward(const void *logits, int T, int E, int K, int renorm, float coef,
                         const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts,
                         int32_t *routed, float *loss, void *workspace, cudaStream_t s)
@@ -428,7 +502,8 @@ cudaError_t run_forward(const void *logits, int T, int E, int K, int renorm, flo
     const size_t smem = ((size_t)(kRouteWarps + 1) * E + 1) * 4;
     const RouteOut o{counts, routed, loss, coef};
     const int single = single_blocks(T);
-    auto *const kernel = single ? route_kernel<NV, VEC, true, L> : route_kernel<NV, VEC, false, L>;
+    auto *const kernel = K == 8 ? single ? route_kernel<NV, W, 8, true, L> : route_kernel<NV, W, 8, false, L>
+                                : single ? route_kernel<NV, W, 0, true, L> : route_kernel<NV, W, 0, false, L>;
     if (smem > 40 << 10) {
         const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
         if (e != cudaSuccess) return e;
@@ -439,26 +514,29 @@ cudaError_t run_forward(const void *logits, int T, int E, int K, int renorm, flo
                                         single ? single : kRouteCluster, static_cast<const L *>(logits),
                                         T, E, K, renorm, mask, ids, weights, part, o);
     if (e != cudaSuccess || single) return e;
-    return launch_pdl(route_finish_kernel, dim3(1), dim3(ceil_div(E, 32) * 32), 0, s, part,
-                      blocks / kRouteCluster, E, K, o);
+    const int lanes = ceil_div(E, 32) * 32;
+    return launch_pdl(route_finish_kernel, dim3(1), dim3(1024 / lanes * lanes), 0, s, part,
+                      blocks / kRouteCluster, E, K, lanes, o);
 }
 
-template <int NV, bool VEC, typename L>
+template <int NV, int W, typename L>
 cudaError_t run_backward(const void *logits, int T, int E, int K, int renorm, float coef,
                          const int32_t *ids, const int32_t *counts, const int32_t *routed,
                          const float *grad_weights, const float *grad_loss, void *grad,
                          cudaStream_t s)
 {
     const int need = ceil_div(T, kBackWarps);
-    return launch_pdl(route_backward_kernel<NV, VEC, L>, dim3(need < kBackBlocks ? need : kBackBlocks),
+    return launch_pdl(route_backward_kernel<NV, W, L>, dim3(need < kBackBlocks ? need : kBackBlocks),
                       dim3(kBackThreads), (size_t)kBackThreads * NV * 4, s, static_cast<const L *>(logits),
                       T, E, K, renorm, coef, ids, counts, routed, grad_weights, grad_loss,
                       static_cast<L *>(grad));
 }
 
-bool rows_aligned(const void *p, const void *q, int E, int size)
+// Whether rows of E values can be read (and written) `bytes` at a time.
+bool rows_aligned(const void *p, const void *q, int E, int size, int bytes)
 {
-    return ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15) == 0 && E * size % 16 == 0;
+    return ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & (bytes - 1)) == 0 &&
+           E * size % bytes == 0;
 }
 
 }  // namespace
@@ -469,32 +547,37 @@ size_t route_workspace_bytes(int T, int E)
     return (clusters * (2 * (size_t)E + 1) * 4 + 255) / 256 * 256;
 }
 
-// Values a lane holds: the smallest of these that covers E.  Rows that 16-byte
-// loads cannot read (a length or an address off the grid) go value by value.
-#define MOE_ROUTE_WIDTHS(CALL, VEC, L)                                          \
-    do {                                                                        \
-        if (E <= 256) return CALL(8, VEC, L);                                   \
-        if (E <= 512) return CALL(16, VEC, L);                                  \
-        return CALL(32, VEC, L);                                                \
-    } while (0)
+// Values a lane holds: the smallest of these that covers E, read in the widest
+// loads that its rows' length and address allow.
 #define MOE_ROUTE_CASES(CALL, OTHER)                                            \
     if (bf16) {                                                                 \
-        if (rows_aligned(logits, OTHER, E, 2)) MOE_ROUTE_WIDTHS(CALL, true, __nv_bfloat16); \
-        MOE_ROUTE_WIDTHS(CALL, false, __nv_bfloat16);                           \
+        using L = __nv_bfloat16;                                                \
+        if (E <= 128 && rows_aligned(logits, OTHER, E, 2, 8)) return CALL(4, 4, L);  \
+        if (rows_aligned(logits, OTHER, E, 2, 16)) {                            \
+            if (E <= 256) return CALL(8, 8, L);                                 \
+            if (E <= 512) return CALL(16, 8, L);                                \
+            return CALL(32, 8, L);                                              \
+        }                                                                       \
+        if (E <= 256 && rows_aligned(logits, OTHER, E, 2, 4)) return CALL(8, 2, L);  \
+        if (E <= 256) return CALL(8, 1, L);                                     \
+        return CALL(32, 1, L);                                                  \
     }                                                                           \
-    if (rows_aligned(logits, OTHER, E, 4)) {                                    \
-        if (E <= 128) return CALL(4, true, float);                              \
-        if (E > 256 && E <= 384) return CALL(12, true, float);                  \
-        MOE_ROUTE_WIDTHS(CALL, true, float);                                    \
+    if (rows_aligned(logits, OTHER, E, 4, 16)) {                                \
+        if (E <= 128) return CALL(4, 4, float);                                 \
+        if (E <= 256) return CALL(8, 4, float);                                 \
+        if (E <= 384) return CALL(12, 4, float);                                \
+        if (E <= 512) return CALL(16, 4, float);                                \
+        return CALL(32, 4, float);                                              \
     }                                                                           \
-    MOE_ROUTE_WIDTHS(CALL, false, float)
+    if (E <= 256) return CALL(8, 1, float);                                     \
+    return CALL(32, 1, float)
 
 cudaError_t launch_route(const void *logits, int bf16, int T, int E, int K, int renorm, float coef,
                          const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts,
                          int32_t *routed, float *loss, void *workspace, cudaStream_t stream)
 {
-#define CALL(NV, VEC, L)                                                                       \
-    run_forward<NV, VEC, L>(logits, T, E, K, renorm, coef, mask, ids, weights, counts, routed, \
+#define CALL(NV, W, L)                                                                       \
+    run_forward<NV, W, L>(logits, T, E, K, renorm, coef, mask, ids, weights, counts, routed, \
                             loss, workspace, stream)
     MOE_ROUTE_CASES(CALL, logits);
 #undef CALL
@@ -505,8 +588,8 @@ cudaError_t launch_route_backward(const void *logits, int bf16, int T, int E, in
                                   const int32_t *routed, const float *grad_weights,
                                   const float *grad_loss, void *grad, cudaStream_t stream)
 {
-#define CALL(NV, VEC, L)                                                                          \
-    run_backward<NV, VEC, L>(logits, T, E, K, renorm, coef, ids, counts, routed, grad_weights,    \
+#define CALL(NV, W, L)                                                                          \
+    run_backward<NV, W, L>(logits, T, E, K, renorm, coef, ids, counts, routed, grad_weights,    \
                              grad_loss, grad, stream)
     MOE_ROUTE_CASES(CALL, grad);
 #undef CALL
