@@ -190,10 +190,27 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
 #pragma unroll
     for (int j = 0; j < NV; ++j) acc[j] = 0.0f;
 
-    for (int t = blockIdx.x * kRouteWarps + warp; t < T; t += gridDim.x * kRouteWarps) {
+    // The next token's row is on its way while one is worked on, where a lane
+    // has the registers for it.
+    constexpr bool kAhead = NV <= 8;
+    const int stride = gridDim.x * kRouteWarps;
+    int t = blockIdx.x * kRouteWarps + warp;
+    float ahead[NV];
+    uint8_t open = 1;
+    auto fetch = [&](int u) {
+        if (u >= T) return;
+        load_row<NV, W>(logits + (size_t)u * E, E, lane, ahead);
+        if (mask) open = mask[u];
+    };
+    if constexpr (kAhead) fetch(t);
+    for (; t < T; t += stride) {
+        if constexpr (!kAhead) fetch(t);
         float x[NV];
-        load_row<NV, W>(logits + (size_t)t * E, E, lane, x);
-        if (mask && !mask[t]) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x[j] = ahead[j];
+        const bool masked = !open;
+        if constexpr (kAhead) fetch(t + stride);
+        if (masked) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) x[j] = -INFINITY;
         }
@@ -339,15 +356,14 @@ route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int 
     __shared__ float share_p[1024];
     __shared__ int32_t share_c[1024];
     __shared__ float red[32];
-    __shared__ int total;
     const int groups = blockDim.x / lanes, g = threadIdx.x / lanes, e = threadIdx.x - g * lanes;
-    const int each = ceil_div(clusters, groups);
-    if (threadIdx.x == 0) total = 0;
-    __syncthreads();
+    const int each = ceil_div(clusters, groups), lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
     const size_t row = 2 * (size_t)E + 1;
-    if (threadIdx.x < clusters) atomicAdd(&total, (int)part[threadIdx.x * row + 2 * E]);
+    static_assert(kRouteClusters <= 64);
+    int n = lane < clusters ? (int)part[lane * row + 2 * E] : 0;
+    if (lane + 32 < clusters) n += (int)part[(lane + 32) * row + 2 * E];
     float p = 0.0f;
     int c = 0;
     if (e < E) {
@@ -361,7 +377,7 @@ route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int 
     share_p[threadIdx.x] = p;
     share_c[threadIdx.x] = c;
     __syncthreads();
-    const int n = total;
+    n = __reduce_add_sync(kFullMask, n);
     float v = 0.0f;
     if (threadIdx.x < E) {
         for (int i = 1; i < groups; ++i) {
@@ -372,7 +388,7 @@ route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int 
         v = loss_term(p, c, n, K);
     }
     v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x < 32) {
         v = warp_sum(threadIdx.x < blockDim.x / 32 ? red[threadIdx.x] : 0.0f);
@@ -413,18 +429,34 @@ route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int ren
         const int e = lane * NV + j;
         a[j] = e < E && unit != 0.0f ? unit * (float)counts[e] : 0.0f;
     }
-    for (int t = blockIdx.x * kBackWarps + warp; t < T; t += gridDim.x * kBackWarps) {
-        const L *row = logits + (size_t)t * E;
-        float x[NV];
-        load_row<NV, W>(row, E, lane, x);
-        int id = -1;
-        float dw = 0.0f;
+    const int stride = gridDim.x * kBackWarps;
+    int t = blockIdx.x * kBackWarps + warp, next_id = -1;
+    float ahead[NV], next_dw = 0.0f;
+    auto fetch = [&](int u) {                            // as in route_kernel
+        if (u >= T) return;
+        load_row<NV, W>(logits + (size_t)u * E, E, lane, ahead);
         if (lane < K) {
-            id = ids[(size_t)t * K + lane];
-            if (grad_weights) dw = grad_weights[(size_t)t * K + lane];
+            next_id = ids[(size_t)u * K + lane];
+            if (grad_weights) next_dw = grad_weights[(size_t)u * K + lane];
         }
+    };
+    constexpr bool kAhead = NV <= 8;
+    if constexpr (kAhead) fetch(t);
+    for (; t < T; t += stride) {
+        if constexpr (!kAhead) fetch(t);
+        float x[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x[j] = ahead[j];
+        int id = next_id;
+        float dw = next_dw;
+        if constexpr (kAhead) fetch(t + stride);
         if ((unsigned)id >= (unsigned)E) id = -1;
-        float chosen = id >= 0 ? to_float(row[id]) : -INFINITY;
+        float chosen = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const float v = __shfl_sync(kFullMask, x[j], id / NV & 31);
+            if (id >= 0 && id % NV == j) chosen = v;
+        }
         const bool masked = __ballot_sync(kFullMask, id >= 0) == 0;
         if (masked) {
 #pragma unroll
