@@ -1,0 +1,92 @@
+"""An MoE layer put together from the library's calls, as a serving loop or a
+training step would use them.
+
+``route`` is the router with its gradient (moe_route / moe_route_backward under
+autograd).  ``Int8Experts`` is a gated MLP whose experts' weights are int8 with
+a scale for each output channel:
+
+    moe_layout           slots of the routing
+    moe_dispatch_int8    rows to int8, packed by expert
+    moe_expert_matmul_int8   gate and up projections      [rows, 2 I]
+    silu(gate) * up      (PyTorch)                        [rows, I]
+    moe_dispatch_int8    rows to int8 (K = 1, in place order)
+    moe_expert_matmul_int8   down projection              [rows, H]
+    moe_combine          the routing-weighted sum         [T, H]
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _binding as moe
+
+
+def quantize_channels(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """[E, N, H] weights to int8 codes and fp32 scales [E, N]: each channel's
+    largest magnitude becomes 127.  Done once, when the weights are loaded."""
+    w = w.float()
+    scale = w.abs().amax(dim=2) / 127.0
+    q = torch.round(w / scale.clamp(min=torch.finfo(torch.float32).tiny)[..., None])
+    return q.clamp_(-127, 127).to(torch.int8), scale
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, K, renormalize, loss_coef, token_mask):
+        T, E = logits.shape
+        logits = logits.contiguous()
+        b = moe.RouteBuffers(T, K, E, device=logits.device)
+        b.run(logits, renormalize, loss_coef, token_mask)
+        ctx.buffers, ctx.settings = b, (renormalize, loss_coef)
+        ctx.save_for_backward(logits)
+        ctx.mark_non_differentiable(b.topk_ids, b.expert_counts)
+        return b.topk_ids, b.topk_weights, b.expert_counts, b.loss.view(())
+
+    @staticmethod
+    def backward(ctx, _ids, grad_weights, _counts, grad_loss):
+        (logits,) = ctx.saved_tensors
+        grad = torch.empty_like(logits)
+        ctx.buffers.backward(logits, grad_weights.float().contiguous(),
+                             grad_loss.float().reshape(1).contiguous(), grad, *ctx.settings)
+        return grad, None, None, None, None
+
+
+def route(logits: torch.Tensor, K: int, renormalize: bool = True, loss_coef: float = 1.0,
+          token_mask: torch.Tensor | None = None):
+    """Router logits [T, E] to (topk_ids, topk_weights, expert_counts, loss);
+    topk_weights and loss carry gradients to the logits."""
+    return _Route.apply(logits, K, renormalize, loss_coef, token_mask)
+
+
+class Int8Experts:
+    """The experts of one layer: gate_up [E, 2 I, H] and down [E, H, I]."""
+
+    def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, ranks: int = 1):
+        E, two_i, H = gate_up.shape
+        if down.shape != (E, H, two_i // 2) or two_i % 2:
+            raise ValueError("Int8Experts: gate_up must be [E, 2 I, H] and down [E, H, I]")
+        self.E, self.H, self.I, self.R = E, H, two_i // 2, ranks
+        self.gate_up, self.gate_up_scales = quantize_channels(gate_up)
+        self.down, self.down_scales = quantize_channels(down)
+
+    def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor,
+                 topk_weights: torch.Tensor) -> torch.Tensor:
+        """x [T, H] bf16 and its routing to [T, H] bf16."""
+        (T, H), K, dev = x.shape, topk_ids.shape[1], x.device
+        rows = T * K
+        lay = moe.LayoutBuffers(T, K, self.E, self.R, device=dev).run(topk_ids)
+        codes = torch.empty((rows, H), dtype=torch.int8, device=dev)
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+        moe.moe_dispatch_int8(x, lay.dst_row, codes, scales)
+        mid = torch.empty((rows, 2 * self.I), dtype=torch.bfloat16, device=dev)
+        moe.moe_expert_matmul_int8(codes, scales, self.gate_up, self.gate_up_scales,
+                                   lay.expert_offsets, mid)
+        act = torch.nn.functional.silu(mid[:, :self.I]) * mid[:, self.I:]
+        codes = torch.empty((rows, self.I), dtype=torch.int8, device=dev)
+        same = torch.arange(rows, dtype=torch.int32, device=dev).view(rows, 1)
+        moe.moe_dispatch_int8(act, same, codes, scales)
+        out_rows = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
+        moe.moe_expert_matmul_int8(codes, scales, self.down, self.down_scales,
+                                   lay.expert_offsets, out_rows)
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        moe.moe_combine(out_rows, topk_weights, lay.dst_row, out)
+        return out
