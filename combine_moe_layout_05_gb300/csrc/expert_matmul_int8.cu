@@ -402,6 +402,10 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 }
                 u += S::PARTS;
             }
+            // The storing warps' last arrivals come from the other CTA too and must
+            // find this one's barriers here: it leaves after they are in.
+            for (int v = max(0, u - 2); v < u && ok; ++v)
+                ok = __all_sync(kFullMask, mbar_wait_bounded(empty_d(v & 1), v >> 1 & 1, abort));
             if (!ok) {                                 // what was issued finishes first
                 if (elect_one()) mma_commit<S::CG>(drained);
                 __syncwarp();

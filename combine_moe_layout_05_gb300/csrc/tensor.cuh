@@ -42,6 +42,8 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
 // tensor cores alone, each from its own CTA's memory, and was handed to them
 // by fence.proxy.async or tcgen05.wait before: no cluster-wide release of
 // ordinary writes is asked for (it costs a memory barrier, 0.4 us, each time).
+// A CTA may leave only when every arrival on its barriers has been waited for:
+// one that finds its target gone is a fault.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
