@@ -354,19 +354,31 @@ def moe_combine_fp8(expert_out, expert_scales, topk_weights, dst_row, out,
     _raise("moe_combine_fp8", st)
 
 
+def _fits(t, dtype) -> bool:
+    return t.dtype is dtype and t.is_cuda and t.is_contiguous()
+
+
+def _check_all(pairs) -> None:
+    """The error of the first (name, tensor, dtype) that does not fit."""
+    for name, t, dtype in pairs:
+        _check(name, t, dtype)
+
+
 def moe_dispatch_int8(tokens, dst_row, packed, scales, stream=None) -> None:
     """Pack token rows into their K slots as int8 codes with one scale a row."""
     T, H = tokens.shape
     K = dst_row.shape[1] if dst_row.dim() == 2 else 1
-    _check("tokens", tokens, torch.bfloat16)
-    _check("dst_row", dst_row, torch.int32)
-    _check("packed", packed, torch.int8)
-    _check("scales", scales, torch.float32)
-    if dst_row.numel() != T * K or packed.numel() < T * K * H or scales.numel() < T * K:
+    if not (_fits(tokens, torch.bfloat16) and _fits(dst_row, torch.int32)
+            and _fits(packed, torch.int8) and _fits(scales, torch.float32)):
+        _check_all((("tokens", tokens, torch.bfloat16), ("dst_row", dst_row, torch.int32),
+                    ("packed", packed, torch.int8), ("scales", scales, torch.float32)))
+    rows = T * K
+    if dst_row.numel() != rows or packed.numel() < rows * H or scales.numel() < rows:
         raise ValueError("moe_dispatch_int8: dst_row/packed/scales have the wrong size")
-    st = load().moe_dispatch_int8(_ptr(tokens), T, H, K, _ptr(dst_row), _ptr(packed),
-                                  _ptr(scales), _stream(stream))
-    _raise("moe_dispatch_int8", st)
+    st = load().moe_dispatch_int8(tokens.data_ptr(), T, H, K, dst_row.data_ptr(),
+                                  packed.data_ptr(), scales.data_ptr(), _stream(stream))
+    if st:
+        _raise("moe_dispatch_int8", st)
 
 
 def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
@@ -374,21 +386,22 @@ def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
     """Packed int8 rows times their experts' int8 weights (see include/moe_layout.h)."""
     rows, H = x.shape
     E, N = weights.shape[0], weights.shape[1]
-    _check("x", x, torch.int8)
-    _check("x_scales", x_scales, torch.float32)
-    _check("weights", weights, torch.int8)
-    _check("w_scales", w_scales, torch.float32)
-    _check("expert_offsets", expert_offsets, torch.int32)
-    _check("out", out, torch.bfloat16)
+    if not (_fits(x, torch.int8) and _fits(x_scales, torch.float32) and _fits(weights, torch.int8)
+            and _fits(w_scales, torch.float32) and _fits(expert_offsets, torch.int32)
+            and _fits(out, torch.bfloat16)):
+        _check_all((("x", x, torch.int8), ("x_scales", x_scales, torch.float32),
+                    ("weights", weights, torch.int8), ("w_scales", w_scales, torch.float32),
+                    ("expert_offsets", expert_offsets, torch.int32), ("out", out, torch.bfloat16)))
     _check("dev_error", dev_error, torch.int32)
     if weights.dim() != 3 or weights.shape[2] != H or w_scales.numel() != E * N \
             or x_scales.numel() < rows or expert_offsets.numel() < E + 1 \
             or out.numel() < rows * N or out.shape[-1] != N:
         raise ValueError("moe_expert_matmul_int8: argument sizes disagree")
-    st = load().moe_expert_matmul_int8(_ptr(x), _ptr(x_scales), _ptr(weights), _ptr(w_scales),
-                                       _ptr(expert_offsets), rows, H, N, E, _ptr(out),
-                                       _ptr(dev_error), _stream(stream))
-    _raise("moe_expert_matmul_int8", st)
+    st = load().moe_expert_matmul_int8(x.data_ptr(), x_scales.data_ptr(), weights.data_ptr(),
+                                       w_scales.data_ptr(), expert_offsets.data_ptr(), rows, H, N,
+                                       E, out.data_ptr(), _ptr(dev_error), _stream(stream))
+    if st:
+        _raise("moe_expert_matmul_int8", st)
 
 
 def moe_route_workspace_bytes(T: int, E: int) -> int:
@@ -396,9 +409,11 @@ def moe_route_workspace_bytes(T: int, E: int) -> int:
 
 
 def _logits_type(fn: str, logits) -> int:
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    if logits.dtype is torch.float32:
+        return 0
+    if logits.dtype is not torch.bfloat16:
         raise TypeError(f"{fn}: logits must be float32 or bfloat16, got {logits.dtype}")
-    return int(logits.dtype == torch.bfloat16)
+    return 1
 
 
 def moe_route(logits, topk_ids, topk_weights, expert_counts, routed_tokens, loss,
@@ -409,12 +424,13 @@ def moe_route(logits, topk_ids, topk_weights, expert_counts, routed_tokens, loss
     T, E = logits.shape
     K = topk_ids.shape[1]
     bf16 = _logits_type("moe_route", logits)
-    _check("logits", logits, logits.dtype)
-    _check("topk_ids", topk_ids, torch.int32)
-    _check("topk_weights", topk_weights, torch.float32)
-    _check("expert_counts", expert_counts, torch.int32)
-    _check("routed_tokens", routed_tokens, torch.int32)
-    _check("loss", loss, torch.float32)
+    if not (logits.is_cuda and logits.is_contiguous() and _fits(topk_ids, torch.int32)
+            and _fits(topk_weights, torch.float32) and _fits(expert_counts, torch.int32)
+            and _fits(routed_tokens, torch.int32) and _fits(loss, torch.float32)):
+        _check_all((("logits", logits, logits.dtype), ("topk_ids", topk_ids, torch.int32),
+                    ("topk_weights", topk_weights, torch.float32),
+                    ("expert_counts", expert_counts, torch.int32),
+                    ("routed_tokens", routed_tokens, torch.int32), ("loss", loss, torch.float32)))
     if token_mask is not None:
         _check("token_mask", token_mask, torch.bool)
         if token_mask.numel() != T:
@@ -422,12 +438,13 @@ def moe_route(logits, topk_ids, topk_weights, expert_counts, routed_tokens, loss
     if topk_ids.numel() != T * K or topk_weights.numel() != T * K or expert_counts.numel() < E \
             or routed_tokens.numel() < 1 or loss.numel() < 1:
         raise ValueError("moe_route: output arrays have the wrong size")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = load().moe_route(_ptr(logits), bf16, T, E, K, int(bool(renormalize)), float(loss_coef),
-                          _ptr(token_mask), _ptr(topk_ids), _ptr(topk_weights),
-                          _ptr(expert_counts), _ptr(routed_tokens), _ptr(loss),
-                          _ptr(workspace), ws_bytes, _stream(stream))
-    _raise("moe_route", st)
+    st = load().moe_route(logits.data_ptr(), bf16, T, E, K, 1 if renormalize else 0, loss_coef,
+                          _ptr(token_mask), topk_ids.data_ptr(), topk_weights.data_ptr(),
+                          expert_counts.data_ptr(), routed_tokens.data_ptr(), loss.data_ptr(),
+                          _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+                          _stream(stream))
+    if st:
+        _raise("moe_route", st)
 
 
 def moe_route_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weights, grad_loss,
@@ -438,11 +455,13 @@ def moe_route_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weig
     T, E = logits.shape
     K = topk_ids.shape[1]
     bf16 = _logits_type("moe_route_backward", logits)
-    _check("logits", logits, logits.dtype)
-    _check("grad_logits", grad_logits, logits.dtype)
-    _check("topk_ids", topk_ids, torch.int32)
-    _check("expert_counts", expert_counts, torch.int32)
-    _check("routed_tokens", routed_tokens, torch.int32)
+    if not (logits.is_cuda and logits.is_contiguous() and _fits(grad_logits, logits.dtype)
+            and _fits(topk_ids, torch.int32) and _fits(expert_counts, torch.int32)
+            and _fits(routed_tokens, torch.int32)):
+        _check_all((("logits", logits, logits.dtype), ("grad_logits", grad_logits, logits.dtype),
+                    ("topk_ids", topk_ids, torch.int32),
+                    ("expert_counts", expert_counts, torch.int32),
+                    ("routed_tokens", routed_tokens, torch.int32)))
     _check("grad_weights", grad_weights, torch.float32)
     _check("grad_loss", grad_loss, torch.float32)
     if topk_ids.numel() != T * K or expert_counts.numel() < E or routed_tokens.numel() < 1 \
@@ -450,11 +469,12 @@ def moe_route_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weig
             or (grad_weights is not None and grad_weights.numel() != T * K) \
             or (grad_loss is not None and grad_loss.numel() != 1):
         raise ValueError("moe_route_backward: argument sizes disagree")
-    st = load().moe_route_backward(_ptr(logits), bf16, T, E, K, int(bool(renormalize)),
-                                   float(loss_coef), _ptr(topk_ids), _ptr(expert_counts),
-                                   _ptr(routed_tokens), _ptr(grad_weights), _ptr(grad_loss),
-                                   _ptr(grad_logits), _stream(stream))
-    _raise("moe_route_backward", st)
+    st = load().moe_route_backward(logits.data_ptr(), bf16, T, E, K, 1 if renormalize else 0,
+                                   loss_coef, topk_ids.data_ptr(), expert_counts.data_ptr(),
+                                   routed_tokens.data_ptr(), _ptr(grad_weights), _ptr(grad_loss),
+                                   grad_logits.data_ptr(), _stream(stream))
+    if st:
+        _raise("moe_route_backward", st)
 
 
 class RouteBuffers:

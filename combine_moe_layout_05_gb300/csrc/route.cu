@@ -143,11 +143,9 @@ __device__ __forceinline__ float weight_of(float x, float m)
     return x == -INFINITY ? 0.0f : exp2_approx((x - m) * kLog2e);
 }
 
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr)
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v)
 {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
 }
 
 // The call's last sums, thread e for expert e: p and c are expert e's totals.
@@ -174,11 +172,13 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
 {
     const int K = KT > 0 ? KT : any_k;
     extern __shared__ float sm[];
-    float *const sums = sm;                              // [kRouteWarps][E], then [E]
+    float *const sums = sm;                              // [kRouteWarps][E]
     int32_t *const cnt = reinterpret_cast<int32_t *>(sm + (size_t)kRouteWarps * E);     // [E] and the routed tokens
+    uint32_t *const inbox = reinterpret_cast<uint32_t *>(cnt + E + 1);  // [blocks][2 share + 1], see below
     __shared__ float warp_terms[kRouteWarps];
     __shared__ float terms[kSingleCluster];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     for (int e = threadIdx.x; e <= E; e += kRouteThreads) cnt[e] = 0;
     pdl_wait();
     pdl_trigger();
@@ -292,28 +292,33 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         if (lane * NV + j < E) sums[warp * E + lane * NV + j] = acc[j];
+    // Expert e is added up by block e % blocks of the cluster: every block puts
+    // its sums, its counts and its routed tokens in that block's inbox.
+    const int rank = (int)cluster_rank(), blocks = SINGLE ? (int)gridDim.x : kRouteCluster;
+    const int share = ceil_div(E, blocks), box = 2 * share + 1;
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");      // the others have started
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kRouteThreads) {
         float v = sums[e];
 #pragma unroll
         for (int w = 1; w < kRouteWarps; ++w) v += sums[w * E + e];
-        sums[e] = v;
+        const uint32_t to = cluster_addr(smem_addr(inbox + rank * box + e / blocks), e % blocks);
+        st_cluster(to, __float_as_uint(v));
+        st_cluster(to + 4 * share, (uint32_t)cnt[e]);
     }
-    const uint32_t rank = cluster_rank();
-    const int blocks = SINGLE ? (int)gridDim.x : kRouteCluster;
+    if (threadIdx.x < blocks) st_cluster(cluster_addr(smem_addr(inbox + rank * box + 2 * share), threadIdx.x), (uint32_t)cnt[E]);
     cluster_sync_all();
-
-    // experts rank, rank + blocks, ... are this block's to add up
-    const uint32_t sums_at = smem_addr(sums), cnt_at = smem_addr(cnt);
     int n = 0;
-    for (int b = 0; b < blocks; ++b) n += (int)ld_cluster(cluster_addr(cnt_at + 4 * E, b));
+    for (int b = 0; b < blocks; ++b) n += (int)inbox[b * box + 2 * share];
     float term = 0.0f;
-    for (int e = threadIdx.x * blocks + rank; e < E; e += kRouteThreads * blocks) {
+    for (int i = threadIdx.x; i < share; i += kRouteThreads) {
+        const int e = i * blocks + rank;
+        if (e >= E) break;
         float v = 0.0f;
         int c = 0;
         for (int b = 0; b < blocks; ++b) {
-            v += __uint_as_float(ld_cluster(cluster_addr(sums_at + 4 * e, b)));
-            c += (int)ld_cluster(cluster_addr(cnt_at + 4 * e, b));
+            v += __uint_as_float(inbox[b * box + i]);
+            c += (int)inbox[b * box + share + i];
         }
         if constexpr (SINGLE) {
             o.counts[e] = c;
@@ -331,8 +336,7 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
         if (threadIdx.x == 0) {
             float v = 0.0f;
             for (int w = 0; w < kRouteWarps; ++w) v += warp_terms[w];
-            const uint32_t to = cluster_addr(smem_addr(&terms[rank]), 0);
-            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(to), "f"(v) : "memory");
+            st_cluster(cluster_addr(smem_addr(&terms[rank]), 0), __float_as_uint(v));
         }
         cluster_sync_all();
         if (rank == 0 && threadIdx.x == 0) {
@@ -341,9 +345,8 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
             *o.loss = o.coef * (float)E * v;
             *o.routed = n;
         }
-    } else {
-        if (rank == 0 && threadIdx.x == 0) part[(size_t)(blockIdx.x / kRouteCluster) * (2 * E + 1) + 2 * E] = (uint32_t)n;
-        cluster_sync_all();                              // the others have read this block's memory
+    } else if (rank == 0 && threadIdx.x == 0) {
+        part[(size_t)(blockIdx.x / kRouteCluster) * (2 * E + 1) + 2 * E] = (uint32_t)n;
     }
 }
 
@@ -368,10 +371,18 @@ route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int 
     int c = 0;
     if (e < E) {
         const int last = min(clusters, (g + 1) * each);
-#pragma unroll 10
-        for (int b = g * each; b < last; ++b) {
-            p += __uint_as_float(part[b * row + e]);
-            c += (int)part[b * row + E + e];
+        for (int b0 = g * each; b0 < last; b0 += 8) {
+            uint32_t vp[8], vc[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                vp[j] = b0 + j < last ? part[(b0 + j) * row + e] : 0u;
+                vc[j] = b0 + j < last ? part[(b0 + j) * row + E + e] : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                p += __uint_as_float(vp[j]);
+                c += (int)vc[j];
+            }
         }
     }
     share_p[threadIdx.x] = p;
@@ -531,7 +542,8 @@ cudaError_t run_forward(const void *logits, int T, int E, int K, int renorm, flo
                         const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts,
                         int32_t *routed, float *loss, void *workspace, cudaStream_t s)
 {
-    const size_t smem = ((size_t)(kRouteWarps + 1) * E + 1) * 4;
+    // sums, counts, and an inbox of at most E + kSingleCluster experts' pairs
+    const size_t smem = ((size_t)(kRouteWarps + 1) * E + 1 + 2 * (E + kSingleCluster) + kSingleCluster) * 4;
     const RouteOut o{counts, routed, loss, coef};
     const int single = single_blocks(T);
     auto *const kernel = K == 8 ? single ? route_kernel<NV, W, 8, true, L> : route_kernel<NV, W, 8, false, L>
