@@ -58,9 +58,13 @@ struct Shape {
     static constexpr int UNIT = NT / PARTS;            // TMEM columns of an accumulator
     static constexpr int ACOL0 = 2 * UNIT, ACOL = KS / 2;   // and of the widened weights
     static_assert(ACOL0 + NC * ACOL <= kTmemColumns && BURST <= NC);
-    // a barrier's parity tells a use from the one before, not from the one
-    // before that: no group may be two rounds of its ring ahead
-    static_assert(GA * PER <= NC && GB * PER <= NC && GA <= N8 && GB <= N8);
+    // A barrier's parity tells a use from the one before, not from the one
+    // before that, so a group that waits for a use has to know that the one
+    // before is over.  Widened slots are consumed in order, and a group has
+    // waited for the last but one round of its own.  Byte slots may land out
+    // of order: there a slot belongs to the same group in every round, which
+    // has then worked on its last use itself.
+    static_assert(GA * PER <= NC && GB * PER <= NC && N8 % GA == 0 && N8 % GB == 0);
     // warps: 0 copies, 1 issues, then those that widen and those that store;
     // the TMEM lanes a warp reaches are those of its number modulo 4
     static constexpr int WB = 4;                       // warps of a group that widens rows
@@ -555,8 +559,9 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 for (int h = 0; h < S::PER; ++h) {
                     if (!ok || k * S::PER + h >= slots) break;
                     const int m = m0 + k * S::PER + h, c = m % S::NC;
-                    // pieces a warp, rounded up to 1, 2 or 4: the rows past the tile's
-                    // are in the slot's memory, and no instruction reads them
+                    // pieces a warp, rounded up: the rows past the tile's are in the
+                    // slot's memory (with two halves there are none: blocks is even),
+                    // and no instruction reads them
                     auto widen = [&](auto pieces) {
                         constexpr int U = decltype(pieces)::value;
                         uint32_t v[U][8];
@@ -581,6 +586,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                     const int pieces = ceil_div(blocks * (S::KS / 64), S::WB);
                     if (pieces == 1) widen(std::integral_constant<int, 1>());
                     else if (kMost <= 2 || pieces == 2) widen(std::integral_constant<int, 2>());
+                    else if (pieces == 3) widen(std::integral_constant<int, kMost <= 2 ? 2 : 3>());
                     else widen(std::integral_constant<int, kMost <= 2 ? 2 : 4>());
                     if (!ok) break;
                     fence_async_shared();
