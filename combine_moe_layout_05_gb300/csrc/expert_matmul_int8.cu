@@ -46,8 +46,11 @@ constexpr int kTmemColumns = 512;
 // GA, GB: groups of warps that widen the weights and the rows; a group takes
 // every GA-th (GB-th) step, since one step's latency (barrier, loads, stores
 // and their wait) is several times its issue slots.
-template <int CG_, int NT_, int PARTS_, int KS_, int N8_, int NC_, int GA_, int GB_>
+// SPLIT: a cluster's CTAs each sum a share of the contraction.
+template <int CG_, int NT_, int PARTS_, int KS_, int N8_, int NC_, int GA_, int GB_, bool SPLIT_ = false>
 struct Shape {
+    static constexpr bool SPLIT = SPLIT_;
+    static_assert(!SPLIT || (CG_ == 1 && PARTS_ == 1 && KS_ == kStep));
     static constexpr int CG = CG_, NT = NT_, PARTS = PARTS_, KS = KS_, N8 = N8_, NC = NC_, GA = GA_, GB = GB_;
     static constexpr int BR = NT / CG;                 // rows a CTA widens at most
     static constexpr int QUANTUM = 16 * CG;            // rows of a part are a multiple of
@@ -71,18 +74,21 @@ struct Shape {
     static_assert(BR * (KS / 64) <= 8 * WB * 4);
     static constexpr int A0 = 4, E0 = A0 + 4 * GA, B0 = E0 + 4, WARPS = B0 + WB * GB;
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int BARS = 2 * N8 + 2 * NC + 4 + 1;
+    static constexpr int BARS = 2 * N8 + 2 * NC + 4 + 1 + SPLIT;
     // ring, widened rows, 16 x 32 outputs and the row scales of each storing
     // warp, barriers, flags, expert table
     static constexpr int OFF16 = N8 * SLOT8;
     static constexpr int OFFTURN = OFF16 + NC * B16;
-    static constexpr int OFFS = OFFTURN + 4 * 1024;
+    static constexpr int OFFBOX = OFFTURN + 4 * 1024;  // SPLIT: the other CTAs' sums, NT x 128 fp32
+    static constexpr int OFFS = OFFBOX + SPLIT * NT * kChannels * 4;
     static constexpr int OFFBAR = OFFS + 4 * NT * 4;
     static constexpr int OFFTAB = OFFBAR + (BARS * 8 + 15) / 16 * 16 + 32;
     static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4 + 1024; }
 };
 using Wide = Shape<2, 256, 2, 64, 4, 4, 2, 2>;
+using Mid = Shape<2, 128, 1, 128, 6, 4, 2, 2>;
 using Narrow = Shape<1, 32, 1, 128, 8, 6, 4, 2>;
+using Split = Shape<1, 32, 1, 128, 4, 6, 4, 2, true>;
 
 // Copies of rows come in these heights; a tile takes the one that covers its
 // share (an instruction of the copy engine costs its issuing thread 150 to 200
@@ -186,8 +192,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
 expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x,
                           const float *__restrict__ x_scales, const float *__restrict__ w_scales,
                           const int32_t *__restrict__ offsets, int rows, int H, int N, int E,
-                          int least, int most, int second, __nv_bfloat16 *__restrict__ out,
-                          uint32_t *__restrict__ dev_error)
+                          __nv_bfloat16 *__restrict__ out, uint32_t *__restrict__ dev_error)
 {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
@@ -202,7 +207,9 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     auto empty16 = [&](int i) { return bar0 + 8 * (2 * S::N8 + S::NC + i); };
     auto full_d = [&](int i) { return bar0 + 8 * (2 * S::N8 + 2 * S::NC + i); };
     auto empty_d = [&](int i) { return bar0 + 8 * (2 * S::N8 + 2 * S::NC + 2 + i); };
-    const uint32_t drained = bar0 + 8 * (S::BARS - 1);
+    const uint32_t drained = bar0 + 8 * (2 * S::N8 + 2 * S::NC + 4), box_full = drained + 8;
+    // SPLIT: which share of the contraction is this CTA's, of how many
+    const int parts = S::SPLIT ? cluster_size() : 1, part = S::SPLIT ? (int)uniform(cluster_rank()) : 0;
     uint32_t *const flags = reinterpret_cast<uint32_t *>(generic + S::OFFBAR + (S::BARS * 8 + 15) / 16 * 16);
     volatile int *const abort = reinterpret_cast<volatile int *>(flags + 1);
     int *const first_row = reinterpret_cast<int *>(generic + S::OFFTAB);
@@ -218,17 +225,15 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         b += 2 * S::NC;
         for (int i = 0; i < 2; ++i) mbar_init(b + i, 1), mbar_init(b + 2 + i, 4 * S::CG);
         mbar_init(b + 4, 1);
+        if (S::SPLIT) mbar_init(b + 5, 4 * parts);
         *abort = 0;
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc<S::CG>(smem_addr(flags), kTmemColumns);
-    // The second of two launches starts as the first one's blocks leave: its
-    // inputs were there when the first one started, and it writes other rows.
-    if (!second) pdl_wait();
+    pdl_wait();
     pdl_trigger();
 
-    // Tiles an expert (none where its rows are not in [least, most]), then
-    // their running sum: thread t has experts 2t, 2t + 1.
+    // Tiles an expert, then their running sum: thread t has experts 2t, 2t + 1.
     {
         static_assert(2 * S::THREADS > MOE_MAX_EXPERTS);
         __shared__ int warp_tiles[S::WARPS];
@@ -240,10 +245,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
             if (e <= E) {
                 const int lo = max(0, min(rows, offsets[e]));
                 first_row[e] = lo;
-                if (e < E) {
-                    const int m = max(0, min(rows, offsets[e + 1])) - lo;
-                    if (m >= least && m <= most) tiles[j] = ceil_div(m, S::NT);
-                }
+                if (e < E) tiles[j] = ceil_div(max(0, min(rows, offsets[e + 1]) - lo), S::NT);
             }
         }
         int sum = tiles[0] + tiles[1];
@@ -261,18 +263,20 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         if (2 * tid <= E) first_tile[2 * tid] = before;
         if (2 * tid + 1 <= E) first_tile[2 * tid + 1] = before + tiles[0];
     }
-    if (dev_error && !second && blockIdx.x == 0 && tid == 0) *dev_error = 0;
+    if (dev_error && blockIdx.x == 0 && tid == 0) *dev_error = 0;
     __syncthreads();
-    if constexpr (S::CG == 2) cluster_sync_all();
+    if constexpr (S::CG == 2 || S::SPLIT) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = uniform(flags[0]);
 
     const Table table{first_row, first_tile};
     const int channel_tiles = ceil_div(N, kChannels * S::CG);
     const int items = uniform(first_tile[E]) * channel_tiles;
-    const int steps = ceil_div(H, kStep), slots = ceil_div(H, S::KS);
+    const int all_steps = ceil_div(H, kStep), step0 = all_steps * part / parts;
+    const int steps = all_steps * (part + 1) / parts - step0;
+    const int slots = S::SPLIT ? steps : ceil_div(H, S::KS), h0 = step0 * kStep;
     uint64_t *const bars = reinterpret_cast<uint64_t *>(generic + S::OFFBAR);
-    const int group = blockIdx.x / S::CG, groups = gridDim.x / S::CG;
+    const int group = blockIdx.x / (S::CG * parts), groups = gridDim.x / (S::CG * parts);
 
     if (warp == 0) {
         int issued = 0;
@@ -291,8 +295,8 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 const uint32_t slot = base + s * S::SLOT8;
                 if (elect_one()) {
                     mbar_arrive_expect(bars + s, bytes);
-                    tile_load_2d(slot, &map_w, k * kStep, wr, full8(s));
-                    tile_load_2d(slot + S::A8, &map_x.box[m], k * kStep, xr, full8(s));
+                    tile_load_2d(slot, &map_w, h0 + k * kStep, wr, full8(s));
+                    tile_load_2d(slot + S::A8, &map_x.box[m], h0 + k * kStep, xr, full8(s));
                 }
                 __syncwarp();
             }
@@ -306,7 +310,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
             int u = 0;                                 // accumulators used so far
             const uint64_t b_first = operand_desc(base + S::OFF16);
             constexpr int kFull = S::KS / 16;          // instructions a slot
-            const int last = (H - (slots - 1) * S::KS) >> 4;     // and in the last one
+            const int last = min(kFull, (H - h0 - (slots - 1) * S::KS) >> 4);        // and in the last one
             bool ok = true;
             auto wait_free = [&](int v) {
                 ok = __all_sync(kFullMask, mbar_wait_bounded(empty_d(v & 1), (v >> 1 & 1) ^ 1, abort));
@@ -438,13 +442,50 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
 #pragma unroll
             for (int j = 0; j < S::NT / 32; ++j) row_scale[j * 32 + lane] = xs[j];
             __syncwarp();
-            const bool vectors = N % 8 == 0 && ch0 + 32 <= N;
+            const bool vectors = N % 8 == 0;
             for (int p = 0; p < S::PARTS && ok; ++p, ++u) {
                 const int d = u & 1, n = t.n[p], mine = n / S::CG;
                 ok = __all_sync(kFullMask, mbar_wait_bounded(full_d(d), u >> 1 & 1, abort));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + d * S::UNIT + ((uint32_t)quarter << 21);
+                if constexpr (S::SPLIT) {
+                    // Row c is added up by CTA c % parts: its sums go to that
+                    // CTA's box, [part][row / parts][128 channels].  A cluster
+                    // has one tile at most, so a box is written once.
+                    const int each = n / parts;
+                    for (int c0 = 0; c0 < n; c0 += 16) {
+                        uint32_t v[16];
+                        tmem_load_16x16(acc + c0, v);
+                        tmem_load_16x16(acc + c0 + (16u << 16), v + 8);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int c = c0 + 8 * (j >> 2 & 1) + 2 * (lane & 3) + (j & 1);
+                            const int ch = quarter * 32 + 16 * (j >> 3) + 8 * (j >> 1 & 1) + (lane >> 2);
+                            st_cluster_u32(cluster_addr(base + S::OFFBOX + ((part * each + c / parts) * kChannels + ch) * 4,
+                                                        c % parts), v[j]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars + 2 * S::N8 + 2 * S::NC + 2 + d);
+                    if (lane < parts) mbar_arrive_release(cluster_addr(box_full, lane));
+                    __syncwarp();
+                    ok = __all_sync(kFullMask, mbar_wait_bounded(box_full, 0, abort));
+                    if (!ok) break;
+                    const int ch = ch0 + lane;
+                    const float scale = ch < N ? w_scales[(size_t)t.e * N + ch] : 0.0f;
+                    const float *box = reinterpret_cast<const float *>(generic + S::OFFBOX) + quarter * 32 + lane;
+                    for (int i = 0; i < each; ++i) {
+                        const int c = i * parts + part;
+                        float sum = 0.0f;
+                        for (int q = 0; q < parts; ++q) sum += box[(q * each + i) * kChannels];
+                        if (c < t.valid && ch < N)
+                            out[(size_t)(t.row + c) * N + ch] = __float2bfloat16_rn(sum * row_scale[c] * scale);
+                    }
+                    continue;
+                }
                 uint32_t next[16];
                 if (n > 0) {
                     tmem_load_16x16(acc, next);
@@ -482,17 +523,16 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                         for (int j = 0; j < 2; ++j) {
                             const int r = 8 * j + (lane >> 2);
                             const uint4 q = lds128(turned + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4));
-                            if (r0 + r < t.valid)
+                            if (r0 + r < t.valid && ch0 + (lane & 3) * 8 < N)
                                 st_v4(out + (size_t)(t.row + r0 + r) * N + ch0 + (lane & 3) * 8, q);
                         }
                     } else if (ch0 + lane < N) {
+                        const __nv_bfloat16 *y = reinterpret_cast<const __nv_bfloat16 *>(generic + (turned - base));
+                        __nv_bfloat16 *o = out + (size_t)(t.row + r0) * N + ch0 + lane;
                         const int rows_left = min(16, t.valid - r0);
-                        for (int r = 0; r < rows_left; ++r) {
-                            uint16_t q;
-                            asm volatile("ld.shared.u16 %0, [%1];"
-                                         : "=h"(q) : "r"(turned + r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4) + (lane & 7) * 2));
-                            out[(size_t)(t.row + r0 + r) * N + ch0 + lane] = __ushort_as_bfloat16(q);
-                        }
+#pragma unroll 1
+                        for (int r = 0; r < rows_left; ++r, o += N)
+                            *o = y[r * 32 + (((lane >> 3) ^ (r >> 1 & 3)) << 3) + (lane & 7)];
                     }
                     __syncwarp();
                 }
@@ -601,11 +641,10 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if constexpr (S::CG == 2) cluster_sync_all();      // the peer is done with this CTA's memory
+    if constexpr (S::CG == 2 || S::SPLIT) cluster_sync_all();      // the peer is done with this CTA's memory
     tc_fence_after();
     if (tid == 0 && *abort && dev_error) atomicOr(dev_error, MOE_DEV_ERR_TIMEOUT);
     if (warp == 1) tmem_free<S::CG>(tmem, kTmemColumns);
-    if (second) pdl_wait();                            // what follows waits for both launches
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -638,10 +677,17 @@ bool byte_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t H, uint32
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tiles there can be at most: every expert's last one may be short.
+template <typename S>
+int64_t most_tiles(int rows, int N, int E)
+{
+    return ((int64_t)(rows < E ? rows : E) + rows / S::NT) * ceil_div(N, kChannels * S::CG);
+}
+
 template <typename S>
 cudaError_t run(const void *x, const float *x_scales, const void *w, const float *w_scales,
-                const int32_t *offsets, int rows, int H, int N, int E, int least, int most, int second,
-                void *out, uint32_t *dev_error, cudaStream_t stream)
+                const int32_t *offsets, int rows, int H, int N, int E, int parts, void *out,
+                uint32_t *dev_error, cudaStream_t stream)
 {
     CUtensorMap map_w;
     RowMaps map_x;
@@ -654,12 +700,46 @@ cudaError_t run(const void *x, const float *x_scales, const void *w, const float
     int sms = 0;
     e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    // tiles there can be at most: every expert's last one may be short
-    const int64_t tiles = ((int64_t)(rows < E ? rows : E) + rows / S::NT) * ceil_div(N, kChannels * S::CG);
-    const int64_t groups = tiles < sms / S::CG ? tiles : sms / S::CG;
-    return launch_pdl_clusters(expert_matmul_int8_kernel<S>, dim3((unsigned)groups * S::CG), dim3(S::THREADS), smem,
-                               stream, S::CG, map_w, map_x, x_scales, w_scales, offsets, rows, H, N, E,
-                               least, most, second, static_cast<__nv_bfloat16 *>(out), dev_error);
+    const int64_t tiles = most_tiles<S>(rows, N, E);
+    const int64_t groups = tiles < sms / (S::CG * parts) ? tiles : sms / (S::CG * parts);
+    return launch_pdl_clusters(expert_matmul_int8_kernel<S>, dim3((unsigned)groups * S::CG * parts), dim3(S::THREADS),
+                               smem, stream, S::CG * parts, map_w, map_x, x_scales, w_scales, offsets, rows, H, N, E,
+                               static_cast<__nv_bfloat16 *>(out), dev_error);
+}
+
+// Clusters of p (2, 4 or 8) splitting CTAs that the current device runs at a
+// time, looked up once for each device.
+cudaError_t split_clusters(int p, int *clusters)
+{
+    constexpr int kMaxDevices = 64;
+    static std::mutex mu;
+    static int known[kMaxDevices][3];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const std::lock_guard<std::mutex> lock(mu);
+    int &n = known[dev][p / 4];
+    if (n == 0) {
+        auto *const kernel = &expert_matmul_int8_kernel<Split>;
+        const size_t smem = Split::bytes(MOE_MAX_EXPERTS);
+        e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(p);
+        cfg.blockDim = dim3(Split::THREADS);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = p;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    *clusters = n;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -669,21 +749,24 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
                                       int H, int N, int E, void *out, uint32_t *dev_error,
                                       cudaStream_t stream)
 {
-    auto go = [&](auto shape, int least, int most, int second) {
-        return run<decltype(shape)>(x, x_scales, w, w_scales, offsets, rows, H, N, E, least, most, second, out,
-                                    dev_error, stream);
+    auto go = [&](auto shape, int parts) {
+        return run<decltype(shape)>(x, x_scales, w, w_scales, offsets, rows, H, N, E, parts, out, dev_error, stream);
     };
-    // Few rows an expert: the weights' bytes are the work, and the narrow form
-    // moves them at 6.8 TB/s where the wide one reaches 5.2 (decode, 256 experts
-    // of 2048 x 7168: 547 and 723 us).  Many: the wide form alone (1.4 ms at 1024
-    // rows an expert, against 1.6 PFLOP/s).  Between them each expert goes by
-    // its own rows, in two launches (16384 skewed rows over 384 experts: 1257 us;
-    // wide alone 1450, narrow alone 2560).
-    constexpr int kLight = Narrow::NT;
-    if (rows <= 16 * E) return go(Narrow{}, 1, INT32_MAX, 0);
-    if (rows >= 512 * E) return go(Wide{}, 1, INT32_MAX, 0);
-    const cudaError_t e = go(Wide{}, kLight + 1, INT32_MAX, 0);
-    return e != cudaSuccess ? e : go(Narrow{}, 1, kLight, 1);
+    int sms = 0;
+    cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = most_tiles<Split>(rows, N, E);
+    const int steps = ceil_div(H, kStep);
+    int parts = 1;
+    for (int p = 2; p <= 8 && tiles * p <= sms && steps >= 16 && steps >= 4 * p; p *= 2) {
+        int clusters = 0;
+        e = split_clusters(p, &clusters);
+        if (e != cudaSuccess) return e;
+        if (tiles <= clusters) parts = p;
+    }
+    if (parts > 1) return go(Split{}, parts);
+    if (rows <= 16 * E) return go(Narrow{}, 1);
+    return rows >= 512 * E ? go(Wide{}, 1) : go(Mid{}, 1);
 }
 
 }  // namespace moe

@@ -143,11 +143,6 @@ __device__ __forceinline__ float weight_of(float x, float m)
     return x == -INFINITY ? 0.0f : exp2_approx((x - m) * kLog2e);
 }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v)
-{
-    asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
-}
-
 // The call's last sums, thread e for expert e: p and c are expert e's totals.
 __device__ __forceinline__ float loss_term(float p, int c, int n, int K)
 {
@@ -303,10 +298,10 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
 #pragma unroll
         for (int w = 1; w < kRouteWarps; ++w) v += sums[w * E + e];
         const uint32_t to = cluster_addr(smem_addr(inbox + rank * box + e / blocks), e % blocks);
-        st_cluster(to, __float_as_uint(v));
-        st_cluster(to + 4 * share, (uint32_t)cnt[e]);
+        st_cluster_u32(to, __float_as_uint(v));
+        st_cluster_u32(to + 4 * share, (uint32_t)cnt[e]);
     }
-    if (threadIdx.x < blocks) st_cluster(cluster_addr(smem_addr(inbox + rank * box + 2 * share), threadIdx.x), (uint32_t)cnt[E]);
+    if (threadIdx.x < blocks) st_cluster_u32(cluster_addr(smem_addr(inbox + rank * box + 2 * share), threadIdx.x), (uint32_t)cnt[E]);
     cluster_sync_all();
     int n = 0;
     for (int b = 0; b < blocks; ++b) n += (int)inbox[b * box + 2 * share];
@@ -336,7 +331,7 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
         if (threadIdx.x == 0) {
             float v = 0.0f;
             for (int w = 0; w < kRouteWarps; ++w) v += warp_terms[w];
-            st_cluster(cluster_addr(smem_addr(&terms[rank]), 0), __float_as_uint(v));
+            st_cluster_u32(cluster_addr(smem_addr(&terms[rank]), 0), __float_as_uint(v));
         }
         cluster_sync_all();
         if (rank == 0 && threadIdx.x == 0) {

@@ -24,6 +24,13 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+__device__ __forceinline__ int cluster_size()
+{
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return (int)n;
+}
+
 // Every thread of the cluster; orders shared memory of both CTAs.
 __device__ __forceinline__ void cluster_sync_all()
 {
@@ -36,6 +43,19 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
+}
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_at, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(cluster_at), "r"(v) : "memory");
+}
+
+// One arrival on a barrier of the cluster, after this warp's earlier writes to
+// the cluster's shared memory (synchronise the warp first).
+__device__ __forceinline__ void mbar_arrive_release(uint32_t cluster_bar)
+{
+    asm volatile("fence.acq_rel.cluster;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                 :: "r"(cluster_bar) : "memory");
 }
 
 // One arrival on a barrier of the pair.  What it announces is read by the

@@ -94,6 +94,27 @@ def test_groups(counts, H, N):
     check(counts, H, N, seed=len(counts), spare=5)
 
 
+@pytest.mark.parametrize("H,N", [(1040, 2600), (144, 2568), (64, 3001), (4112, 2560)])
+@pytest.mark.parametrize("counts", [[1500, 700], [0, 2049], [129, 0, 2500, 513, 96, 1]])
+def test_many_rows(counts, H, N):
+    """Full and ragged tiles of many rows, channels that end inside a tile."""
+    check(counts, H, N, seed=H + N, spare=3)
+
+
+@pytest.mark.parametrize("H,N", [(272, 2600), (1040, 2049), (64, 3000)])
+@pytest.mark.parametrize("counts", [[33, 64, 65, 96, 97, 127, 128, 129, 160], [20, 0, 250, 1, 40, 48], [17] * 40])
+def test_tens_of_rows(counts, H, N):
+    check(counts, H, N, seed=H + N, spare=1)
+
+
+@pytest.mark.parametrize("rows", [1, 15, 16, 17, 31, 32])
+@pytest.mark.parametrize("H,N", [(528, 100), (1008, 129), (2064, 40), (7168, 130), (1040, 1000)])
+def test_contraction_split_over_blocks(rows, H, N):
+    """A few tiles: their contraction is shared out, in uneven parts at these H."""
+    check([rows], H, N, seed=rows + H)
+    check([0, rows, 3, 0, 1], H, N, seed=rows + N, spare=2)
+
+
 def test_full_codes_below_the_exact_bound():
     """All 256 codes, -128 among them: 1008 * 128 * 128 < 2^24."""
     o = offsets_of([40, 0, 90])
