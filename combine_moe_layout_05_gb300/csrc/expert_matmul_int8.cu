@@ -530,9 +530,21 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                         const __nv_bfloat16 *y = reinterpret_cast<const __nv_bfloat16 *>(generic + (turned - base));
                         __nv_bfloat16 *o = out + (size_t)(t.row + r0) * N + ch0 + lane;
                         const int rows_left = min(16, t.valid - r0);
-#pragma unroll 1
-                        for (int r = 0; r < rows_left; ++r, o += N)
-                            *o = y[r * 32 + (((lane >> 3) ^ (r >> 1 & 3)) << 3) + (lane & 7)];
+                        if (rows_left == 16) {
+                            const int turn = lane >> 3, in = lane & 7;
+#pragma unroll
+                            for (int half = 0; half < 16; half += 8) {
+                                __nv_bfloat16 q[8];
+#pragma unroll
+                                for (int r = 0; r < 8; ++r) q[r] = y[(half + r) * 32 + ((turn ^ (r >> 1 & 3)) << 3) + in];
+#pragma unroll
+                                for (int r = 0; r < 8; ++r, o += N) *o = q[r];
+                            }
+                        } else {
+#pragma unroll 4
+                            for (int r = 0; r < rows_left; ++r, o += N)
+                                *o = y[r * 32 + (((lane >> 3) ^ (r >> 1 & 3)) << 3) + (lane & 7)];
+                        }
                     }
                     __syncwarp();
                 }
