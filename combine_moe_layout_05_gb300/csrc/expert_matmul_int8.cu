@@ -18,8 +18,8 @@
 //   one copies 128-byte-wide tiles of weights and rows into a ring;
 //   one issues the matrix instructions (the pair's first CTA's);
 //   4 GA widen the weights into TMEM (operand A), one channel a thread;
-//   WB GB widen the rows into shared memory (operand B), one row a thread;
-//   four scale the sums and store them, one channel a thread.
+//   WB GB widen the rows into shared memory (operand B), 16 bytes a thread;
+//   4 SETS scale the sums, turn them in shared memory and store them.
 //
 // A pair shares each other's widened rows: every CTA widens half of the tile's
 // rows, which is what keeps shared memory from being the bound (a 128-wide
@@ -72,16 +72,17 @@ struct Shape {
     // the TMEM lanes a warp reaches are those of its number modulo 4
     static constexpr int WB = 4;                       // warps of a group that widens rows
     static_assert(BR * (KS / 64) <= 8 * WB * 4);
-    static constexpr int A0 = 4, E0 = A0 + 4 * GA, B0 = E0 + 4, WARPS = B0 + WB * GB;
+    static constexpr int SETS = PARTS;                 // sets of four warps that store
+    static constexpr int A0 = 4, E0 = A0 + 4 * GA, B0 = E0 + 4 * SETS, WARPS = B0 + WB * GB;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int BARS = 2 * N8 + 2 * NC + 4 + 1 + SPLIT;
     // ring, widened rows, 16 x 32 outputs and the row scales of each storing
     // warp, barriers, flags, expert table
     static constexpr int OFF16 = N8 * SLOT8;
     static constexpr int OFFTURN = OFF16 + NC * B16;
-    static constexpr int OFFBOX = OFFTURN + 4 * 1024;  // SPLIT: the other CTAs' sums, NT x 128 fp32
+    static constexpr int OFFBOX = OFFTURN + 4 * SETS * 1024;  // SPLIT: the other CTAs' sums, NT x 128 fp32
     static constexpr int OFFS = OFFBOX + SPLIT * NT * kChannels * 4;
-    static constexpr int OFFBAR = OFFS + 4 * NT * 4;
+    static constexpr int OFFBAR = OFFS + 4 * SETS * NT * 4;
     static constexpr int OFFTAB = OFFBAR + (BARS * 8 + 15) / 16 * 16 + 32;
     static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4 + 1024; }
 };
@@ -223,7 +224,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         b += 2 * S::N8;
         for (int i = 0; i < S::NC; ++i) mbar_init(b + i, (4 + S::WB) * S::CG), mbar_init(b + S::NC + i, 1);
         b += 2 * S::NC;
-        for (int i = 0; i < 2; ++i) mbar_init(b + i, 1), mbar_init(b + 2 + i, 4 * S::CG);
+        for (int i = 0; i < 2; ++i) mbar_init(b + i, 1), mbar_init(b + 2 + i, 4 * S::SETS * S::CG);
         mbar_init(b + 4, 1);
         if (S::SPLIT) mbar_init(b + 5, 4 * parts);
         *abort = 0;
@@ -420,10 +421,11 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 mbar_drain_bounded(drained, 0);
             }
         }
-    } else if (warp >= S::E0 && warp < S::E0 + 4) {
-        const int quarter = warp & 3;
-        float *const row_scale = reinterpret_cast<float *>(generic + S::OFFS) + quarter * S::NT;
-        const uint32_t turned = base + S::OFFTURN + quarter * 1024;
+    } else if (warp >= S::E0 && warp < S::B0) {
+        // set by set, 16 rows at a time
+        const int quarter = warp & 3, set = (warp - S::E0) >> 2;
+        float *const row_scale = reinterpret_cast<float *>(generic + S::OFFS) + (warp - S::E0) * S::NT;
+        const uint32_t turned = base + S::OFFTURN + (warp - S::E0) * 1024;
         int u = 0;
         bool ok = true;
         for (int i = group; i < items && ok; i += groups) {
@@ -487,18 +489,18 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                     continue;
                 }
                 uint32_t next[16];
-                if (n > 0) {
-                    tmem_load_16x16(acc, next);
-                    tmem_load_16x16(acc + (16u << 16), next + 8);
+                if (16 * set < n) {
+                    tmem_load_16x16(acc + 16 * set, next);
+                    tmem_load_16x16(acc + 16 * set + (16u << 16), next + 8);
                 }
-                for (int c0 = 0; c0 < n; c0 += 16) {
+                for (int c0 = 16 * set; c0 < n; c0 += 16 * S::SETS) {
                     uint32_t v[16];
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = next[j];
-                    if (c0 + 16 < n) {
-                        tmem_load_16x16(acc + c0 + 16, next);
-                        tmem_load_16x16(acc + c0 + 16 + (16u << 16), next + 8);
+                    if (c0 + 16 * S::SETS < n) {
+                        tmem_load_16x16(acc + c0 + 16 * S::SETS, next);
+                        tmem_load_16x16(acc + c0 + 16 * S::SETS + (16u << 16), next + 8);
                     }
                     // the tile's row of column c0: the second CTA's share follows the first's
                     const int second = S::CG == 2 && c0 >= mine;
