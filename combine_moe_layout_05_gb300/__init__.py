@@ -4,7 +4,8 @@ The computation lives in the CUDA library ``libmoe_layout.so`` (C ABI in
 ``include/moe_layout.h``); this package builds it (``build.build()``) and
 binds it with ctypes.  ``workload`` draws seeded synthetic routing inputs and
 ``experts`` holds the stand-in experts a test or benchmark runs between
-dispatch and combine.
+dispatch and combine.  ``layer`` puts the calls together as an MoE layer: the
+router under autograd, and int8 experts.
 """
 from ._binding import (MOE_DEV_ERR_DUPLICATE, MOE_DEV_ERR_EXPERT_RANGE,
                        MOE_DEV_ERR_REGION_OVERFLOW, MOE_DEV_ERR_TIMEOUT,

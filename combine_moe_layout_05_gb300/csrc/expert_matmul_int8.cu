@@ -22,9 +22,15 @@
 //   4 SETS scale the sums, turn them in shared memory and store them.
 //
 // A pair shares each other's widened rows: every CTA widens half of the tile's
-// rows, which is what keeps shared memory from being the bound (a 128-wide
-// step of a full tile moves 16 KB in, 32 KB through the widening warps and
-// 32 KB into the tensor core, in 1024 cycles of the instruction).
+// rows, which keeps shared memory within its 128 bytes a cycle (a 128-byte step
+// of 256 rows moves 32 KB in, 32 KB to the widening warps, 32 KB of widened
+// rows back and 32 KB to the tensor core, in the instruction's 1024 cycles).
+//
+// Measured: 131072 rows, 4096 -> 2048, 128 experts 1.39 ms (1.59 PFLOP/s, 92 %
+// of the card's sustained bf16 rate; power-bound); 1024 rows over 256 experts,
+// 7168 -> 2048, 0.54 ms (6.9 TB/s of weights: HBM-bound); 32768 skewed rows
+// over 384 experts, 7168 -> 2048, 1.24 ms (bound by widening tiles of few
+// rows: 850 cycles a step, where HBM would take 700).
 #include "common.cuh"
 #include "internal.h"
 #include "moe_layout.h"
@@ -86,14 +92,17 @@ struct Shape {
     static constexpr int OFFTAB = OFFBAR + (BARS * 8 + 15) / 16 * 16 + 32;
     static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4 + 1024; }
 };
+// Shared memory and TMEM are what the numbers divide: a deep byte ring where
+// HBM feeds it (Narrow: 8 slots, 144 KB), two accumulators in all, and as many
+// widened slots as are left.  Cycles a step, weights in L2: Narrow 645, Mid
+// 850, Wide 1272 at 256 rows (1024 are the instruction's).
 using Wide = Shape<2, 256, 2, 64, 4, 4, 2, 2>;
 using Mid = Shape<2, 128, 1, 128, 6, 4, 2, 2>;
 using Narrow = Shape<1, 32, 1, 128, 8, 6, 4, 2>;
 using Split = Shape<1, 32, 1, 128, 4, 6, 4, 2, true>;
 
 // Copies of rows come in these heights; a tile takes the one that covers its
-// share (an instruction of the copy engine costs its issuing thread 150 to 200
-// cycles, so a copy too high is cheaper than several that fit).
+// share, so that a step is one copy of weights and one of rows.
 constexpr int kBoxes = 4, kLeastBox = 16;
 struct RowMaps {
     CUtensorMap box[kBoxes];    // 16, 32, 64, 128 rows
@@ -769,6 +778,9 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
+    // Few tiles: share the contraction, as far as every tile's cluster runs at
+    // once and the steps saved outweigh the cluster's barriers (30 tiles of 4272:
+    // 13.7 -> 9.6 us; 4 tiles of 992, 8 steps: 6.4 -> 7.2 us).
     const int64_t tiles = most_tiles<Split>(rows, N, E);
     const int steps = ceil_div(H, kStep);
     int parts = 1;
@@ -779,6 +791,9 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
         if (tiles <= clusters) parts = p;
     }
     if (parts > 1) return go(Split{}, parts);
+    // By rows an expert.  Narrow and Mid: 56.8 and 58.5 us at 8 (15 experts,
+    // 6208 -> 3586), 87 and 64 us at 43 (327, 1008 -> 668).  Mid and Wide: 63 and
+    // 73 us at 304 (87, 2352 -> 368), 1406 and 1256 us at 1024 (128, 4096 -> 2048).
     if (rows <= 16 * E) return go(Narrow{}, 1);
     return rows >= 512 * E ? go(Wide{}, 1) : go(Mid{}, 1);
 }

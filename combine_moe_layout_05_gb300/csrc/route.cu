@@ -17,6 +17,12 @@
 // tokens, are added warp by warp in a block, block by block in a cluster
 // (distributed shared memory) and cluster by cluster at the end, always in
 // that order, so a call's results do not depend on timing.
+//
+// Bound by issue slots, not bytes: about 330 instructions a token at E = 128,
+// K = 8, of which the picks are half.  16384 x 128 fp32: 14.1 us, of which the
+// loop 4.8, the sums 1.5, the finishing kernel 2 and the two launches the rest;
+// one token of 256 experts: 3.5 us.  Sixteen warps a block, two blocks a
+// multiprocessor (three: 17.7 against 16.6 us then).
 #include "common.cuh"
 #include "internal.h"
 #include "moe_layout.h"
@@ -411,6 +417,8 @@ constexpr int kBackBlocks = 152 * 5;
 
 // grad_te = p_te (a_e - sum_j p_tj a_j) with a_e = dL coef E c_e / (K n^2),
 // plus the weights' part at (renormalised) or around (not) the chosen ids.
+// The row is read once and its softmax computed again.  4096 x 384 fp32: 5.0
+// us on the device (2.5 TB/s), 16384 x 128 bf16: 7.2 us; latency and issue.
 template <int NV, int W, typename L>
 __global__ void __launch_bounds__(kBackThreads)
 route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm, float coef,

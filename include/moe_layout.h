@@ -17,8 +17,9 @@
  *    never synchronises, and apart from moe_layout_static's scratch array
  *    (described with that call) it keeps no state between calls.
  *  - moe_layout, moe_dispatch, moe_combine, moe_combine_fp8,
- *    moe_combine_rank_partial, moe_dispatch_send, moe_dispatch_recv and
- *    moe_layout_dispatch are asynchronous on `stream` (0 = legacy default
+ *    moe_combine_rank_partial, moe_dispatch_send, moe_dispatch_recv,
+ *    moe_layout_dispatch, moe_route, moe_route_backward, moe_dispatch_int8 and
+ *    moe_expert_matmul_int8 are asynchronous on `stream` (0 = legacy default
  *    stream) and may be captured into a CUDA graph.
  *  - Arguments are checked on the host before anything is enqueued.  A
  *    failed check returns an error status and enqueues nothing.
