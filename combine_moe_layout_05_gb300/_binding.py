@@ -106,14 +106,20 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()          # 0 for an empty tensor
 
 
+# The current stream's handle without a Stream object, at a tenth of its cost.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+if _raw_stream is None or _get_device is None:
+    def _current_stream() -> int:
+        return torch.cuda.current_stream().cuda_stream
+else:
+    def _current_stream() -> int:
+        return _raw_stream(_get_device())
 
 
 def _stream(stream) -> int | None:
     if stream is None:
-        if _raw_stream is not None:                     # a tenth of a Stream object's cost
-            return _raw_stream(torch.cuda.current_device())
-        stream = torch.cuda.current_stream()
+        return _current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -354,8 +360,9 @@ def moe_combine_fp8(expert_out, expert_scales, topk_weights, dst_row, out,
     _raise("moe_combine_fp8", st)
 
 
-def _fits(t, dtype) -> bool:
-    return t.dtype is dtype and t.is_cuda and t.is_contiguous()
+# The calls below test their tensors in place: a function call for each would
+# cost as much as the tests, and a small call waits for its host side.
+_bf16, _f32, _i32, _i8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
 
 
 def _check_all(pairs) -> None:
@@ -368,15 +375,18 @@ def moe_dispatch_int8(tokens, dst_row, packed, scales, stream=None) -> None:
     """Pack token rows into their K slots as int8 codes with one scale a row."""
     T, H = tokens.shape
     K = dst_row.shape[1] if dst_row.dim() == 2 else 1
-    if not (_fits(tokens, torch.bfloat16) and _fits(dst_row, torch.int32)
-            and _fits(packed, torch.int8) and _fits(scales, torch.float32)):
+    if not (tokens.dtype is _bf16 and tokens.is_cuda and tokens.is_contiguous()
+            and dst_row.dtype is _i32 and dst_row.is_cuda and dst_row.is_contiguous()
+            and packed.dtype is _i8 and packed.is_cuda and packed.is_contiguous()
+            and scales.dtype is _f32 and scales.is_cuda and scales.is_contiguous()):
         _check_all((("tokens", tokens, torch.bfloat16), ("dst_row", dst_row, torch.int32),
                     ("packed", packed, torch.int8), ("scales", scales, torch.float32)))
     rows = T * K
     if dst_row.numel() != rows or packed.numel() < rows * H or scales.numel() < rows:
         raise ValueError("moe_dispatch_int8: dst_row/packed/scales have the wrong size")
-    st = load().moe_dispatch_int8(tokens.data_ptr(), T, H, K, dst_row.data_ptr(),
-                                  packed.data_ptr(), scales.data_ptr(), _stream(stream))
+    st = (_lib or load()).moe_dispatch_int8(
+        tokens.data_ptr(), T, H, K, dst_row.data_ptr(), packed.data_ptr(), scales.data_ptr(),
+        _current_stream() if stream is None else _stream(stream))
     if st:
         _raise("moe_dispatch_int8", st)
 
@@ -386,9 +396,12 @@ def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
     """Packed int8 rows times their experts' int8 weights (see include/moe_layout.h)."""
     rows, H = x.shape
     E, N = weights.shape[0], weights.shape[1]
-    if not (_fits(x, torch.int8) and _fits(x_scales, torch.float32) and _fits(weights, torch.int8)
-            and _fits(w_scales, torch.float32) and _fits(expert_offsets, torch.int32)
-            and _fits(out, torch.bfloat16)):
+    if not (x.dtype is _i8 and x.is_cuda and x.is_contiguous()
+            and x_scales.dtype is _f32 and x_scales.is_cuda and x_scales.is_contiguous()
+            and weights.dtype is _i8 and weights.is_cuda and weights.is_contiguous()
+            and w_scales.dtype is _f32 and w_scales.is_cuda and w_scales.is_contiguous()
+            and expert_offsets.dtype is _i32 and expert_offsets.is_cuda and expert_offsets.is_contiguous()
+            and out.dtype is _bf16 and out.is_cuda and out.is_contiguous()):
         _check_all((("x", x, torch.int8), ("x_scales", x_scales, torch.float32),
                     ("weights", weights, torch.int8), ("w_scales", w_scales, torch.float32),
                     ("expert_offsets", expert_offsets, torch.int32), ("out", out, torch.bfloat16)))
@@ -397,9 +410,10 @@ def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
             or x_scales.numel() < rows or expert_offsets.numel() < E + 1 \
             or out.numel() < rows * N or out.shape[-1] != N:
         raise ValueError("moe_expert_matmul_int8: argument sizes disagree")
-    st = load().moe_expert_matmul_int8(x.data_ptr(), x_scales.data_ptr(), weights.data_ptr(),
-                                       w_scales.data_ptr(), expert_offsets.data_ptr(), rows, H, N,
-                                       E, out.data_ptr(), _ptr(dev_error), _stream(stream))
+    st = (_lib or load()).moe_expert_matmul_int8(
+        x.data_ptr(), x_scales.data_ptr(), weights.data_ptr(), w_scales.data_ptr(),
+        expert_offsets.data_ptr(), rows, H, N, E, out.data_ptr(), _ptr(dev_error),
+        _current_stream() if stream is None else _stream(stream))
     if st:
         _raise("moe_expert_matmul_int8", st)
 
@@ -409,9 +423,9 @@ def moe_route_workspace_bytes(T: int, E: int) -> int:
 
 
 def _logits_type(fn: str, logits) -> int:
-    if logits.dtype is torch.float32:
+    if logits.dtype is _f32:
         return 0
-    if logits.dtype is not torch.bfloat16:
+    if logits.dtype is not _bf16:
         raise TypeError(f"{fn}: logits must be float32 or bfloat16, got {logits.dtype}")
     return 1
 
@@ -424,9 +438,12 @@ def moe_route(logits, topk_ids, topk_weights, expert_counts, routed_tokens, loss
     T, E = logits.shape
     K = topk_ids.shape[1]
     bf16 = _logits_type("moe_route", logits)
-    if not (logits.is_cuda and logits.is_contiguous() and _fits(topk_ids, torch.int32)
-            and _fits(topk_weights, torch.float32) and _fits(expert_counts, torch.int32)
-            and _fits(routed_tokens, torch.int32) and _fits(loss, torch.float32)):
+    if not (logits.is_cuda and logits.is_contiguous()
+            and topk_ids.dtype is _i32 and topk_ids.is_cuda and topk_ids.is_contiguous()
+            and topk_weights.dtype is _f32 and topk_weights.is_cuda and topk_weights.is_contiguous()
+            and expert_counts.dtype is _i32 and expert_counts.is_cuda and expert_counts.is_contiguous()
+            and routed_tokens.dtype is _i32 and routed_tokens.is_cuda and routed_tokens.is_contiguous()
+            and loss.dtype is _f32 and loss.is_cuda and loss.is_contiguous()):
         _check_all((("logits", logits, logits.dtype), ("topk_ids", topk_ids, torch.int32),
                     ("topk_weights", topk_weights, torch.float32),
                     ("expert_counts", expert_counts, torch.int32),
@@ -438,11 +455,12 @@ def moe_route(logits, topk_ids, topk_weights, expert_counts, routed_tokens, loss
     if topk_ids.numel() != T * K or topk_weights.numel() != T * K or expert_counts.numel() < E \
             or routed_tokens.numel() < 1 or loss.numel() < 1:
         raise ValueError("moe_route: output arrays have the wrong size")
-    st = load().moe_route(logits.data_ptr(), bf16, T, E, K, 1 if renormalize else 0, loss_coef,
-                          _ptr(token_mask), topk_ids.data_ptr(), topk_weights.data_ptr(),
-                          expert_counts.data_ptr(), routed_tokens.data_ptr(), loss.data_ptr(),
-                          _ptr(workspace), 0 if workspace is None else workspace.nbytes,
-                          _stream(stream))
+    st = (_lib or load()).moe_route(
+        logits.data_ptr(), bf16, T, E, K, 1 if renormalize else 0, loss_coef, _ptr(token_mask),
+        topk_ids.data_ptr(), topk_weights.data_ptr(), expert_counts.data_ptr(),
+        routed_tokens.data_ptr(), loss.data_ptr(), _ptr(workspace),
+        0 if workspace is None else workspace.nbytes,
+        _current_stream() if stream is None else _stream(stream))
     if st:
         _raise("moe_route", st)
 
@@ -455,9 +473,11 @@ def moe_route_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weig
     T, E = logits.shape
     K = topk_ids.shape[1]
     bf16 = _logits_type("moe_route_backward", logits)
-    if not (logits.is_cuda and logits.is_contiguous() and _fits(grad_logits, logits.dtype)
-            and _fits(topk_ids, torch.int32) and _fits(expert_counts, torch.int32)
-            and _fits(routed_tokens, torch.int32)):
+    if not (logits.is_cuda and logits.is_contiguous()
+            and grad_logits.dtype is logits.dtype and grad_logits.is_cuda and grad_logits.is_contiguous()
+            and topk_ids.dtype is _i32 and topk_ids.is_cuda and topk_ids.is_contiguous()
+            and expert_counts.dtype is _i32 and expert_counts.is_cuda and expert_counts.is_contiguous()
+            and routed_tokens.dtype is _i32 and routed_tokens.is_cuda and routed_tokens.is_contiguous()):
         _check_all((("logits", logits, logits.dtype), ("grad_logits", grad_logits, logits.dtype),
                     ("topk_ids", topk_ids, torch.int32),
                     ("expert_counts", expert_counts, torch.int32),
@@ -469,10 +489,10 @@ def moe_route_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weig
             or (grad_weights is not None and grad_weights.numel() != T * K) \
             or (grad_loss is not None and grad_loss.numel() != 1):
         raise ValueError("moe_route_backward: argument sizes disagree")
-    st = load().moe_route_backward(logits.data_ptr(), bf16, T, E, K, 1 if renormalize else 0,
-                                   loss_coef, topk_ids.data_ptr(), expert_counts.data_ptr(),
-                                   routed_tokens.data_ptr(), _ptr(grad_weights), _ptr(grad_loss),
-                                   grad_logits.data_ptr(), _stream(stream))
+    st = (_lib or load()).moe_route_backward(
+        logits.data_ptr(), bf16, T, E, K, 1 if renormalize else 0, loss_coef, topk_ids.data_ptr(),
+        expert_counts.data_ptr(), routed_tokens.data_ptr(), _ptr(grad_weights), _ptr(grad_loss),
+        grad_logits.data_ptr(), _current_stream() if stream is None else _stream(stream))
     if st:
         _raise("moe_route_backward", st)
 
