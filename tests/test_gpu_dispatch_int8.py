@@ -109,3 +109,18 @@ def test_side_stream_and_offset_view():
     side.synchronize()
     eq, es = reference(x[4:].float().numpy(), dst, 72)
     assert np.array_equal(q.cpu().numpy(), eq) and np.array_equal(s.cpu().numpy(), es)
+
+
+def test_past_32_bit_offsets():
+    """More than 2^31 values: the last rows' addresses need 64 bits."""
+    T, H = 33000, 65536
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    tail = torch.randn((6, H), generator=g).to(torch.bfloat16)
+    x[T - 6:] = tail.cuda()
+    q = torch.full((T, H), -99, dtype=torch.int8, device="cuda")
+    s = torch.full((T,), float("nan"), device="cuda")
+    moe.moe_dispatch_int8(x, torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1), q, s)
+    eq, es = reference(tail.float().numpy(), np.arange(6).reshape(6, 1), 6)
+    assert np.array_equal(q[T - 6:].cpu().numpy(), eq) and np.array_equal(s[T - 6:].cpu().numpy(), es)
+    assert torch.count_nonzero(s[:T - 6]) == 0 and torch.count_nonzero(q[::997]) <= 6 * H

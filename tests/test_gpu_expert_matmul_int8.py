@@ -168,6 +168,35 @@ def test_long_weights_pass_32_bit_offsets():
     check(counts, H, N, seed=9)
 
 
+def test_longest_contraction():
+    check([5, 0, 40], 65536, 40, seed=11)
+    check([20] * 30, 65536, 24, seed=12)
+
+
+def test_outputs_past_32_bit_offsets():
+    """More than 2^31 outputs: the last rows' addresses need 64 bits."""
+    rows, H, N = 1_060_000, 16, 2048
+    x, w = codes((rows, H), 1), codes((2, N, H), 2)
+    xs, ws = scales(rows, 2, N, 3)
+    o = [0, 1000, rows]
+    out = run(x, xs, w, ws, o)
+    for r in (slice(0, 300), slice(900, 1100), slice(rows - 3000, rows)):
+        at = torch.arange(rows, device="cuda")[r]
+        e = (at >= 1000).long()
+        s = torch.einsum("rh,rnh->rn", x[r].double(), w[e].double())
+        assert torch.equal(out[r], (s.float() * xs[r, None] * ws[e]).to(torch.bfloat16))
+
+
+def test_error_word_is_cleared():
+    x, w = codes((20, 64), 1), codes((2, 24, 64), 2)
+    xs, ws = scales(20, 2, 24, 3)
+    err = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+    out = torch.empty((20, 24), dtype=torch.bfloat16, device="cuda")
+    o = torch.tensor([0, 10, 20], dtype=torch.int32, device="cuda")
+    moe.moe_expert_matmul_int8(x, xs, w, ws, o, out, dev_error=err)
+    assert err.item() == 0
+
+
 def test_side_stream_graph_and_repeat():
     x, w = codes((300, 512), 1, -60, 61), codes((4, 512, 512), 2, -60, 61)
     xs, ws = scales(300, 4, 512, 3)

@@ -258,3 +258,51 @@ def test_counts_are_the_layouts():
     b = run(x, 6, True, 1.0)
     lay = moe.LayoutBuffers(3000, 6, 64, 8).run(b.topk_ids)
     assert torch.equal(lay.expert_counts, b.expert_counts) and lay.dev_error.item() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,K", [(70, 64, 4), (70, 250, 8), (700, 384, 8), (9, 512, 3)])
+def test_rows_off_the_16_byte_grid(T, E, K, dtype):
+    """Views that start one value in: the same results as aligned copies, bit for bit."""
+    x = make(T, E, dtype, 5).cuda()
+    flat = torch.empty(T * E + 1, dtype=dtype, device="cuda")
+    view = flat[1:].view(T, E)
+    view.copy_(x)
+    a, b = run(x, K, True, 0.1), run(view, K, True, 0.1)
+    assert torch.equal(a.topk_ids, b.topk_ids) and torch.equal(a.expert_counts, b.expert_counts)
+    assert torch.allclose(a.topk_weights, b.topk_weights, rtol=REL, atol=0)
+    assert abs(a.loss.item() - b.loss.item()) <= REL * a.loss.item()
+    dw, dl = torch.randn(T, K, device="cuda"), torch.ones(1, device="cuda")
+    ga, gb = torch.empty_like(x), torch.empty(T * E + 1, dtype=dtype, device="cuda")[1:].view(T, E)
+    a.backward(x, dw, dl, ga, True, 0.1)
+    b.backward(view, dw, dl, gb, True, 0.1)
+    # each side is within 2 REL of its terms' magnitudes, at most 3 |dw| here; bf16 rounds by 2^-8
+    tol = 4 * REL * 3 * dw.abs().max() + (2.0 ** -7 * ga.float().abs() if dtype == torch.bfloat16 else 0)
+    assert bool(((ga.float() - gb.float()).abs() <= tol).all())
+
+
+def test_past_32_bit_offsets():
+    """More than 2^31 logits: the last rows' addresses need 64 bits."""
+    E, K, tail = 256, 4, 500
+    T = 2 ** 31 // E + tail
+    x = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    last = make(tail, E, torch.bfloat16, 3)
+    x[T - tail:] = last.cuda()
+    b = run(x, K, True, 1.0)
+    p, ids, w, counts, n, loss = reference(last.double().numpy(), K, True, 1.0)
+    assert np.array_equal(b.topk_ids[T - tail:].cpu().numpy(), ids)
+    assert np.all(np.abs(b.topk_weights[T - tail:].cpu().double().numpy() - w) <= REL * w)
+    assert bool((b.topk_ids[: T - tail] == torch.arange(K, device="cuda")).all())
+    total = counts.copy()
+    total[:K] += T - tail
+    assert np.array_equal(b.expert_counts.cpu().numpy(), total) and b.routed_tokens.item() == T
+    grad = torch.full_like(x, torch.nan)
+    dw = torch.zeros((T, K), device="cuda")
+    dw[T - 1, 0] = 1.0
+    b.backward(x, dw, None, grad)
+    assert torch.count_nonzero(grad[: T - 1]) == 0
+    want = np.zeros(E)
+    want[ids[-1]] -= w[-1] * w[-1, 0]
+    want[ids[-1, 0]] += w[-1, 0]
+    got = grad[T - 1].cpu().double().numpy()
+    assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 4 * REL)
