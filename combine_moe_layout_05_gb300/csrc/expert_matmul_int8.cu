@@ -122,20 +122,22 @@ struct Table {
     const int *first_tile;     // [E + 1]
 };
 
+// Tile i, for a whole warp; at: its expert or one before it, and its expert
+// afterwards.  A warp goes through its tiles in order, so the search goes on
+// from the last one's expert, 32 experts a step.
 template <typename S>
-__device__ __forceinline__ Tile tile_of(const Table &t, int E, int channel_tiles, int i)
+__device__ __forceinline__ Tile tile_of(const Table &t, int E, int channel_tiles, int i, int &at)
 {
-    const int tt = i / channel_tiles;
-    int lo = 0, hi = E;                                // first_tile[lo] <= tt < first_tile[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.first_tile[mid] <= tt) lo = mid;
-        else hi = mid;
+    const int tt = (int)((unsigned)i / (unsigned)channel_tiles);
+    for (unsigned passed = kFullMask; passed == kFullMask; at += __popc(passed)) {
+        const int e = at + 1 + (int)(threadIdx.x & 31);
+        passed = __ballot_sync(kFullMask, e < E && t.first_tile[e] <= tt);
     }
+    const int lo = at;                                 // first_tile[lo] <= tt < first_tile[lo + 1]
     const int base = t.first_tile[lo], tiles = t.first_tile[lo + 1] - base;
     const int rows = t.first_row[lo + 1] - t.first_row[lo];
     // an expert's rows are split evenly; a share is at most NT, so no tile is empty
-    const int share = ceil_div(ceil_div(rows, tiles), S::QUANTUM) * S::QUANTUM;
+    const int share = ceil_div((int)((unsigned)(rows + tiles - 1) / (unsigned)tiles), S::QUANTUM) * S::QUANTUM;
     Tile r;
     r.e = uniform(lo);
     r.row = uniform(t.first_row[lo] + (tt - base) * share);
@@ -289,10 +291,10 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     const int group = blockIdx.x / (S::CG * parts), groups = gridDim.x / (S::CG * parts);
 
     if (warp == 0) {
-        int issued = 0;
+        int issued = 0, at = 0;
         bool ok = true;
         for (int i = group; i < items && ok; i += groups) {
-            const Tile t = tile_of<S>(table, E, channel_tiles, i);
+            const Tile t = tile_of<S>(table, E, channel_tiles, i, at);
             const int share = (t.n[0] + t.n[1]) / S::CG;
             int m = 0;
             while (kLeastBox << m < share) ++m;
@@ -317,7 +319,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     } else if (warp == 1) {
         if (rank == 0) {
             int c = 0, cphase = 0;                     // slot of widened operands
-            int u = 0;                                 // accumulators used so far
+            int u = 0, at = 0;                         // accumulators used so far
             const uint64_t b_first = operand_desc(base + S::OFF16);
             constexpr int kFull = S::KS / 16;          // instructions a slot
             const int last = min(kFull, (H - h0 - (slots - 1) * S::KS) >> 4);        // and in the last one
@@ -331,7 +333,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 tc_fence_after();
             };
             for (int i = group; i < items && ok; i += groups) {
-                const Tile t = tile_of<S>(table, E, channel_tiles, i);
+                const Tile t = tile_of<S>(table, E, channel_tiles, i, at);
                 const uint32_t idesc0 = instruction_desc_f16(kChannels * S::CG, t.n[0]);
                 const uint32_t idesc1 = instruction_desc_f16(kChannels * S::CG, t.n[1]);
                 const uint32_t b_part = t.n[0] / S::CG * (128 / 16);       // part 1's rows follow part 0's
@@ -435,24 +437,33 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         const int quarter = warp & 3, set = (warp - S::E0) >> 2;
         float *const row_scale = reinterpret_cast<float *>(generic + S::OFFS) + (warp - S::E0) * S::NT;
         const uint32_t turned = base + S::OFFTURN + (warp - S::E0) * 1024;
-        int u = 0;
+        int u = 0, at = 0;
         bool ok = true;
-        for (int i = group; i < items && ok; i += groups) {
-            const Tile t = tile_of<S>(table, E, channel_tiles, i);
-            const int ch0 = t.channel + (int)rank * kChannels + quarter * 32;
-            __syncwarp();                              // the last tile's scales have been read
-            float xs[S::NT / 32], ws[4];
+        // the next tile and its scales are on their way while one is stored
+        Tile next_tile;
+        float next_xs[S::NT / 32], next_ws[4];
+        auto fetch = [&](int i) {
+            if (i >= items) return;
+            next_tile = tile_of<S>(table, E, channel_tiles, i, at);
 #pragma unroll
             for (int j = 0; j < S::NT / 32; ++j)
-                xs[j] = j * 32 + lane < t.valid ? x_scales[t.row + j * 32 + lane] : 0.0f;
+                next_xs[j] = j * 32 + lane < next_tile.valid ? x_scales[next_tile.row + j * 32 + lane] : 0.0f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int ch = ch0 + 8 * q + (lane >> 2);
-                ws[q] = ch < N ? w_scales[(size_t)t.e * N + ch] : 0.0f;
+                const int ch = next_tile.channel + (int)rank * kChannels + quarter * 32 + 8 * q + (lane >> 2);
+                next_ws[q] = ch < N ? w_scales[(size_t)next_tile.e * N + ch] : 0.0f;
             }
+        };
+        fetch(group);
+        for (int i = group; i < items && ok; i += groups) {
+            const Tile t = next_tile;
+            const int ch0 = t.channel + (int)rank * kChannels + quarter * 32;
+            const float ws[4] = {next_ws[0], next_ws[1], next_ws[2], next_ws[3]};
+            __syncwarp();                              // the last tile's scales have been read
 #pragma unroll
-            for (int j = 0; j < S::NT / 32; ++j) row_scale[j * 32 + lane] = xs[j];
+            for (int j = 0; j < S::NT / 32; ++j) row_scale[j * 32 + lane] = next_xs[j];
             __syncwarp();
+            fetch(i + groups);
             const bool vectors = N % 8 == 0;
             for (int p = 0; p < S::PARTS && ok; ++p, ++u) {
                 const int d = u & 1, n = t.n[p], mine = n / S::CG;
@@ -497,7 +508,13 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                     }
                     continue;
                 }
+                auto release = [&] {                   // all read: the accumulator is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(S::CG == 2 ? cluster_addr(empty_d(d), 0) : empty_d(d));
+                };
                 uint32_t next[16];
+                if (16 * set >= n) release();
                 if (16 * set < n) {
                     tmem_load_16x16(acc + 16 * set, next);
                     tmem_load_16x16(acc + 16 * set + (16u << 16), next + 8);
@@ -510,6 +527,8 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                     if (c0 + 16 * S::SETS < n) {
                         tmem_load_16x16(acc + c0 + 16 * S::SETS, next);
                         tmem_load_16x16(acc + c0 + 16 * S::SETS + (16u << 16), next + 8);
+                    } else {
+                        release();
                     }
                     // the tile's row of column c0: the second CTA's share follows the first's
                     const int second = S::CG == 2 && c0 >= mine;
@@ -559,9 +578,6 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                     }
                     __syncwarp();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(S::CG == 2 ? cluster_addr(empty_d(d), 0) : empty_d(d));
             }
         }
     } else if (warp >= S::A0 && warp < S::E0) {
@@ -608,10 +624,10 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         // rows: group `g` has every GB-th step; a warp takes 8 rows by 64 bytes at
         // a time, a thread 16 bytes, so that few rows are spread over all warps
         const int g = (warp - S::B0) / S::WB, w = (warp - S::B0) % S::WB;
-        int n = 0, m0 = 0;
+        int n = 0, m0 = 0, at = 0;
         bool ok = true;
         for (int i = group; i < items && ok; i += groups, m0 += slots) {
-            const Tile t = tile_of<S>(table, E, channel_tiles, i);
+            const Tile t = tile_of<S>(table, E, channel_tiles, i, at);
             const int blocks = (t.n[0] + t.n[1]) / (8 * S::CG);
             for (int k = 0; k < steps && ok; ++k, ++n) {
                 if (n % S::GB != g) continue;
