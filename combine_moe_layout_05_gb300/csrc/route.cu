@@ -1,6 +1,5 @@
 // route.cu -- from router logits to top-k ids, weights, per-expert counts and
-// the balance loss in one pass, and the gradient of the weights and the loss
-// with respect to the logits.
+// the balance loss in one pass.
 //
 // With p_t = softmax of row t over its open experts (logit > -inf, token not
 // masked), c_e the entries that chose expert e and n the routed tokens:
@@ -13,19 +12,18 @@
 // it the lowest place, is the lowest expert.  The maximum and each pick are
 // one warp-wide maximum over the lanes' next largest: a lane keeps its logits
 // sorted as well and steps on by predicated moves when its own is picked; which
-// expert a pick was is looked up for all K at once, after the last.  Sums of p over tokens stay in registers (fp32) while a warp walks its
-// tokens, are added warp by warp in a block, block by block in a cluster
-// (distributed shared memory) and cluster by cluster at the end, always in
-// that order, so a call's results do not depend on timing.
+// expert a pick was is looked up for all K at once, after the last.  Sums of p
+// over tokens stay in registers (fp32) while a warp walks its tokens, are added
+// warp by warp in a block, block by block in a cluster (distributed shared
+// memory) and cluster by cluster at the end, always in that order, so a call's
+// results do not depend on timing.
 //
 // Bound by issue slots, not bytes: about 330 instructions a token at E = 128,
 // K = 8, of which the picks are half.  16384 x 128 fp32: 14.1 us, of which the
 // loop 4.8, the sums 1.5, the finishing kernel 2 and the two launches the rest;
 // one token of 256 experts: 3.5 us.  Sixteen warps a block, two blocks a
 // multiprocessor (three: 17.7 against 16.6 us then).
-#include "common.cuh"
-#include "internal.h"
-#include "moe_layout.h"
+#include "route_common.cuh"
 #include "tensor.cuh"
 
 namespace moe {
@@ -36,118 +34,6 @@ constexpr int kRouteThreads = kRouteWarps * 32;
 constexpr int kRouteCluster = 8;                    // blocks that add their sums up together
 constexpr int kRouteClusters = 38;                  // at most: two blocks a multiprocessor
 constexpr int kSingleCluster = 8;                   // blocks of the form that needs one launch
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float from_float(float v, float) { return v; }
-__device__ __forceinline__ __nv_bfloat16 from_float(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
-
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Sum over the first `lanes` lanes, a power of two (the others get other sums).
-__device__ __forceinline__ float lanes_sum(float v, int lanes)
-{
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
-    return v;
-}
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
-    return v;
-}
-
-// Largest of the warp's values that are numbers (NaN if none is).
-__device__ __forceinline__ float warp_max(float v)
-{
-    float m;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-    return m;
-}
-
-// 4, 8 or 16 bytes read once, as W values.
-template <int W, typename L>
-__device__ __forceinline__ void load_values(const L *p, float *x)
-{
-    union {
-        uint4 v4;
-        uint2 v2;
-        uint32_t v1;
-        L one[16 / sizeof(L)];
-    } u;
-    if constexpr (W * sizeof(L) == 16) u.v4 = ld_stream_v4(p);
-    else if constexpr (W * sizeof(L) == 8) u.v2 = ld_stream_v2(p);
-    else if constexpr (W * sizeof(L) == 4) u.v1 = __ldg(reinterpret_cast<const uint32_t *>(p));
-    else u.one[0] = *p;
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = to_float(u.one[i]);
-}
-
-template <int W, typename L>
-__device__ __forceinline__ void store_values(L *p, const float *x)
-{
-    union {
-        uint4 v4;
-        uint2 v2;
-        uint32_t v1;
-        L one[16 / sizeof(L)];
-    } u;
-#pragma unroll
-    for (int i = 0; i < W; ++i) u.one[i] = from_float(x[i], L());
-    if constexpr (W * sizeof(L) == 16) st_v4(p, u.v4);
-    else if constexpr (W * sizeof(L) == 8) st_v2(p, u.v2);
-    else if constexpr (W * sizeof(L) == 4) *reinterpret_cast<uint32_t *>(p) = u.v1;
-    else *p = u.one[0];
-}
-
-// Lane's NV logits of a row of E (-inf past E), W at a time: rows start on
-// that many values' bytes, and E is a multiple of W.
-template <int NV, int W, typename L>
-__device__ __forceinline__ void load_row(const L *row, int E, int lane, float (&x)[NV])
-{
-#pragma unroll
-    for (int j = 0; j < NV; ++j) x[j] = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < NV; j += W)
-        if (lane * NV + j < E) load_values<W>(row + lane * NV + j, x + j);
-}
-
-// Descending, by a network of odd and even transpositions (no NaN among them).
-template <int NV>
-__device__ __forceinline__ void sort_values(float (&v)[NV])
-{
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = i & 1; j + 1 < NV; j += 2) {
-            const float hi = fmaxf(v[j], v[j + 1]), lo = fminf(v[j], v[j + 1]);
-            v[j] = hi;
-            v[j + 1] = lo;
-        }
-}
-
-template <int NV>
-__device__ __forceinline__ float lane_max(const float (&x)[NV])
-{
-    float m = x[0];
-#pragma unroll
-    for (int j = 1; j < NV; ++j) m = fmaxf(m, x[j]);
-    return m;
-}
-
-// The probability of logit x before the division by the row's sum: exactly 0
-// at -inf, and NaN for NaN or +inf, which then reaches the whole row.
-__device__ __forceinline__ float weight_of(float x, float m)
-{
-    return x == -INFINITY ? 0.0f : exp2_approx((x - m) * kLog2e);
-}
 
 // The call's last sums, thread e for expert e: p and c are expert e's totals.
 __device__ __forceinline__ float loss_term(float p, int c, int n, int K)
@@ -162,6 +48,7 @@ struct RouteOut {
     float coef;
 };
 
+// KT > 0: K is KT, and the picks are unrolled.
 // SINGLE: the grid is one cluster, which writes the results; otherwise every
 // cluster writes its totals to part[cluster]: E probability sums, E counts and
 // the routed tokens.
@@ -235,8 +122,8 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
         float next[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) next[j] = x[j] > -INFINITY ? x[j] + 0.0f : -INFINITY;  // no NaN, one zero
-        if constexpr (NV <= 12) sort_values<NV>(next);
-        float best = NV <= 12 ? next[0] : lane_max<NV>(next);
+        if constexpr (NV <= 16) sort_values<NV>(next);
+        float best = NV <= 16 ? next[0] : lane_max<NV>(next);
         auto pick = [&](int k) {
             const float top = warp_max(best);
             const int owner = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
@@ -244,7 +131,7 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
                 mine = top;
                 from = owner;
             }
-            if constexpr (NV <= 12) {
+            if constexpr (NV <= 16) {
 #pragma unroll
                 for (int j = 0; j + 1 < NV; ++j) next[j] = lane == owner ? next[j + 1] : next[j];
                 next[NV - 1] = lane == owner ? -INFINITY : next[NV - 1];
@@ -411,127 +298,18 @@ route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int 
     }
 }
 
-constexpr int kBackWarps = 8;
-constexpr int kBackThreads = kBackWarps * 32;
-constexpr int kBackBlocks = 152 * 5;
-
-// grad_te = p_te (a_e - sum_j p_tj a_j) with a_e = dL coef E c_e / (K n^2),
-// plus the weights' part at (renormalised) or around (not) the chosen ids.
-// The row is read once and its softmax computed again.  4096 x 384 fp32: 5.0
-// us on the device (2.5 TB/s), 16384 x 128 bf16: 7.2 us; latency and issue.
-template <int NV, int W, typename L>
-__global__ void __launch_bounds__(kBackThreads)
-route_backward_kernel(const L *__restrict__ logits, int T, int E, int K, int renorm, float coef,
-                      const int32_t *__restrict__ ids, const int32_t *__restrict__ counts,
-                      const int32_t *__restrict__ routed, const float *__restrict__ grad_weights,
-                      const float *__restrict__ grad_loss, L *__restrict__ grad)
-{
-    extern __shared__ float sm[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *add = sm + (size_t)warp * 32 * NV;            // this warp's row of additions
-#pragma unroll
-    for (int j = 0; j < NV; ++j) add[j * 32 + lane] = 0.0f;
-    __syncwarp();
-    pdl_wait();
-    pdl_trigger();
-    const int k_lanes = 1 << (32 - __clz(K - 1));
-    const float n = (float)max(*routed, 1);
-    const float unit = grad_loss ? *grad_loss * coef * (float)E / ((float)K * n) / n : 0.0f;
-    float a[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = lane * NV + j;
-        a[j] = e < E && unit != 0.0f ? unit * (float)counts[e] : 0.0f;
-    }
-    const int stride = gridDim.x * kBackWarps;
-    int t = blockIdx.x * kBackWarps + warp, next_id = -1;
-    float ahead[NV], next_dw = 0.0f;
-    auto fetch = [&](int u) {                            // as in route_kernel
-        if (u >= T) return;
-        load_row<NV, W>(logits + (size_t)u * E, E, lane, ahead);
-        if (lane < K) {
-            next_id = ids[(size_t)u * K + lane];
-            if (grad_weights) next_dw = grad_weights[(size_t)u * K + lane];
-        }
-    };
-    constexpr bool kAhead = NV <= 8;
-    if constexpr (kAhead) fetch(t);
-    for (; t < T; t += stride) {
-        if constexpr (!kAhead) fetch(t);
-        float x[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) x[j] = ahead[j];
-        int id = next_id;
-        float dw = next_dw;
-        if constexpr (kAhead) fetch(t + stride);
-        if ((unsigned)id >= (unsigned)E) id = -1;
-        float chosen = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const float v = __shfl_sync(kFullMask, x[j], id / NV & 31);
-            if (id >= 0 && id % NV == j) chosen = v;
-        }
-        const bool masked = __ballot_sync(kFullMask, id >= 0) == 0;
-        if (masked) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) x[j] = -INFINITY;
-        }
-        float m = warp_max(lane_max<NV>(x));
-        if (!(m > -INFINITY)) m = 0.0f;
-        float s = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            x[j] = weight_of(x[j], m);
-            s += x[j];
-            dot += x[j] * a[j];
-        }
-        s = warp_sum(s);
-        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
-        dot = warp_sum(dot) * inv;
-        float w = id >= 0 ? weight_of(chosen, m) * inv : 0.0f;
-        if (id < 0) dw = 0.0f;
-        if (renorm) {
-            const float total = lanes_sum(w, k_lanes);
-            if (total != 0.0f) w = __fdividef(w, total);
-        }
-        float inner = lanes_sum(w * dw, k_lanes);
-        inner = __shfl_sync(kFullMask, inner, 0);
-        float v = renorm ? w * (dw - inner) : w * dw;
-        if (!renorm) dot += inner;
-        // one id listed twice: its first lane adds them all, in k order
-        const unsigned same = __match_any_sync(kFullMask, id);
-        if (__any_sync(kFullMask, id >= 0 && (same & (same - 1)))) {
-            float sum = 0.0f;
-            for (int k = 0; k < K; ++k) {
-                const float other = __shfl_sync(kFullMask, v, k);
-                if (same >> k & 1) sum += other;
-            }
-            v = sum;
-            if (lane != __ffs(same) - 1) id = -1;
-        }
-        if (id >= 0) add[id] = v;
-        __syncwarp();
-        float y[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) y[j] = x[j] * inv * (a[j] - dot) + add[lane * NV + j];
-        L *to = grad + (size_t)t * E + lane * NV;
-#pragma unroll
-        for (int j = 0; j < NV; j += W)
-            if (lane * NV + j < E) store_values<W>(to + j, y + j);
-        __syncwarp();
-        if (id >= 0) add[id] = 0.0f;
-        __syncwarp();
-    }
-}
-
-// Blocks of one cluster that writes the results itself, or 0: up to four
-// tokens a warp one launch is quicker than two.
-int single_blocks(int T)
+// Blocks of one cluster that writes the results itself, or 0 where two
+// launches over all multiprocessors are quicker: by tokens a warp, fewer the
+// wider the rows (one and two launches, a call among others: E = 128, 512
+// tokens 6.7 and 7.9 us; E = 256, 256 tokens 6.1 and 8.7, 512 tokens 8.9 and
+// 7.7; E = 1000, 256 tokens 23.3 and 20.4).
+int single_blocks(int T, int E)
 {
     const int need = ceil_div(T, kRouteWarps);
     for (int b = 1; b <= kSingleCluster; b *= 2)
         if (need <= b) return b;
-    return need <= 4 * kSingleCluster ? kSingleCluster : 0;
+    const int tokens = E <= 128 ? 4 : E <= 512 ? 2 : 1;
+    return need <= tokens * kSingleCluster ? kSingleCluster : 0;
 }
 
 int route_clusters(int T)
@@ -548,8 +326,11 @@ cudaError_t run_forward(const void *logits, int T, int E, int K, int renorm, flo
     // sums, counts, and an inbox of at most E + kSingleCluster experts' pairs
     const size_t smem = ((size_t)(kRouteWarps + 1) * E + 1 + 2 * (E + kSingleCluster) + kSingleCluster) * 4;
     const RouteOut o{counts, routed, loss, coef};
-    const int single = single_blocks(T);
-    auto *const kernel = K == 8 ? single ? route_kernel<NV, W, 8, true, L> : route_kernel<NV, W, 8, false, L>
+    const int single = single_blocks(T, E);
+    // K = 8, the models' usual, has its own form with the picks unrolled (16384 x
+    // 128: 14.0 us, 16.4 with a test of K at each); rows read value by value not
+    constexpr int KT = W > 1 ? 8 : 0;
+    auto *const kernel = K == KT ? single ? route_kernel<NV, W, KT, true, L> : route_kernel<NV, W, KT, false, L>
                                 : single ? route_kernel<NV, W, 0, true, L> : route_kernel<NV, W, 0, false, L>;
     if (smem > 40 << 10) {
         const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
@@ -566,58 +347,13 @@ cudaError_t run_forward(const void *logits, int T, int E, int K, int renorm, flo
                       blocks / kRouteCluster, E, K, lanes, o);
 }
 
-template <int NV, int W, typename L>
-cudaError_t run_backward(const void *logits, int T, int E, int K, int renorm, float coef,
-                         const int32_t *ids, const int32_t *counts, const int32_t *routed,
-                         const float *grad_weights, const float *grad_loss, void *grad,
-                         cudaStream_t s)
-{
-    const int need = ceil_div(T, kBackWarps);
-    return launch_pdl(route_backward_kernel<NV, W, L>, dim3(need < kBackBlocks ? need : kBackBlocks),
-                      dim3(kBackThreads), (size_t)kBackThreads * NV * 4, s, static_cast<const L *>(logits),
-                      T, E, K, renorm, coef, ids, counts, routed, grad_weights, grad_loss,
-                      static_cast<L *>(grad));
-}
-
-// Whether rows of E values can be read (and written) `bytes` at a time.
-bool rows_aligned(const void *p, const void *q, int E, int size, int bytes)
-{
-    return ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & (bytes - 1)) == 0 &&
-           E * size % bytes == 0;
-}
-
 }  // namespace
 
 size_t route_workspace_bytes(int T, int E)
 {
-    const size_t clusters = single_blocks(T) ? 1 : route_clusters(T);
+    const size_t clusters = single_blocks(T, E) ? 1 : route_clusters(T);
     return (clusters * (2 * (size_t)E + 1) * 4 + 255) / 256 * 256;
 }
-
-// Values a lane holds: the smallest of these that covers E, read in the widest
-// loads that its rows' length and address allow.
-#define MOE_ROUTE_CASES(CALL, OTHER)                                            \
-    if (bf16) {                                                                 \
-        using L = __nv_bfloat16;                                                \
-        if (E <= 128 && rows_aligned(logits, OTHER, E, 2, 8)) return CALL(4, 4, L);  \
-        if (rows_aligned(logits, OTHER, E, 2, 16)) {                            \
-            if (E <= 256) return CALL(8, 8, L);                                 \
-            if (E <= 512) return CALL(16, 8, L);                                \
-            return CALL(32, 8, L);                                              \
-        }                                                                       \
-        if (E <= 256 && rows_aligned(logits, OTHER, E, 2, 4)) return CALL(8, 2, L);  \
-        if (E <= 256) return CALL(8, 1, L);                                     \
-        return CALL(32, 1, L);                                                  \
-    }                                                                           \
-    if (rows_aligned(logits, OTHER, E, 4, 16)) {                                \
-        if (E <= 128) return CALL(4, 4, float);                                 \
-        if (E <= 256) return CALL(8, 4, float);                                 \
-        if (E <= 384) return CALL(12, 4, float);                                \
-        if (E <= 512) return CALL(16, 4, float);                                \
-        return CALL(32, 4, float);                                              \
-    }                                                                           \
-    if (E <= 256) return CALL(8, 1, float);                                     \
-    return CALL(32, 1, float)
 
 cudaError_t launch_route(const void *logits, int bf16, int T, int E, int K, int renorm, float coef,
                          const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts,
@@ -627,18 +363,6 @@ cudaError_t launch_route(const void *logits, int bf16, int T, int E, int K, int 
     run_forward<NV, W, L>(logits, T, E, K, renorm, coef, mask, ids, weights, counts, routed, \
                             loss, workspace, stream)
     MOE_ROUTE_CASES(CALL, logits);
-#undef CALL
-}
-
-cudaError_t launch_route_backward(const void *logits, int bf16, int T, int E, int K, int renorm,
-                                  float coef, const int32_t *ids, const int32_t *counts,
-                                  const int32_t *routed, const float *grad_weights,
-                                  const float *grad_loss, void *grad, cudaStream_t stream)
-{
-#define CALL(NV, W, L)                                                                          \
-    run_backward<NV, W, L>(logits, T, E, K, renorm, coef, ids, counts, routed, grad_weights,    \
-                             grad_loss, grad, stream)
-    MOE_ROUTE_CASES(CALL, grad);
 #undef CALL
 }
 
