@@ -725,19 +725,17 @@ int64_t most_tiles(int rows, int N, int E)
 
 template <typename S>
 cudaError_t run(const void *x, const float *x_scales, const void *w, const float *w_scales,
-                const int32_t *offsets, int rows, int H, int N, int E, int parts, void *out,
+                const int32_t *offsets, int rows, int H, int N, int E, int sms, int parts, void *out,
                 uint32_t *dev_error, cudaStream_t stream)
 {
     CUtensorMap map_w;
     RowMaps map_x;
     if (!byte_map(&map_w, w, (uint64_t)E * N, H, kChannels)) return cudaErrorInvalidValue;
-    for (int m = 0; m < kBoxes; ++m)
-        if (!byte_map(&map_x.box[m], x, rows, H, min(kLeastBox << m, S::BR))) return cudaErrorInvalidValue;
+    for (int m = 0; m < kBoxes; ++m)                   // higher boxes than a CTA's rows are not used
+        if (kLeastBox << m > S::BR) map_x.box[m] = map_x.box[0];
+        else if (!byte_map(&map_x.box[m], x, rows, H, kLeastBox << m)) return cudaErrorInvalidValue;
     const size_t smem = S::bytes(E);
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(&expert_matmul_int8_kernel<S>), smem);
-    if (e != cudaSuccess) return e;
-    int sms = 0;
-    e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
     const int64_t tiles = most_tiles<S>(rows, N, E);
     const int64_t groups = tiles < sms / (S::CG * parts) ? tiles : sms / (S::CG * parts);
@@ -746,9 +744,9 @@ cudaError_t run(const void *x, const float *x_scales, const void *w, const float
                                static_cast<__nv_bfloat16 *>(out), dev_error);
 }
 
-// Clusters of p (2, 4 or 8) splitting CTAs that the current device runs at a
-// time, looked up once for each device.
-cudaError_t split_clusters(int p, int *clusters)
+// Clusters of 2, 4 and 8 splitting CTAs that the current device runs at a time,
+// looked up once for each device.
+cudaError_t split_clusters(int (&clusters)[3])
 {
     constexpr int kMaxDevices = 64;
     static std::mutex mu;
@@ -758,26 +756,28 @@ cudaError_t split_clusters(int p, int *clusters)
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     const std::lock_guard<std::mutex> lock(mu);
-    int &n = known[dev][p / 4];
-    if (n == 0) {
-        auto *const kernel = &expert_matmul_int8_kernel<Split>;
-        const size_t smem = Split::bytes(MOE_MAX_EXPERTS);
-        e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(p);
-        cfg.blockDim = dim3(Split::THREADS);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = p;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-        if (e != cudaSuccess) return e;
+    auto *const kernel = &expert_matmul_int8_kernel<Split>;
+    const size_t smem = Split::bytes(MOE_MAX_EXPERTS);
+    for (int i = 0; i < 3; ++i) {
+        int &n = known[dev][i];
+        if (n == 0) {
+            e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 << i);
+            cfg.blockDim = dim3(Split::THREADS);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        clusters[i] = n;
     }
-    *clusters = n;
     return cudaSuccess;
 }
 
@@ -788,25 +788,27 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
                                       int H, int N, int E, void *out, uint32_t *dev_error,
                                       cudaStream_t stream)
 {
-    auto go = [&](auto shape, int parts) {
-        return run<decltype(shape)>(x, x_scales, w, w_scales, offsets, rows, H, N, E, parts, out, dev_error, stream);
-    };
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
+    auto go = [&](auto shape, int parts) {
+        return run<decltype(shape)>(x, x_scales, w, w_scales, offsets, rows, H, N, E, sms, parts, out, dev_error,
+                                    stream);
+    };
     // Few tiles: share the contraction, as far as every tile's cluster runs at
     // once and the steps saved outweigh the cluster's barriers (30 tiles of 4272:
     // 13.7 -> 9.6 us; 4 tiles of 992, 8 steps: 6.4 -> 7.2 us).
     const int64_t tiles = most_tiles<Split>(rows, N, E);
     const int steps = ceil_div(H, kStep);
-    int parts = 1;
-    for (int p = 2; p <= 8 && tiles * p <= sms && steps >= 16 && steps >= 4 * p; p *= 2) {
-        int clusters = 0;
-        e = split_clusters(p, &clusters);
+    if (tiles * 2 <= sms && steps >= 16) {
+        int clusters[3];
+        e = split_clusters(clusters);
         if (e != cudaSuccess) return e;
-        if (tiles <= clusters) parts = p;
+        int parts = 1;
+        for (int p = 2; p <= 8 && steps >= 4 * p; p *= 2)
+            if (tiles <= clusters[p / 4]) parts = p;
+        if (parts > 1) return go(Split{}, parts);
     }
-    if (parts > 1) return go(Split{}, parts);
     // By rows an expert.  Narrow and Mid: 56.8 and 58.5 us at 8 (15 experts,
     // 6208 -> 3586), 87 and 64 us at 43 (327, 1008 -> 668).  Mid and Wide: 63 and
     // 73 us at 304 (87, 2352 -> 368), 1406 and 1256 us at 1024 (128, 4096 -> 2048).
