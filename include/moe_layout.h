@@ -377,10 +377,10 @@ MOE_API moe_status_t moe_layout_static(const int32_t *topk_ids, int32_t T, int32
  *   loss               coef * E * sum over e of (expert_counts[e] / (K n)) *
  *                      (sum over t of p[t,e] / n); 0 when n == 0             [1]
  *
- * All sums are fp32 in an order that the sizes fix: the same inputs give the
- * same bits.  A NaN logit is never chosen; a NaN or +inf logit of a token that
- * is not masked makes the token's weights and the loss NaN.  A masked token's
- * logits are not looked at.  An id of -1 is what moe_layout reports as
+ * All sums are fp32 in an order that the sizes and the alignment of logits fix:
+ * the same inputs give the same bits.  A NaN logit is never chosen; a NaN or
+ * +inf logit of a token that is not masked makes the token's weights and the
+ * loss NaN.  A masked token's logits are not looked at.  An id of -1 is what moe_layout reports as
  * MOE_DEV_ERR_EXPERT_RANGE and then skips.
  *
  * logits      [T,E], fp32 (bf16 == 0) or bf16 (bf16 == 1), aligned to their type.
