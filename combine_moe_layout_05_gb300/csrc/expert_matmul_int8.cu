@@ -583,31 +583,33 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     } else if (warp >= S::A0 && warp < S::E0) {
         // weights: group `g` has every GA-th step, and in it a thread one channel
         const int g = (warp - S::A0) >> 2, r = (warp & 3) * 32 + lane;
-        int n = 0, m0 = 0;                             // steps, and widened slots, so far
+        // a row's 16-byte pieces are permuted by the row's low bits: piece q is
+        // at piece q ^ (r & 7), a flip of address bits
+        const uint32_t row = base + r * kStep + ((r & 7) << 4);
+        int n0 = 0, m0 = 0;                            // steps, and widened slots, of the tiles before
         bool ok = true;
-        for (int i = group; i < items && ok; i += groups, m0 += slots)
-            for (int k = 0; k < steps && ok; ++k, ++n) {
-                if (n % S::GA != g) continue;
-                const int s = n % S::N8;
+        for (int i = group; i < items && ok; i += groups, n0 += steps, m0 += slots)
+            for (int k = (g + S::GA - n0 % S::GA) % S::GA; k < steps && ok; k += S::GA) {
+                const int n = n0 + k, s = n % S::N8;
                 ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, abort));
-                const uint32_t src = base + s * S::SLOT8 + r * kStep;
+                const uint32_t src = row + s * S::SLOT8;
 #pragma unroll 1
                 for (int h = 0; h < S::PER; ++h) {
                     if (!ok || k * S::PER + h >= slots) break;
                     const int m = m0 + k * S::PER + h, c = m % S::NC;
+                    const uint32_t half = src ^ (h << 6);
+                    const uint32_t dst = tmem + S::ACOL0 + c * S::ACOL + ((uint32_t)(warp & 3) << 21);
                     uint32_t v[32];
 #pragma unroll
                     for (int w = 0; w < S::KS / 64; ++w) {
-                        const int q0 = 4 * (h + w);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            widen16(lds128(src + (((q0 + q) ^ (r & 7)) << 4)), v + 8 * q);
+                        for (int q = 0; q < 4; ++q) widen16(lds128(half ^ (4 * w + q) << 4), v + 8 * q);
                         if (w == 0) {
                             ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, abort));
                             if (!ok) break;
                             tc_fence_after();
                         }
-                        tmem_store_x32(tmem + S::ACOL0 + c * S::ACOL + 32 * w + ((uint32_t)(warp & 3) << 21), v);
+                        tmem_store_x32(dst + 32 * w, v);
                     }
                     if (!ok) break;
                     tmem_wait_st();
@@ -624,14 +626,13 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         // rows: group `g` has every GB-th step; a warp takes 8 rows by 64 bytes at
         // a time, a thread 16 bytes, so that few rows are spread over all warps
         const int g = (warp - S::B0) / S::WB, w = (warp - S::B0) % S::WB;
-        int n = 0, m0 = 0, at = 0;
+        int n0 = 0, m0 = 0, at = 0;
         bool ok = true;
-        for (int i = group; i < items && ok; i += groups, m0 += slots) {
+        for (int i = group; i < items && ok; i += groups, n0 += steps, m0 += slots) {
             const Tile t = tile_of<S>(table, E, channel_tiles, i, at);
             const int blocks = (t.n[0] + t.n[1]) / (8 * S::CG);
-            for (int k = 0; k < steps && ok; ++k, ++n) {
-                if (n % S::GB != g) continue;
-                const int s = n % S::N8;
+            for (int k = (g + S::GB - n0 % S::GB) % S::GB; k < steps && ok; k += S::GB) {
+                const int n = n0 + k, s = n % S::N8;
                 ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, abort));
                 const uint32_t src = base + s * S::SLOT8 + S::A8;
 #pragma unroll 1

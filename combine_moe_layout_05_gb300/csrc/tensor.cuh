@@ -88,7 +88,19 @@ __device__ __forceinline__ bool elect_one()
     return one != 0;
 }
 
+// Whether the phase with the given parity is over; asks once.
 __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
+// The same, asleep for a while until it is.
+__device__ __forceinline__ bool mbar_sleep_cluster(uint32_t bar, uint32_t parity)
 {
     uint32_t done;
     asm volatile("{\n\t.reg .pred p;\n\t"
@@ -105,7 +117,7 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
 static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort)
 {
     const long long start = clock64();
-    while (!mbar_test_cluster(bar, parity))
+    while (!mbar_sleep_cluster(bar, parity))
         if (*abort || clock64() - start > kWaitLimitCycles) {
             *abort = 1;
             return false;
@@ -115,14 +127,14 @@ static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity
 
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort)
 {
-    return mbar_test_cluster(bar, parity) || mbar_wait_long(bar, parity, abort);
+    return mbar_sleep_cluster(bar, parity) || mbar_wait_long(bar, parity, abort);
 }
 
 // The same for a copy or a matrix instruction in flight while giving up.
 __device__ __forceinline__ void mbar_drain_bounded(uint32_t bar, uint32_t parity)
 {
     const long long start = clock64();
-    while (!mbar_test_cluster(bar, parity))
+    while (!mbar_sleep_cluster(bar, parity))
         if (clock64() - start > kWaitLimitCycles) return;
 }
 
