@@ -26,11 +26,12 @@
 // of 256 rows moves 32 KB in, 32 KB to the widening warps, 32 KB of widened
 // rows back and 32 KB to the tensor core, in the instruction's 1024 cycles).
 //
-// Measured: 131072 rows, 4096 -> 2048, 128 experts 1.39 ms (1.59 PFLOP/s, 92 %
-// of the card's sustained bf16 rate; power-bound); 1024 rows over 256 experts,
-// 7168 -> 2048, 0.54 ms (6.9 TB/s of weights: HBM-bound); 32768 skewed rows
-// over 384 experts, 7168 -> 2048, 1.24 ms (bound by widening tiles of few
-// rows: 850 cycles a step, where HBM would take 700).
+// Measured: 131072 rows, 4096 -> 2048, 128 experts 1.22 ms (1.80 PFLOP/s, 96 %
+// of a library bf16 product's rate) in a burst and 1.40 under the power cap;
+// 1024 rows over 256 experts, 7168 -> 2048, 0.54 ms (7.0 TB/s of weights:
+// HBM-bound); 32768 skewed rows over 384 experts, 7168 -> 2048, 1.12 ms in a
+// burst, 1.22 under the cap (547 tiles of 60 rows on average, 600 to 700 cycles
+// a step; HBM takes 706 for the first tile of an expert, L2 feeds the others).
 #include "common.cuh"
 #include "internal.h"
 #include "moe_layout.h"
@@ -94,8 +95,9 @@ struct Shape {
 };
 // Shared memory and TMEM are what the numbers divide: a deep byte ring where
 // HBM feeds it (Narrow: 8 slots, 144 KB), two accumulators in all, and as many
-// widened slots as are left.  Cycles a step, weights in L2: Narrow 645, Mid
-// 850, Wide 1272 at 256 rows (1024 are the instruction's).
+// widened slots as are left.  Cycles a step, weights in L2: Narrow 552 (16
+// rows) and 584 (32), Mid 613 (64) and 704 (128), Wide 1233 (256; 1024 are the
+// instruction's).
 using Wide = Shape<2, 256, 2, 64, 4, 4, 2, 2>;
 using Mid = Shape<2, 128, 1, 128, 6, 4, 2, 2>;
 using Narrow = Shape<1, 32, 1, 128, 8, 6, 4, 2>;
@@ -798,7 +800,7 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
     };
     // Few tiles: share the contraction, as far as every tile's cluster runs at
     // once and the steps saved outweigh the cluster's barriers (30 tiles of 4272:
-    // 13.7 -> 9.6 us; 4 tiles of 992, 8 steps: 6.4 -> 7.2 us).
+    // 12.2 -> 9.3 us; 4 tiles of 992, 8 steps: 6.4 -> 7.2 us).
     const int64_t tiles = most_tiles<Split>(rows, N, E);
     const int steps = ceil_div(H, kStep);
     if (tiles * 2 <= sms && steps >= 16) {
@@ -810,9 +812,9 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
             if (tiles <= clusters[p / 4]) parts = p;
         if (parts > 1) return go(Split{}, parts);
     }
-    // By rows an expert.  Narrow and Mid: 56.8 and 58.5 us at 8 (15 experts,
-    // 6208 -> 3586), 87 and 64 us at 43 (327, 1008 -> 668).  Mid and Wide: 63 and
-    // 73 us at 304 (87, 2352 -> 368), 1406 and 1256 us at 1024 (128, 4096 -> 2048).
+    // By rows an expert.  Narrow and Mid: 56.3 and 58.1 us at 8 (15 experts,
+    // 6208 -> 3586), 70 and 53 us at 43 (327, 1008 -> 668).  Mid and Wide: 55 and
+    // 62 us at 304 (87, 2352 -> 368), 1283 and 1225 us at 1024 (128, 4096 -> 2048).
     if (rows <= 16 * E) return go(Narrow{}, 1);
     return rows >= 512 * E ? go(Wide{}, 1) : go(Mid{}, 1);
 }
