@@ -79,7 +79,7 @@ struct Shape {
     // the TMEM lanes a warp reaches are those of its number modulo 4
     static constexpr int WB = 4;                       // warps of a group that widens rows
     static_assert(BR * (KS / 64) <= 8 * WB * 4);
-    static constexpr int SETS = PARTS;                 // sets of four warps that store
+    static constexpr int SETS = CG;                    // sets of four warps that store
     static constexpr int A0 = 4, E0 = A0 + 4 * GA, B0 = E0 + 4 * SETS, WARPS = B0 + WB * GB;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int BARS = 2 * N8 + 2 * NC + 4 + 1 + SPLIT;
