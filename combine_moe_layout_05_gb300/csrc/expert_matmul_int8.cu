@@ -46,6 +46,7 @@ namespace {
 constexpr int kStep = 128;                 // bytes of the contraction a ring slot holds
 constexpr int kChannels = 128;             // channels a CTA
 constexpr int kTmemColumns = 512;
+constexpr int kMaxShared = 227 * 1024;
 
 // CG: CTAs a tile.  NT: rows a tile at most.  PARTS: parts a tile's rows are
 // summed in, each with its accumulator.  KS: the contraction's share of a slot
@@ -89,9 +90,11 @@ struct Shape {
     static constexpr int OFFTURN = OFF16 + NC * B16;
     static constexpr int OFFBOX = OFFTURN + 4 * SETS * 1024;  // SPLIT: the other CTAs' sums, NT x 128 fp32
     static constexpr int OFFS = OFFBOX + SPLIT * NT * kChannels * 4;
-    static constexpr int OFFBAR = OFFS + 4 * SETS * NT * 4;
+    static constexpr int SCALES = PARTS == 1 ? NT / SETS : NT;    // rows a storing warp needs the scales of
+    static constexpr int OFFBAR = OFFS + 4 * SETS * SCALES * 4;
     static constexpr int OFFTAB = OFFBAR + (BARS * 8 + 15) / 16 * 16 + 32;
-    static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4 + 1024; }
+    static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4; }
+    static_assert(bytes(MOE_MAX_EXPERTS) <= kMaxShared);
 };
 // Shared memory and TMEM are what the numbers divide: a deep byte ring where
 // HBM feeds it (Narrow: 8 slots, 144 KB), two accumulators in all, and as many
@@ -148,6 +151,15 @@ __device__ __forceinline__ Tile tile_of(const Table &t, int E, int channel_tiles
     r.n[0] = S::PARTS == 1 ? n : ceil_div(n, 2 * S::QUANTUM) * S::QUANTUM;
     r.n[1] = n - r.n[0];
     r.channel = (i - tt * channel_tiles) * kChannels * S::CG;
+    return r;
+}
+
+// Two products at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
 
@@ -208,9 +220,8 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                           const int32_t *__restrict__ offsets, int rows, int H, int N, int E,
                           __nv_bfloat16 *__restrict__ out, uint32_t *__restrict__ dev_error)
 {
-    extern __shared__ uint8_t raw[];
-    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-    uint8_t *const generic = raw + (base - smem_addr(raw));
+    extern __shared__ __align__(1024) uint8_t generic[];   // the swizzle is of addresses; no other shared arrays
+    const uint32_t base = smem_addr(generic);
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
     const uint32_t rank = S::CG == 2 ? uniform(cluster_rank()) : 0;
 
@@ -250,7 +261,8 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     // Tiles an expert, then their running sum: thread t has experts 2t, 2t + 1.
     {
         static_assert(2 * S::THREADS > MOE_MAX_EXPERTS);
-        __shared__ int warp_tiles[S::WARPS];
+        static_assert(S::WARPS * 4 <= 4 * S::SETS * 1024);
+        int *const warp_tiles = reinterpret_cast<int *>(generic + S::OFFTURN);      // not in use yet
         int tiles[2], before = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -437,19 +449,23 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     } else if (warp >= S::E0 && warp < S::B0) {
         // set by set, 16 rows at a time
         const int quarter = warp & 3, set = (warp - S::E0) >> 2;
-        float *const row_scale = reinterpret_cast<float *>(generic + S::OFFS) + (warp - S::E0) * S::NT;
+        float *const row_scale = reinterpret_cast<float *>(generic + S::OFFS) + (warp - S::E0) * S::SCALES;
         const uint32_t turned = base + S::OFFTURN + (warp - S::E0) * 1024;
         int u = 0, at = 0;
         bool ok = true;
         // the next tile and its scales are on their way while one is stored
         Tile next_tile;
-        float next_xs[S::NT / 32], next_ws[4];
+        float next_xs[S::SCALES / 32], next_ws[4];
         auto fetch = [&](int i) {
             if (i >= items) return;
             next_tile = tile_of<S>(table, E, channel_tiles, i, at);
 #pragma unroll
-            for (int j = 0; j < S::NT / 32; ++j)
-                next_xs[j] = j * 32 + lane < next_tile.valid ? x_scales[next_tile.row + j * 32 + lane] : 0.0f;
+            for (int j = 0; j < S::SCALES / 32; ++j) {
+                // all rows, or every SETS-th 16 of them where the sets take them by turns
+                const int k = j * 32 + lane;
+                const int r = S::PARTS == 1 ? (k >> 4) * 16 * S::SETS + 16 * set + (k & 15) : k;
+                next_xs[j] = r < next_tile.valid ? x_scales[next_tile.row + r] : 0.0f;
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int ch = next_tile.channel + (int)rank * kChannels + quarter * 32 + 8 * q + (lane >> 2);
@@ -463,7 +479,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
             const float ws[4] = {next_ws[0], next_ws[1], next_ws[2], next_ws[3]};
             __syncwarp();                              // the last tile's scales have been read
 #pragma unroll
-            for (int j = 0; j < S::NT / 32; ++j) row_scale[j * 32 + lane] = next_xs[j];
+            for (int j = 0; j < S::SCALES / 32; ++j) row_scale[j * 32 + lane] = next_xs[j];
             __syncwarp();
             fetch(i + groups);
             const bool vectors = N % 8 == 0;
@@ -535,7 +551,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                     // the tile's row of column c0: the second CTA's share follows the first's
                     const int second = S::CG == 2 && c0 >= mine;
                     const int r0 = c0 + (p ? t.n[0] / S::CG : 0) + (second ? (t.n[0] + t.n[1]) / 2 - mine : 0);
-                    const float *rs = row_scale + r0 + 2 * (lane & 3);
+                    const float *rs = row_scale + (S::PARTS == 1 ? r0 / S::SETS & ~15 : r0) + 2 * (lane & 3);
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {      // 8 rows, of 4 times 8 channels
                         const float2 r = *reinterpret_cast<const float2 *>(rs + 8 * b);
@@ -543,7 +559,8 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t *w = v + 8 * (q >> 1) + 4 * b + 2 * (q & 1);
-                            y[q] = pack_bf16x2_rn(__uint_as_float(w[0]) * r.x * ws[q], __uint_as_float(w[1]) * r.y * ws[q]);
+                            const float2 z = mul2(mul2({__uint_as_float(w[0]), __uint_as_float(w[1])}, r), {ws[q], ws[q]});
+                            y[q] = pack_bf16x2_rn(z.x, z.y);
                         }
                         const int j = lane & 7;        // a row of 64 bytes, its 16-byte pieces permuted
                         store_turned_x4(turned + (8 * b + j) * 64 + (((lane >> 3) ^ (j >> 1 & 3)) << 4),

@@ -107,6 +107,12 @@ def test_tens_of_rows(counts, H, N):
     check(counts, H, N, seed=H + N, spare=1)
 
 
+@pytest.mark.parametrize("each", [3, 40, 520])
+def test_the_most_experts_of_few_and_many_rows(each):
+    """The experts' table takes the most shared memory, in each form."""
+    check([each + (e % 5 == 0) for e in range(1024)], 48, 24, seed=each)
+
+
 @pytest.mark.parametrize("rows", [1, 15, 16, 17, 31, 32])
 @pytest.mark.parametrize("H,N", [(528, 100), (1008, 129), (2064, 40), (7168, 130), (1040, 1000)])
 def test_contraction_split_over_blocks(rows, H, N):
