@@ -830,10 +830,13 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
         if (parts > 1) return go(Split{}, parts);
     }
     // By rows an expert.  Narrow and Mid: 56.3 and 58.1 us at 8 (15 experts,
-    // 6208 -> 3586), 70 and 53 us at 43 (327, 1008 -> 668).  Mid and Wide: 55 and
-    // 62 us at 304 (87, 2352 -> 368), 1283 and 1225 us at 1024 (128, 4096 -> 2048).
+    // 6208 -> 3586), 93 and 53 us at 64 (64, 1024 -> 4096).  Mid and Wide: 68 and
+    // 77 us at 128 (64, 2048 -> 2048), 248 and 232 us at 384 (32, 7168 -> 2048),
+    // 667 and 638 us at 1024 (64, 4096 -> 2048).  A short contraction leaves Wide
+    // waiting for its stores, which Mid's alternate accumulators hide: 300 and
+    // 321 us (64 experts of 1024 rows, 512 -> 4096), equal at 2560.
     if (rows <= 16 * E) return go(Narrow{}, 1);
-    return rows >= 512 * E ? go(Wide{}, 1) : go(Mid{}, 1);
+    return rows >= 384 * E && steps >= 20 ? go(Wide{}, 1) : go(Mid{}, 1);
 }
 
 }  // namespace moe

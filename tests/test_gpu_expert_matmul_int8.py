@@ -101,6 +101,12 @@ def test_many_rows(counts, H, N):
     check(counts, H, N, seed=H + N, spare=3)
 
 
+@pytest.mark.parametrize("H,N", [(2560, 2600), (2576, 257), (2752, 2561), (3984, 1), (2816, 520)])
+@pytest.mark.parametrize("counts", [[385], [900, 33, 410], [0, 255, 2049, 1, 256, 257, 17]])
+def test_many_rows_and_a_long_contraction(counts, H, N):
+    check(counts, H, N, seed=H + N, spare=2)
+
+
 @pytest.mark.parametrize("H,N", [(272, 2600), (1040, 2049), (64, 3000)])
 @pytest.mark.parametrize("counts", [[33, 64, 65, 96, 97, 127, 128, 129, 160], [20, 0, 250, 1, 40, 48], [17] * 40])
 def test_tens_of_rows(counts, H, N):
