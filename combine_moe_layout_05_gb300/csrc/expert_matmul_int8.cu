@@ -26,11 +26,11 @@
 // of 256 rows moves 32 KB in, 32 KB to the widening warps, 32 KB of widened
 // rows back and 32 KB to the tensor core, in the instruction's 1024 cycles).
 //
-// Measured: 131072 rows, 4096 -> 2048, 128 experts 1.22 ms (1.80 PFLOP/s, 96 %
-// of a library bf16 product's rate) in a burst and 1.40 under the power cap;
+// Measured: 131072 rows, 4096 -> 2048, 128 experts 1.23 ms (1.79 PFLOP/s, 96 %
+// of a library bf16 product's rate) in a burst and 1.38 under the power cap;
 // 1024 rows over 256 experts, 7168 -> 2048, 0.54 ms (7.0 TB/s of weights:
 // HBM-bound); 32768 skewed rows over 384 experts, 7168 -> 2048, 1.12 ms in a
-// burst, 1.22 under the cap (547 tiles of 60 rows on average, 600 to 700 cycles
+// burst, 1.20 under the cap (547 tiles of 60 rows on average, 600 to 700 cycles
 // a step; HBM takes 706 for the first tile of an expert, L2 feeds the others).
 #include "common.cuh"
 #include "internal.h"
