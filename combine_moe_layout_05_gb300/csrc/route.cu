@@ -1,7 +1,7 @@
 // route.cu -- from router logits to top-k ids, weights, per-expert counts and
 // the balance loss in one pass.
 //
-// With p_t = softmax of row t over its open experts (logit > -inf, token not
+// With p_t = softmax of row t over its open experts (logit not -inf, token not
 // masked), c_e the entries that chose expert e and n the routed tokens:
 //
 //   loss = coef * E * sum_e (c_e / (K n)) * (sum_t p_te / n)
@@ -74,6 +74,7 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
 
     const int k_lanes = 1 << (32 - __clz(K - 1));        // K, rounded up to a power of two
     int routed = 0;                                      // tokens with a first pick (lane 0)
+    bool bad = false;                                    // a token's probabilities are NaN
     float acc[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) acc[j] = 0.0f;
@@ -111,12 +112,13 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
             s += p[j];
         }
         s = warp_sum(s);
+        bad |= s != s;
         const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
 #pragma unroll
         for (int j = 0; j < NV; ++j) acc[j] += p[j] * inv;
 
         // Pick number `lane`: its logit, and the lane that holds it.  Past the
-        // last open expert the picks are -inf, and not taken below.
+        // last open number the picks are -inf, and not taken below.
         float mine = -INFINITY;
         int from = 0;
         float next[NV];
@@ -176,10 +178,35 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
         if (taken) atomicAdd(&cnt[id], 1);
         routed += taken;
     }
-    if (lane == 0) atomicAdd(&cnt[E], routed);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         if (lane * NV + j < E) sums[warp * E + lane * NV + j] = acc[j];
+    // NaN logits are behind every number: where a token's numbers were fewer than
+    // K, its NaN ones take the picks that are left, lowest index first, with NaN
+    // for weights.  Rare, so after the loop, whose registers are all in use.
+    if (bad)
+        for (t = blockIdx.x * kRouteWarps + warp; t < T; t += stride) {
+            if (mask && !mask[t]) continue;
+            int32_t *const id = ids + (size_t)t * K;
+            float *const w = weights + (size_t)t * K;
+            __syncwarp();
+            const int numbers = __popc(__ballot_sync(kFullMask, lane < K && id[lane] >= 0));
+            int picks = numbers;
+            for (int e0 = 0; e0 < E && picks < K; e0 += 32) {
+                const float x = e0 + lane < E ? to_float(logits[(size_t)t * E + e0 + lane]) : 0.0f;
+                const unsigned nans = __ballot_sync(kFullMask, x != x);
+                const int k = picks + __popc(nans & ((1u << lane) - 1));
+                if (x != x && k < K) {
+                    id[k] = e0 + lane;
+                    w[k] = x;
+                    atomicAdd(&cnt[e0 + lane], 1);
+                }
+                picks += __popc(nans);
+            }
+            if (lane < K && lane >= picks) w[lane] = 0.0f;      // no expert, so no weight
+            routed += numbers == 0 && picks > 0;
+        }
+    if (lane == 0) atomicAdd(&cnt[E], routed);
     // Expert e is added up by block e % blocks of the cluster: every block puts
     // its sums, its counts and its routed tokens in that block's inbox.
     const int rank = (int)cluster_rank(), blocks = SINGLE ? (int)gridDim.x : kRouteCluster;

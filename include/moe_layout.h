@@ -364,7 +364,7 @@ MOE_API moe_status_t moe_layout_static(const int32_t *topk_ids, int32_t T, int32
  * with the per-expert counts and the balance loss, in one pass.
  *
  * An expert is open for a token when the token is not masked and its logit is
- * above -inf; a token with an open expert is routed.  With x the logits:
+ * not -inf; a token with an open expert is routed.  With x the logits:
  *
  *   p[t,e]  = exp(x[t,e] - m_t) / sum over open e' of exp(x[t,e'] - m_t),
  *             0 for an expert that is not open
@@ -378,10 +378,12 @@ MOE_API moe_status_t moe_layout_static(const int32_t *topk_ids, int32_t T, int32
  *                      (sum over t of p[t,e] / n); 0 when n == 0             [1]
  *
  * All sums are fp32 in an order that the sizes and the alignment of logits fix:
- * the same inputs give the same bits.  A NaN logit is never chosen; a NaN or
- * +inf logit of a token that is not masked makes the token's weights and the
- * loss NaN.  A masked token's logits are not looked at.  An id of -1 is what moe_layout reports as
- * MOE_DEV_ERR_EXPERT_RANGE and then skips.
+ * the same inputs give the same bits.  A NaN logit ranks below every number: it
+ * is chosen only where fewer than K open logits are numbers, the lowest index
+ * first.  A NaN or +inf logit of a token that is not masked makes the weights of
+ * the token's chosen experts and the loss NaN, and moe_route_backward the
+ * token's gradient.  A masked token's logits are not looked at.  An id of -1 is
+ * what moe_layout reports as MOE_DEV_ERR_EXPERT_RANGE and then skips.
  *
  * logits      [T,E], fp32 (bf16 == 0) or bf16 (bf16 == 1), aligned to their type.
  * token_mask  [T] bytes or NULL; 0 masks the token (padding).
