@@ -36,24 +36,29 @@ class _Route(torch.autograd.Function):
         logits = logits.contiguous()
         b = moe.RouteBuffers(T, K, E, device=logits.device)
         b.run(logits, renormalize, loss_coef, token_mask)
-        ctx.buffers, ctx.settings = b, (renormalize, loss_coef)
-        ctx.save_for_backward(logits)
+        ctx.settings = renormalize, loss_coef
+        # saved, not kept on ctx: an edit in place is then an error in backward,
+        # and the outputs are in no cycle with their own node
+        ctx.save_for_backward(logits, b.topk_ids, b.expert_counts, b.routed_tokens)
         ctx.mark_non_differentiable(b.topk_ids, b.expert_counts)
         return b.topk_ids, b.topk_weights, b.expert_counts, b.loss.view(())
 
     @staticmethod
     def backward(ctx, _ids, grad_weights, _counts, grad_loss):
-        (logits,) = ctx.saved_tensors
+        logits, ids, counts, routed = ctx.saved_tensors
         grad = torch.empty_like(logits)
-        ctx.buffers.backward(logits, grad_weights.float().contiguous(),
-                             grad_loss.float().reshape(1).contiguous(), grad, *ctx.settings)
+        moe.moe_route_backward(logits, ids, counts, routed, grad_weights.float().contiguous(),
+                               grad_loss.float().reshape(1).contiguous(), grad, *ctx.settings)
         return grad, None, None, None, None
 
 
 def route(logits: torch.Tensor, K: int, renormalize: bool = True, loss_coef: float = 1.0,
           token_mask: torch.Tensor | None = None):
     """Router logits [T, E] to (topk_ids, topk_weights, expert_counts, loss);
-    topk_weights and loss carry gradients to the logits."""
+    topk_weights and loss carry gradients to the logits.  The gradient needs
+    topk_ids and expert_counts as they are: to drop entries, edit a copy
+    (``topk_ids.masked_fill(full, -1)``); after an edit in place backward
+    raises."""
     return _Route.apply(logits, K, renormalize, loss_coef, token_mask)
 
 

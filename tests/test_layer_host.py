@@ -1,0 +1,90 @@
+"""layer.py on the CPU, with stand-ins for the library's calls: what autograd
+keeps and refuses, and what the layer hands to the calls.  The stand-ins compute
+the router by PyTorch, so a gradient is compared with one of the same operations
+in the same type (equal but for the order of sums, 1e-6)."""
+import gc
+import weakref
+
+import pytest
+import torch
+
+from combine_moe_layout_05_gb300 import _binding, layer
+
+
+def _outputs(x, ids, counts, renormalize, coef):
+    T, E = x.shape
+    K = ids.shape[1]
+    p = torch.softmax(x, 1)
+    w = torch.where(ids >= 0, p.gather(1, ids.long().clamp(min=0)), torch.zeros((), dtype=x.dtype))
+    if renormalize:
+        w = w / w.sum(1, keepdim=True)
+    return w, coef * E * (counts.to(x.dtype) / (K * T) * p.mean(0)).sum()
+
+
+def _route(logits, topk_ids, topk_weights, expert_counts, routed_tokens, loss, renormalize=True, loss_coef=1.0,
+           token_mask=None, workspace=None, stream=None):
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    topk_ids.copy_(torch.sort(logits, dim=1, descending=True, stable=True)[1][:, :K])
+    expert_counts.copy_(torch.bincount(topk_ids.reshape(-1).long(), minlength=E))
+    routed_tokens.fill_(T)
+    w, value = _outputs(logits, topk_ids, expert_counts, renormalize, loss_coef)
+    topk_weights.copy_(w)
+    loss.copy_(value)
+
+
+def _route_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weights, grad_loss, grad_logits,
+                    renormalize=True, loss_coef=1.0, stream=None):
+    with torch.enable_grad():
+        x = logits.detach().requires_grad_()
+        w, value = _outputs(x, topk_ids, expert_counts, renormalize, loss_coef)
+        grad_logits.copy_(torch.autograd.grad((w * grad_weights).sum() + value * grad_loss.reshape(()), x)[0])
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    monkeypatch.setattr(_binding, "moe_route", _route)
+    monkeypatch.setattr(_binding, "moe_route_backward", _route_backward)
+    monkeypatch.setattr(_binding, "moe_route_workspace_bytes", lambda T, E: 256)
+
+
+def _logits(T=6, E=10):
+    return torch.randn((T, E), generator=torch.Generator().manual_seed(0)).requires_grad_()
+
+
+def test_gradient_through_the_stand_ins(calls):
+    logits = _logits()
+    ids, weights, counts, loss = layer.route(logits, 3, True, 0.5)
+    pull = torch.arange(18.0).view(6, 3)
+    ((weights * pull).sum() + 2 * loss).backward()
+    x = logits.detach().clone().requires_grad_()
+    w, value = _outputs(x, ids, counts, True, 0.5)
+    ((w * pull).sum() + 2 * value).backward()
+    assert torch.allclose(logits.grad, x.grad, rtol=0, atol=1e-6)
+
+
+@pytest.mark.parametrize("which", ["ids", "counts"])
+def test_an_edit_of_what_the_gradient_needs_is_an_error(calls, which):
+    """Dropping entries by ids[...] = -1 must not change the gradient of weights
+    that were computed with the old ids."""
+    ids, weights, counts, loss = layer.route(_logits(), 3)
+    (ids if which == "ids" else counts)[2] = -1
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        (weights.sum() + loss).backward()
+
+
+@pytest.mark.parametrize("with_backward", [False, True])
+def test_nothing_is_kept_in_a_cycle(calls, with_backward):
+    """Buffers and logits go with the last reference, not with the collector."""
+    gc.collect()
+    gc.disable()
+    try:
+        ids, weights, counts, loss = layer.route(_logits(), 3)
+        node = weakref.ref(weights.grad_fn)
+        if with_backward:
+            (weights.sum() + loss).backward()
+        assert node() is not None
+        del ids, weights, counts, loss
+        assert node() is None
+    finally:
+        gc.enable()
