@@ -35,13 +35,14 @@ class _Route(torch.autograd.Function):
         T, E = logits.shape
         logits = logits.contiguous()
         b = moe.RouteBuffers(T, K, E, device=logits.device)
+        b.loss = torch.empty((), dtype=torch.float32, device=logits.device)   # a view could not be scaled in place
         b.run(logits, renormalize, loss_coef, token_mask)
         ctx.settings = renormalize, loss_coef
         # saved, not kept on ctx: an edit in place is then an error in backward,
         # and the outputs are in no cycle with their own node
         ctx.save_for_backward(logits, b.topk_ids, b.expert_counts, b.routed_tokens)
         ctx.mark_non_differentiable(b.topk_ids, b.expert_counts)
-        return b.topk_ids, b.topk_weights, b.expert_counts, b.loss.view(())
+        return b.topk_ids, b.topk_weights, b.expert_counts, b.loss
 
     @staticmethod
     def backward(ctx, _ids, grad_weights, _counts, grad_loss):

@@ -73,6 +73,20 @@ def test_an_edit_of_what_the_gradient_needs_is_an_error(calls, which):
         (weights.sum() + loss).backward()
 
 
+def test_edited_copies_weights_and_losses_are_fine(calls):
+    logits = _logits()
+    ids, weights, _, loss = layer.route(logits, 3, False)
+    ids = ids.masked_fill(ids == 1, -1)
+    weights *= 2.0
+    loss *= 3.0
+    (weights.sum() + loss).backward()
+    a = logits.grad.clone()
+    logits.grad = None
+    _, weights, _, loss = layer.route(logits, 3, False)
+    (2 * weights.sum() + 3 * loss).backward()
+    assert torch.allclose(a, logits.grad, rtol=0, atol=1e-6)
+
+
 @pytest.mark.parametrize("with_backward", [False, True])
 def test_nothing_is_kept_in_a_cycle(calls, with_backward):
     """Buffers and logits go with the last reference, not with the collector."""
