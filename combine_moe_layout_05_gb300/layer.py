@@ -45,6 +45,7 @@ class _Route(torch.autograd.Function):
         return b.topk_ids, b.topk_weights, b.expert_counts, b.loss
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, _ids, grad_weights, _counts, grad_loss):
         logits, ids, counts, routed = ctx.saved_tensors
         grad = torch.empty_like(logits)

@@ -102,3 +102,13 @@ def test_nothing_is_kept_in_a_cycle(calls, with_backward):
         assert node() is None
     finally:
         gc.enable()
+
+
+def test_a_second_derivative_is_an_error(calls):
+    """Not a term that is silently left out."""
+    logits = _logits()
+    _, weights, _, loss = layer.route(logits, 3)
+    total = weights.square().sum() + loss
+    (grad,) = torch.autograd.grad(total, logits, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (total + grad.square().sum()).backward()
