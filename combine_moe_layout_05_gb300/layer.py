@@ -1,9 +1,9 @@
-"""An MoE layer put together from the library's calls, as a serving loop or a
-training step would use them.
+"""An MoE layer put together from the library's calls.
 
 ``route`` is the router with its gradient (moe_route / moe_route_backward under
-autograd).  ``Int8Experts`` is a gated MLP whose experts' weights are int8 with
-a scale for each output channel:
+autograd), for training and serving.  ``Int8Experts``, for serving, is a gated
+MLP whose experts' weights are int8 with a scale for each output channel.  It
+has no gradient, and refuses inputs that ask for one:
 
     moe_layout           slots of the routing
     moe_dispatch_int8    rows to int8, packed by expert
@@ -77,7 +77,10 @@ class Int8Experts:
 
     def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor,
                  topk_weights: torch.Tensor) -> torch.Tensor:
-        """x [T, H] bf16 and its routing to [T, H] bf16."""
+        """x [T, H] bf16 and its routing to [T, H] bf16; under no_grad, or with
+        inputs that do not require a gradient."""
+        if torch.is_grad_enabled() and (x.requires_grad or topk_weights.requires_grad):
+            raise RuntimeError("Int8Experts has no gradient: detach x and topk_weights, or call it under no_grad")
         (T, H), K, dev = x.shape, topk_ids.shape[1], x.device
         rows = T * K
         lay = moe.LayoutBuffers(T, K, self.E, self.R, device=dev).run(topk_ids)

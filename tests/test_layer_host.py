@@ -48,6 +48,63 @@ def calls(monkeypatch):
     monkeypatch.setattr(_binding, "moe_route_workspace_bytes", lambda T, E: 256)
 
 
+class _Experts:
+    """Stand-ins for the layout, int8 and combine calls; `timeouts` are the
+    products (0, 1) whose error word is set."""
+
+    def __init__(self, timeouts=()):
+        self.timeouts, self.products = timeouts, 0
+
+    def layout(self, topk_ids, E, R, expert_counts, expert_offsets, rank_offsets, src_token, dst_row, dev_error=None,
+               workspace=None, stream=None):
+        flat = topk_ids.reshape(-1).long()
+        kept = flat >= 0
+        expert_counts.copy_(torch.bincount(flat[kept], minlength=E))
+        expert_offsets[0] = 0
+        expert_offsets[1:] = torch.cumsum(expert_counts, 0)
+        order = torch.argsort(torch.where(kept, flat, E), stable=True)
+        dst = torch.empty_like(flat)
+        dst[order] = torch.arange(flat.numel())
+        dst_row.copy_(torch.where(kept, dst, -1).view(topk_ids.shape))
+        if dev_error is not None:
+            dev_error.fill_(0 if bool(kept.all()) else _binding.MOE_DEV_ERR_EXPERT_RANGE)
+
+    def dispatch(self, tokens, dst_row, packed, scales, stream=None):
+        for t, k in (dst_row >= 0).nonzero().tolist():
+            scale = tokens[t].float().abs().max() / 127
+            packed[dst_row[t, k]] = (tokens[t].float() / scale).round().to(torch.int8)
+            scales[dst_row[t, k]] = scale
+
+    def product(self, x, x_scales, weights, w_scales, expert_offsets, out, dev_error=None, stream=None):
+        if x.shape[0] == 0:
+            return
+        for e in range(weights.shape[0]):
+            r = slice(int(expert_offsets[e]), int(expert_offsets[e + 1]))
+            y = x[r].float() @ weights[e].float().t()
+            out[r] = (y * x_scales[r, None] * w_scales[e]).to(torch.bfloat16)
+        if dev_error is not None:
+            dev_error.fill_(_binding.MOE_DEV_ERR_TIMEOUT if self.products in self.timeouts else 0)
+        self.products += 1
+
+    def combine(self, expert_out, topk_weights, dst_row, out, stream=None):
+        rows = expert_out[dst_row.clamp(min=0).long()].float() * (dst_row >= 0)[..., None]
+        out.copy_((rows * topk_weights[..., None]).sum(1))
+
+
+@pytest.fixture
+def experts(calls, monkeypatch):
+    def use(timeouts=()):
+        e = _Experts(timeouts)
+        monkeypatch.setattr(_binding, "moe_layout", e.layout)
+        monkeypatch.setattr(_binding, "moe_dispatch_int8", e.dispatch)
+        monkeypatch.setattr(_binding, "moe_expert_matmul_int8", e.product)
+        monkeypatch.setattr(_binding, "moe_combine", e.combine)
+        monkeypatch.setattr(_binding, "moe_layout_workspace_bytes", lambda T, K, E: 256)
+        g = torch.Generator().manual_seed(1)
+        return layer.Int8Experts(torch.randn((10, 32, 16), generator=g), torch.randn((10, 16, 16), generator=g))
+    return use
+
+
 def _logits(T=6, E=10):
     return torch.randn((T, E), generator=torch.Generator().manual_seed(0)).requires_grad_()
 
@@ -112,3 +169,18 @@ def test_a_second_derivative_is_an_error(calls):
     (grad,) = torch.autograd.grad(total, logits, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (total + grad.square().sum()).backward()
+
+
+def test_the_layer_refuses_to_cut_a_graph(experts):
+    """It has no gradient: what would lose one is an error, outside no_grad."""
+    run = experts()
+    x = torch.randn(6, 16).to(torch.bfloat16)
+    ids, weights, _, _ = layer.route(_logits(), 3)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        run(x, ids, weights)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        run(x.clone().requires_grad_(), ids, weights.detach())
+    out = run(x, ids, weights.detach())
+    with torch.no_grad():
+        assert torch.equal(run(x.clone().requires_grad_(), ids, weights), out)
+    assert not out.requires_grad and out.abs().max() > 0
