@@ -65,7 +65,11 @@ def route(logits: torch.Tensor, K: int, renormalize: bool = True, loss_coef: flo
 
 
 class Int8Experts:
-    """The experts of one layer: gate_up [E, 2 I, H] and down [E, H, I]."""
+    """The experts of one layer: gate_up [E, 2 I, H] and down [E, H, I].
+
+    ``dev_error``, [3] int32 on the device, holds the last call's error words:
+    the layout's (MOE_DEV_ERR_EXPERT_RANGE where an id is -1) and the two
+    products', whose MOE_DEV_ERR_TIMEOUT says that the output is unspecified."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, ranks: int = 1):
         E, two_i, H = gate_up.shape
@@ -74,6 +78,7 @@ class Int8Experts:
         self.E, self.H, self.I, self.R = E, H, two_i // 2, ranks
         self.gate_up, self.gate_up_scales = quantize_channels(gate_up)
         self.down, self.down_scales = quantize_channels(down)
+        self.dev_error = None
 
     def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor,
                  topk_weights: torch.Tensor) -> torch.Tensor:
@@ -83,20 +88,24 @@ class Int8Experts:
             raise RuntimeError("Int8Experts has no gradient: detach x and topk_weights, or call it under no_grad")
         (T, H), K, dev = x.shape, topk_ids.shape[1], x.device
         rows = T * K
-        lay = moe.LayoutBuffers(T, K, self.E, self.R, device=dev).run(topk_ids)
+        # every call has words of its own; products of no rows do not write theirs
+        self.dev_error = err = (torch.empty if rows else torch.zeros)(3, dtype=torch.int32, device=dev)
+        lay = moe.LayoutBuffers(T, K, self.E, self.R, device=dev)
+        lay.dev_error = err[:1]
+        lay.run(topk_ids)
         codes = torch.empty((rows, H), dtype=torch.int8, device=dev)
         scales = torch.empty(rows, dtype=torch.float32, device=dev)
         moe.moe_dispatch_int8(x, lay.dst_row, codes, scales)
         mid = torch.empty((rows, 2 * self.I), dtype=torch.bfloat16, device=dev)
         moe.moe_expert_matmul_int8(codes, scales, self.gate_up, self.gate_up_scales,
-                                   lay.expert_offsets, mid)
+                                   lay.expert_offsets, mid, err[1:2])
         act = torch.nn.functional.silu(mid[:, :self.I]) * mid[:, self.I:]
         codes = torch.empty((rows, self.I), dtype=torch.int8, device=dev)
         same = torch.arange(rows, dtype=torch.int32, device=dev).view(rows, 1)
         moe.moe_dispatch_int8(act, same, codes, scales)
         out_rows = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
         moe.moe_expert_matmul_int8(codes, scales, self.down, self.down_scales,
-                                   lay.expert_offsets, out_rows)
+                                   lay.expert_offsets, out_rows, err[2:])
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         moe.moe_combine(out_rows, topk_weights, lay.dst_row, out)
         return out

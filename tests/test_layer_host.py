@@ -184,3 +184,23 @@ def test_the_layer_refuses_to_cut_a_graph(experts):
     with torch.no_grad():
         assert torch.equal(run(x.clone().requires_grad_(), ids, weights), out)
     assert not out.requires_grad and out.abs().max() > 0
+
+
+@pytest.mark.parametrize("timeouts", [(), (0,), (1,), (0, 1)])
+@pytest.mark.parametrize("dropped", [False, True])
+def test_the_layer_keeps_every_error_word(experts, timeouts, dropped):
+    """A wait that expired in either product, and the layout's word, can be read after the call."""
+    run = experts(timeouts)
+    ids, weights, _, _ = layer.route(_logits().detach(), 3)
+    if dropped:
+        ids = ids.masked_fill(ids == 1, -1)
+    run(torch.randn(6, 16).to(torch.bfloat16), ids, weights)
+    words = [_binding.MOE_DEV_ERR_EXPERT_RANGE if dropped else 0]
+    words += [_binding.MOE_DEV_ERR_TIMEOUT if p in timeouts else 0 for p in (0, 1)]
+    assert run.dev_error.dtype == torch.int32 and run.dev_error.tolist() == words
+
+
+def test_the_error_words_of_no_token(experts):
+    run = experts()
+    out = run(torch.empty((0, 16), dtype=torch.bfloat16), torch.empty((0, 3), dtype=torch.int32), torch.empty((0, 3)))
+    assert out.shape == (0, 16) and run.dev_error.tolist() == [0, 0, 0]
