@@ -38,9 +38,13 @@ moe_status_t rows_ok(int32_t T, int32_t H, int32_t K)
     return MOE_OK;
 }
 
+// Most tokens, rows and channels of the calls whose kernels step through them
+// in 32 bits: room for a grid's stride (6080 tokens) or a tile past the last.
+constexpr int32_t kMostSteps = INT32_MAX - 65535;
+
 bool route_sizes_ok(int32_t T, int32_t E, int32_t K)
 {
-    return T >= 0 && E >= 1 && E <= MOE_MAX_EXPERTS && K >= 1 && K <= MOE_MAX_TOPK && K <= E &&
+    return T >= 0 && T <= kMostSteps && E >= 1 && E <= MOE_MAX_EXPERTS && K >= 1 && K <= MOE_MAX_TOPK && K <= E &&
            (int64_t)T * K <= (int64_t)INT32_MAX - 1;
 }
 
@@ -274,7 +278,7 @@ int32_t moe_layout_kernels(int32_t T, int32_t K, int32_t E)
 
 size_t moe_route_workspace_bytes(int32_t T, int32_t E)
 {
-    if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS) return 0;
+    if (T < 0 || T > kMostSteps || E < 1 || E > MOE_MAX_EXPERTS) return 0;
     return moe::route_workspace_bytes(T, E);
 }
 
@@ -340,8 +344,8 @@ moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales, const 
                                     uint32_t *dev_error, cudaStream_t stream)
 {
     const CallRange range("moe_expert_matmul_int8");
-    if (rows < 0 || H < 16 || H > 65536 || H % 16 != 0 || N < 1 || E < 1 || E > MOE_MAX_EXPERTS ||
-        (int64_t)E * N > (int64_t)INT32_MAX)
+    if (rows < 0 || rows > kMostSteps || H < 16 || H > 65536 || H % 16 != 0 || N < 1 || E < 1 ||
+        E > MOE_MAX_EXPERTS || (int64_t)E * N > (int64_t)kMostSteps)
         return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!x || !x_scales || !weights || !w_scales || !expert_offsets || !out) return MOE_ERR_INVALID_ARG;

@@ -391,9 +391,9 @@ MOE_API moe_status_t moe_layout_static(const int32_t *topk_ids, int32_t T, int32
  * routed_tokens [1] int32, loss [1] fp32: 4-byte aligned.
  * workspace   moe_route_workspace_bytes(T,E) bytes (never 0 for valid sizes),
  *             16-byte aligned; its contents on entry do not matter.
- * T >= 0, 1 <= E <= MOE_MAX_EXPERTS, 1 <= K <= min(E, MOE_MAX_TOPK),
- * T*K < 2^31.  T == 0 writes zero counts and loss.  Asynchronous on `stream`;
- * may be captured.
+ * 0 <= T <= 2^31 - 65536, 1 <= E <= MOE_MAX_EXPERTS,
+ * 1 <= K <= min(E, MOE_MAX_TOPK), T*K < 2^31 - 1.  T == 0 writes zero counts and
+ * loss.  Asynchronous on `stream`; may be captured.
  */
 MOE_API size_t moe_route_workspace_bytes(int32_t T, int32_t E);
 
@@ -480,9 +480,9 @@ MOE_API moe_status_t moe_dispatch_int8(const void *tokens, int32_t T, int32_t H,
  * dev_error      [1] uint32 or NULL.  Overwritten with 0, or with
  *                MOE_DEV_ERR_TIMEOUT when a bounded wait (2 s) between the
  *                kernel's warps expired; the outputs are then unspecified.
- * rows >= 0, 16 <= H <= 65536 with H % 16 == 0, N >= 1, E*N < 2^31,
- * 1 <= E <= MOE_MAX_EXPERTS.  rows == 0 is a no-op.  Asynchronous on `stream`;
- * may be captured.
+ * 0 <= rows <= 2^31 - 65536, 16 <= H <= 65536 with H % 16 == 0, N >= 1,
+ * E*N <= 2^31 - 65536, 1 <= E <= MOE_MAX_EXPERTS.  rows == 0 is a no-op.
+ * Asynchronous on `stream`; may be captured.
  */
 MOE_API moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales,
                                             const void *weights, const float *w_scales,
