@@ -216,12 +216,23 @@ __device__ __forceinline__ void mma_slot_n(uint32_t acc, uint32_t a, uint64_t b,
         mma_f16_ts<S::CG>(acc, a + 8 * q, b + (q >> 2) * (S::BR * 128 / 16) + (q & 3) * 2, idesc, accumulate || q > 0);
 }
 
+// The barrier that a test holds back in the first tile's CTAs: the first of a
+// kind (0 to 6), or none.
+template <typename S>
+__device__ __forceinline__ int stalled_barrier(int kind)
+{
+    if (kind < 0 || kind >= 6 + S::SPLIT) return -1;
+    if (kind < 4) return (kind > 0 ? S::N8 : 0) + (kind > 1 ? S::N8 : 0) + (kind > 2 ? S::NC : 0);
+    return 2 * S::N8 + 2 * S::NC + (kind == 4 ? 0 : kind == 5 ? 2 : 5);
+}
+
 template <typename S>
 __global__ void __launch_bounds__(S::THREADS, 1)
 expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x,
                           const float *__restrict__ x_scales, const float *__restrict__ w_scales,
                           const int32_t *__restrict__ offsets, int rows, int H, int N, int E,
-                          __nv_bfloat16 *__restrict__ out, uint32_t *__restrict__ dev_error)
+                          __nv_bfloat16 *__restrict__ out, uint32_t *__restrict__ dev_error,
+                          long long wait_limit, int stall)
 {
     extern __shared__ __align__(1024) uint8_t generic[];   // the swizzle is of addresses; no other shared arrays
     const uint32_t base = smem_addr(generic);
@@ -239,22 +250,31 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     // SPLIT: which share of the contraction is this CTA's, of how many
     const int parts = S::SPLIT ? cluster_size() : 1, part = S::SPLIT ? (int)uniform(cluster_rank()) : 0;
     uint32_t *const flags = reinterpret_cast<uint32_t *>(generic + S::OFFBAR + (S::BARS * 8 + 15) / 16 * 16);
-    volatile int *const abort = reinterpret_cast<volatile int *>(flags + 1);
+    WaitState *const waits = reinterpret_cast<WaitState *>(flags + 2);
+    const int group = blockIdx.x / (S::CG * parts), groups = gridDim.x / (S::CG * parts);
     int *const first_row = reinterpret_cast<int *>(generic + S::OFFTAB);
     int *const first_tile = first_row + E + 1;
 
     if (tid == 0) {
         prefetch_map(&map_w);
         for (int m = 0; kLeastBox << m <= S::BR; ++m) prefetch_map(&map_x.box[m]);
-        uint64_t *b = reinterpret_cast<uint64_t *>(generic + S::OFFBAR);
-        for (int i = 0; i < S::N8; ++i) mbar_init(b + i, 1), mbar_init(b + S::N8 + i, 4 + S::WB);
-        b += 2 * S::N8;
-        for (int i = 0; i < S::NC; ++i) mbar_init(b + i, (4 + S::WB) * S::CG), mbar_init(b + S::NC + i, 1);
-        b += 2 * S::NC;
-        for (int i = 0; i < 2; ++i) mbar_init(b + i, 1), mbar_init(b + 2 + i, 4 * S::SETS * S::CG);
-        mbar_init(b + 4, 1);
-        if (S::SPLIT) mbar_init(b + 5, 4 * parts);
-        *abort = 0;
+        // a stalled barrier expects one arrival more than it gets
+        const int held = group == 0 ? stalled_barrier<S>(stall) : -1;
+        int at = 0;
+        auto init = [&](int barriers, uint32_t arrivals) {
+            for (int i = 0; i < barriers; ++i, ++at)
+                mbar_init(reinterpret_cast<uint64_t *>(generic + S::OFFBAR) + at, arrivals + (at == held));
+        };
+        init(S::N8, 1);
+        init(S::N8, 4 + S::WB);
+        init(S::NC, (4 + S::WB) * S::CG);
+        init(S::NC, 1);
+        init(2, 1);
+        init(2, 4 * S::SETS * S::CG);
+        init(1, 1);
+        if (S::SPLIT) init(1, 4 * parts);
+        waits->limit = wait_limit;
+        waits->abort = 0;
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc<S::CG>(smem_addr(flags), kTmemColumns);
@@ -305,7 +325,6 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     const int steps = all_steps * (part + 1) / parts - step0;
     const int slots = S::SPLIT ? steps : ceil_div(H, S::KS), h0 = step0 * kStep;
     uint64_t *const bars = reinterpret_cast<uint64_t *>(generic + S::OFFBAR);
-    const int group = blockIdx.x / (S::CG * parts), groups = gridDim.x / (S::CG * parts);
 
     if (warp == 0) {
         int issued = 0, at = 0;
@@ -319,7 +338,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
             const uint32_t bytes = S::A8 + (kLeastBox << m) * kStep;
             for (int k = 0; k < steps; ++k, ++issued) {
                 const int s = issued % S::N8;
-                ok = __all_sync(kFullMask, mbar_wait_bounded(empty8(s), (issued / S::N8 & 1) ^ 1, abort));
+                ok = __all_sync(kFullMask, mbar_wait_bounded(empty8(s), (issued / S::N8 & 1) ^ 1, waits));
                 if (!ok) break;
                 const uint32_t slot = base + s * S::SLOT8;
                 if (elect_one()) {
@@ -330,9 +349,9 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 __syncwarp();
             }
         }
-        if (!ok)                                       // the copies in flight land first
-            for (int j = max(0, issued - S::N8); j < issued; ++j)
-                mbar_drain_bounded(full8(j % S::N8), j / S::N8 & 1);
+        // The copies in flight land first: if another warp gave up, nobody else waits for them.
+        for (int j = max(0, issued - S::N8); j < issued; ++j)
+            mbar_drain_bounded(full8(j % S::N8), j / S::N8 & 1, waits);
     } else if (warp == 1) {
         if (rank == 0) {
             int c = 0, cphase = 0;                     // slot of widened operands
@@ -342,11 +361,11 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
             const int last = min(kFull, (H - h0 - (slots - 1) * S::KS) >> 4);        // and in the last one
             bool ok = true;
             auto wait_free = [&](int v) {
-                ok = __all_sync(kFullMask, mbar_wait_bounded(empty_d(v & 1), (v >> 1 & 1) ^ 1, abort));
+                ok = __all_sync(kFullMask, mbar_wait_bounded(empty_d(v & 1), (v >> 1 & 1) ^ 1, waits));
                 tc_fence_after();
             };
             auto wait_slot = [&](int s, int phase) {
-                ok = __all_sync(kFullMask, mbar_wait_bounded(full16(s), phase, abort));
+                ok = __all_sync(kFullMask, mbar_wait_bounded(full16(s), phase, waits));
                 tc_fence_after();
             };
             for (int i = group; i < items && ok; i += groups) {
@@ -439,15 +458,13 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 }
                 u += S::PARTS;
             }
+            // all that was issued, given up or not: the widening warps of both CTAs wait for it
+            if (elect_one()) mma_commit<S::CG>(drained);
+            __syncwarp();
             // The storing warps' last arrivals come from the other CTA too and must
             // find this one's barriers here: it leaves after they are in.
             for (int v = max(0, u - 2); v < u && ok; ++v)
-                ok = __all_sync(kFullMask, mbar_wait_bounded(empty_d(v & 1), v >> 1 & 1, abort));
-            if (!ok) {                                 // what was issued finishes first
-                if (elect_one()) mma_commit<S::CG>(drained);
-                __syncwarp();
-                mbar_drain_bounded(drained, 0);
-            }
+                ok = __all_sync(kFullMask, mbar_wait_bounded(empty_d(v & 1), v >> 1 & 1, waits));
         }
     } else if (warp >= S::E0 && warp < S::B0) {
         // set by set, 16 rows at a time
@@ -488,7 +505,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
             const bool vectors = N % 8 == 0;
             for (int p = 0; p < S::PARTS && ok; ++p, ++u) {
                 const int d = u & 1, n = t.n[p], mine = n / S::CG;
-                ok = __all_sync(kFullMask, mbar_wait_bounded(full_d(d), u >> 1 & 1, abort));
+                ok = __all_sync(kFullMask, mbar_wait_bounded(full_d(d), u >> 1 & 1, waits));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + d * S::UNIT + ((uint32_t)quarter << 21);
@@ -515,7 +532,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                     if (lane == 0) mbar_arrive(bars + 2 * S::N8 + 2 * S::NC + 2 + d);
                     if (lane < parts) mbar_arrive_release(cluster_addr(box_full, lane));
                     __syncwarp();
-                    ok = __all_sync(kFullMask, mbar_wait_bounded(box_full, 0, abort));
+                    ok = __all_sync(kFullMask, mbar_wait_bounded(box_full, 0, waits));
                     if (!ok) break;
                     const int ch = ch0 + lane;
                     const float scale = ch < N ? w_scales[(size_t)t.e * N + ch] : 0.0f;
@@ -613,7 +630,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
         for (int i = group; i < items && ok; i += groups, n0 += steps, m0 += slots)
             for (int k = (g + S::GA - n0 % S::GA) % S::GA; k < steps && ok; k += S::GA) {
                 const int n = n0 + k, s = n % S::N8;
-                ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, abort));
+                ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, waits));
                 const uint32_t src = row + s * S::SLOT8;
 #pragma unroll 1
                 for (int h = 0; h < S::PER; ++h) {
@@ -627,7 +644,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
 #pragma unroll
                         for (int q = 0; q < 4; ++q) widen16(lds128(half ^ (4 * w + q) << 4), v + 8 * q);
                         if (w == 0) {
-                            ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, abort));
+                            ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, waits));
                             if (!ok) break;
                             tc_fence_after();
                         }
@@ -643,7 +660,9 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                 if (lane == 0) mbar_arrive(bars + S::N8 + s);
             }
         for (int j = max(0, m0 - S::NC); j < m0 && ok; ++j)           // the last slots' arrivals are in
-            ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(j % S::NC), j / S::NC & 1, abort));
+            ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(j % S::NC), j / S::NC & 1, waits));
+        // What was issued finishes first, whoever gave up: it uses the TMEM and the memory of both CTAs.
+        mbar_drain_bounded(drained, 0, waits);
     } else if (warp >= S::B0 && warp < S::B0 + S::WB * S::GB) {
         // rows: group `g` has every GB-th step; a warp takes 8 rows by 64 bytes at
         // a time, a thread 16 bytes, so that few rows are spread over all warps
@@ -655,7 +674,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
             const int blocks = (t.n[0] + t.n[1]) / (8 * S::CG);
             for (int k = (g + S::GB - n0 % S::GB) % S::GB; k < steps && ok; k += S::GB) {
                 const int n = n0 + k, s = n % S::N8;
-                ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, abort));
+                ok = __all_sync(kFullMask, mbar_wait_bounded(full8(s), n / S::N8 & 1, waits));
                 const uint32_t src = base + s * S::SLOT8 + S::A8;
 #pragma unroll 1
                 for (int h = 0; h < S::PER; ++h) {
@@ -673,7 +692,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
                             const int r = 8 * block + (lane & 7), q = 4 * (h + half) + (lane >> 3);
                             widen16(lds128(src + r * kStep + ((q ^ (r & 7)) << 4)), v[j]);
                         }
-                        ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, abort));
+                        ok = __all_sync(kFullMask, mbar_wait_bounded(empty16(c), (m / S::NC & 1) ^ 1, waits));
                         if (!ok) return;
 #pragma unroll
                         for (int j = 0; j < U; ++j) {
@@ -705,7 +724,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     __syncthreads();
     if constexpr (S::CG == 2 || S::SPLIT) cluster_sync_all();      // the peer is done with this CTA's memory
     tc_fence_after();
-    if (tid == 0 && *abort && dev_error) atomicOr(dev_error, MOE_DEV_ERR_TIMEOUT);
+    if (tid == 0 && waits->abort && dev_error) atomicOr(dev_error, MOE_DEV_ERR_TIMEOUT);
     if (warp == 1) tmem_free<S::CG>(tmem, kTmemColumns);
 }
 
@@ -749,7 +768,7 @@ int64_t most_tiles(int rows, int N, int E)
 template <typename S>
 cudaError_t run(const void *x, const float *x_scales, const void *w, const float *w_scales,
                 const int32_t *offsets, int rows, int H, int N, int E, int sms, int parts, void *out,
-                uint32_t *dev_error, cudaStream_t stream)
+                uint32_t *dev_error, long long wait_limit, int stall, cudaStream_t stream)
 {
     CUtensorMap map_w;
     RowMaps map_x;
@@ -764,7 +783,7 @@ cudaError_t run(const void *x, const float *x_scales, const void *w, const float
     const int64_t groups = tiles < sms / (S::CG * parts) ? tiles : sms / (S::CG * parts);
     return launch_pdl_clusters(expert_matmul_int8_kernel<S>, dim3((unsigned)groups * S::CG * parts), dim3(S::THREADS),
                                smem, stream, S::CG * parts, map_w, map_x, x_scales, w_scales, offsets, rows, H, N, E,
-                               static_cast<__nv_bfloat16 *>(out), dev_error);
+                               static_cast<__nv_bfloat16 *>(out), dev_error, wait_limit, stall);
 }
 
 // Clusters of 2, 4 and 8 splitting CTAs that the current device runs at a time,
@@ -809,14 +828,15 @@ cudaError_t split_clusters(int (&clusters)[3])
 cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, const void *w,
                                       const float *w_scales, const int32_t *offsets, int rows,
                                       int H, int N, int E, void *out, uint32_t *dev_error,
-                                      cudaStream_t stream)
+                                      cudaStream_t stream, int64_t wait_cycles, int stall)
 {
+    const long long wait_limit = wait_cycles > 0 ? wait_cycles : kWaitLimitCycles;
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
     auto go = [&](auto shape, int parts) {
         return run<decltype(shape)>(x, x_scales, w, w_scales, offsets, rows, H, N, E, sms, parts, out, dev_error,
-                                    stream);
+                                    wait_limit, stall, stream);
     };
     // Few tiles: share the contraction, as far as every tile's cluster runs at
     // once and the steps saved outweigh the cluster's barriers (30 tiles of 4272:
@@ -843,3 +863,23 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
 }
 
 }  // namespace moe
+
+// Test hook, deliberately absent from the public header: the product with a
+// chosen bound on every wait (in clock cycles; 0: the default) and, in the
+// CTAs of the first tiles, one barrier that waits for an arrival that never
+// comes: stall 0 a tile's bytes in shared memory, 1 their slot free again, 2
+// widened operands, 3 their slot free again, 4 sums ready, 5 sums stored, 6 the
+// other CTAs' sums (where the contraction is split); anything else none.  A
+// test uses it to see a bounded wait expire: the kernel sets
+// MOE_DEV_ERR_TIMEOUT and finishes, and the context stays usable.  Arguments
+// are checked by the caller (tests only).
+extern "C" __attribute__((visibility("default"))) int32_t
+moe_testing_expert_matmul_int8(const void *x, const float *x_scales, const void *weights,
+                               const float *w_scales, const int32_t *expert_offsets, int32_t rows,
+                               int32_t H, int32_t N, int32_t E, void *out, uint32_t *dev_error,
+                               int64_t wait_cycles, int32_t stall, cudaStream_t stream)
+{
+    const cudaError_t e = moe::launch_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, rows, H, N, E,
+                                                         out, dev_error, stream, wait_cycles, stall);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -104,11 +104,12 @@ cudaError_t launch_dispatch_recv(const void *priv, const float *priv_scales, int
 cudaError_t launch_dispatch_int8(const void *tokens, int T, int H, int K, const int32_t *dst_row,
                                  void *packed, float *scales, cudaStream_t stream);
 
-// Packed int8 rows times their experts' int8 weights.
+// Packed int8 rows times their experts' int8 weights.  wait_cycles > 0 bounds
+// every wait, and stall >= 0 holds one kind of barrier back (tests only).
 cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, const void *w,
                                       const float *w_scales, const int32_t *offsets, int rows,
                                       int H, int N, int E, void *out, uint32_t *dev_error,
-                                      cudaStream_t stream);
+                                      cudaStream_t stream, int64_t wait_cycles = 0, int stall = -1);
 
 // Router logits (bf16 != 0: bf16, else fp32) to ids, weights, counts and the
 // balance loss; and the gradient back to the logits.

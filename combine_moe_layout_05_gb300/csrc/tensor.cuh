@@ -17,6 +17,13 @@ namespace moe {
 // a read of the nanosecond timer takes long enough to delay every wait.
 constexpr long long kWaitLimitCycles = 4000000000ll;
 
+// A block's, in its shared memory: how long a wait may take, and whether one
+// took longer.
+struct WaitState {
+    long long limit;
+    volatile int abort;
+};
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -110,32 +117,33 @@ __device__ __forceinline__ bool mbar_sleep_cluster(uint32_t bar, uint32_t parity
     return done != 0;
 }
 
-// Waits for the phase of `bar` with the given parity; false, and *abort set,
+// Waits for the phase of `bar` with the given parity; false, and w->abort set,
 // when the limit passed or another thread of the block gave up.  Once, not
 // inline: the kernel's warps run different loops, which together have to stay
 // in the instruction cache.
-static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort)
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, WaitState *w)
 {
-    const long long start = clock64();
+    const long long start = clock64(), limit = w->limit;
     while (!mbar_sleep_cluster(bar, parity))
-        if (*abort || clock64() - start > kWaitLimitCycles) {
-            *abort = 1;
+        if (w->abort || clock64() - start > limit) {
+            w->abort = 1;
             return false;
         }
     return true;
 }
 
-__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort)
+__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, WaitState *w)
 {
-    return mbar_sleep_cluster(bar, parity) || mbar_wait_long(bar, parity, abort);
+    return mbar_sleep_cluster(bar, parity) || mbar_wait_long(bar, parity, w);
 }
 
-// The same for a copy or a matrix instruction in flight while giving up.
-__device__ __forceinline__ void mbar_drain_bounded(uint32_t bar, uint32_t parity)
+// The same for a copy or matrix instructions in flight, which have to land
+// before the block leaves, whether it gave up or not.
+__device__ __forceinline__ void mbar_drain_bounded(uint32_t bar, uint32_t parity, const WaitState *w)
 {
-    const long long start = clock64();
+    const long long start = clock64(), limit = w->limit;
     while (!mbar_sleep_cluster(bar, parity))
-        if (clock64() - start > kWaitLimitCycles) return;
+        if (clock64() - start > limit) return;
 }
 
 // Tile of a two-dimensional tensor at (column c, row r) to shared memory;
