@@ -455,6 +455,8 @@ def moe_route(logits, topk_ids, topk_weights, expert_counts, routed_tokens, loss
     if topk_ids.numel() != T * K or topk_weights.numel() != T * K or expert_counts.numel() < E \
             or routed_tokens.numel() < 1 or loss.numel() < 1:
         raise ValueError("moe_route: output arrays have the wrong size")
+    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("moe_route: workspace must be a contiguous CUDA tensor")
     st = (_lib or load()).moe_route(
         logits.data_ptr(), bf16, T, E, K, 1 if renormalize else 0, loss_coef, _ptr(token_mask),
         topk_ids.data_ptr(), topk_weights.data_ptr(), expert_counts.data_ptr(),
