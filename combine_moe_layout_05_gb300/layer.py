@@ -25,7 +25,7 @@ def quantize_channels(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     largest magnitude becomes 127.  Done once, when the weights are loaded."""
     w = w.float()
     scale = w.abs().amax(dim=2) / 127.0
-    q = torch.round(w / scale.clamp(min=torch.finfo(torch.float32).tiny)[..., None])
+    q = torch.round(w / torch.where(scale == 0, 1.0, scale)[..., None])
     return q.clamp_(-127, 127).to(torch.int8), scale
 
 

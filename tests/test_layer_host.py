@@ -204,3 +204,17 @@ def test_the_error_words_of_no_token(experts):
     run = experts()
     out = run(torch.empty((0, 16), dtype=torch.bfloat16), torch.empty((0, 3), dtype=torch.int32), torch.empty((0, 3)))
     assert out.shape == (0, 16) and run.dev_error.tolist() == [0, 0, 0]
+
+
+def test_channels_are_quantised_whatever_their_size():
+    """127 codes either side of zero, from the largest channels to ones whose
+    scale is subnormal; a channel of zeros has scale 0 and codes 0.  A weight is
+    its code times the scale to half a scale, and the scale's own rounding (at
+    most 2^-150) 127 times."""
+    g = torch.Generator().manual_seed(2)
+    w = torch.randn((1, 6, 64), generator=g)
+    w *= torch.tensor([1e30, 1.0, 1e-30, 1e-36, 1e-38, 0.0])[None, :, None]
+    q, scale = layer.quantize_channels(w)
+    assert q.abs().amax(2).tolist() == [[127] * 5 + [0]] and scale[0, 5] == 0
+    back = q.double() * scale.double()[..., None]
+    assert bool(((back - w.double()).abs() <= 0.5001 * scale.double()[..., None] + 128 * 2.0 ** -150).all())
