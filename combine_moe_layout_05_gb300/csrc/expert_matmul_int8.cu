@@ -7,8 +7,9 @@
 // sm_103a has no 8-bit integer matrix instruction of the tcgen05 kind, and an
 // int8 value is exactly a fp16 value: the codes travel as bytes through HBM,
 // L2 and the copies into shared memory, and are widened on the way to the
-// fp16 tensor cores.  A product is below 2^14 and the fp32 accumulator exact
-// up to 2^24, so the sum is the integer's while partial sums stay below that.
+// fp16 tensor cores.  A product is at most 2^14 and the fp32 accumulator exact
+// up to 2^24, so the sum is the integer's while partial sums stay below that;
+// past it the accumulator rounds or truncates to 24 bits at each instruction.
 //
 // A tile is 128 channels a CTA (256 a pair of CTAs) by up to NT rows of one
 // expert.  Channels are the instruction's M, so that a tile with few rows
@@ -82,7 +83,8 @@ struct Shape {
     static_assert(BR * (KS / 64) <= 8 * WB * 4);
     // Sets of four warps that store, two where a tile has more than 32 rows: a
     // short contraction waits for them (64 experts of 128 rows, 512 -> 4096, in
-    // the 128-row form: 63.8 us with one set, 53.7 with two).
+    // the 128-row form: 63.8 us with one set, 56.7 with two, and 53.7 since they
+    // multiply in pairs and keep the scales of their own rows only).
     static constexpr int SETS = CG;
     static constexpr int A0 = 4, E0 = A0 + 4 * GA, B0 = E0 + 4 * SETS, WARPS = B0 + WB * GB;
     static constexpr int THREADS = WARPS * 32;
@@ -852,12 +854,13 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
             if (tiles <= clusters[p / 4]) parts = p;
         if (parts > 1) return go(Split{}, parts);
     }
-    // By rows an expert.  Narrow and Mid: 56.3 and 58.1 us at 8 (15 experts,
-    // 6208 -> 3586), 93 and 53 us at 64 (64, 1024 -> 4096).  Mid and Wide: 68 and
-    // 77 us at 128 (64, 2048 -> 2048), 248 and 232 us at 384 (32, 7168 -> 2048),
-    // 667 and 638 us at 1024 (64, 4096 -> 2048).  A short contraction leaves Wide
-    // waiting for its stores, which Mid's alternate accumulators hide: 300 and
-    // 321 us (64 experts of 1024 rows, 512 -> 4096), equal at 2560.
+    // By rows an expert, on average; up to 16 measured with even counts only.
+    // Narrow and Mid: 56.3 and 58.1 us at 8 (15 experts, 6208 -> 3586), 93 and 53
+    // us at 64 (64, 1024 -> 4096).  Mid and Wide: 68 and 77 us at 128 (64, 2048 ->
+    // 2048), 248 and 232 us at 384 (32, 7168 -> 2048), 667 and 638 us at 1024 (64,
+    // 4096 -> 2048).  A short contraction leaves Wide waiting for its stores, which
+    // Mid's alternate accumulators hide: 300 and 321 us (64 experts of 1024 rows,
+    // 512 -> 4096), equal at 2560.
     if (rows <= 16 * E) return go(Narrow{}, 1);
     return rows >= 384 * E && steps >= 20 ? go(Wide{}, 1) : go(Mid{}, 1);
 }

@@ -18,11 +18,13 @@
 // memory) and cluster by cluster at the end, always in that order, so a call's
 // results do not depend on timing.
 //
-// Bound by issue slots, not bytes: about 330 instructions a token at E = 128,
-// K = 8, of which the picks are half.  16384 x 128 fp32: 14.1 us, of which the
-// loop 4.8, the sums 1.5, the finishing kernel 2 and the two launches the rest;
-// one token of 256 experts: 3.5 us.  Sixteen warps a block, two blocks a
-// multiprocessor (three: 17.7 against 16.6 us then).
+// Bound by latency, of two dependent launches first: 16384 x 128 fp32 takes 14.1
+// us, of which the loop 4.8, the sums 1.5, the finishing kernel 2 and the two
+// launches the rest; one token of 256 experts: 3.5 us.  In the loop the issue
+// slots weigh most (338 instructions a token at E = 128, K = 8, half of them the
+// picks; 61 % of the slots of active cycles, a third of the kernel's), the bytes
+// least.  Sixteen warps a block, two blocks a multiprocessor (three: 17.7 against
+// 16.6 us then).
 #include "route_common.cuh"
 #include "tensor.cuh"
 
@@ -354,8 +356,10 @@ cudaError_t run_forward(const void *logits, int T, int E, int K, int renorm, flo
     const size_t smem = ((size_t)(kRouteWarps + 1) * E + 1 + 2 * (E + kSingleCluster) + kSingleCluster) * 4;
     const RouteOut o{counts, routed, loss, coef};
     const int single = single_blocks(T, E);
-    // K = 8, the models' usual, has its own form with the picks unrolled (16384 x
-    // 128: 14.0 us, 16.4 with a test of K at each); rows read value by value not
+    // K = 8, the models' usual, has its own form with the picks unrolled (8192
+    // tokens, unrolled and not: E = 64 9.8 and 10.9 us, 128 10.1 and 11.1, 256 13.5
+    // and 14.4, 384 16.4 and 17.5, 512 25.6 and 27.8, 1000 68.1 and 69.8; bf16 gains
+    // as much); rows read value by value not
     constexpr int KT = W > 1 ? 8 : 0;
     auto *const kernel = K == KT ? single ? route_kernel<NV, W, KT, true, L> : route_kernel<NV, W, KT, false, L>
                                 : single ? route_kernel<NV, W, 0, true, L> : route_kernel<NV, W, 0, false, L>;

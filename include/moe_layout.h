@@ -367,7 +367,7 @@ MOE_API moe_status_t moe_layout_static(const int32_t *topk_ids, int32_t T, int32
  * not -inf; a token with an open expert is routed.  With x the logits:
  *
  *   p[t,e]  = exp(x[t,e] - m_t) / sum over open e' of exp(x[t,e'] - m_t),
- *             0 for an expert that is not open
+ *             0 for an expert that is not open or whose exp is below 2^-126
  *   topk_ids[t,:]      the K open experts of largest logit, largest first, ties
  *                      to the lowest index; -1 where fewer than K are open
  *   topk_weights[t,k]  p at topk_ids[t,k], divided by the sum of the token's K
@@ -467,9 +467,11 @@ MOE_API moe_status_t moe_dispatch_int8(const void *tokens, int32_t T, int32_t H,
  *   s = sum over h of x[r,h] * weights[e,n,h]
  *   out[r,n] = bf16(float(s) * x_scales[r] * w_scales[e,n])      (RN, ties to even)
  *
- * s is exact while its partial sums stay below 2^24, else rounded to fp32 as
- * it is summed.  Rows outside all experts' ranges are not written.  E == 1 with
- * offsets {0, rows} is the plain matrix product.
+ * s is exact while its partial sums stay below 2^24.  Past that each step of the
+ * sum (16 terms) may round or truncate to 24 bits: its error is then at most
+ * 2^-23 of the sum of the terms' magnitudes for every 16 terms.  Rows outside
+ * all experts' ranges are not written.  E == 1 with offsets {0, rows} is the
+ * plain matrix product.
  *
  * x              [rows,H] int8, 16-byte aligned.   x_scales [rows] fp32.
  * weights        [E,N,H] int8, 16-byte aligned (a channel's H values together).
