@@ -91,6 +91,14 @@ def load(path: str | None = None):
             lib.moe_dispatch_int8.restype = ctypes.c_int
             lib.moe_expert_matmul_int8.argtypes = [P, P, P, P, P, i32, i32, i32, i32, P, P, P]
             lib.moe_expert_matmul_int8.restype = ctypes.c_int
+            lib.moe_expert_matmul.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, P, P, P, P, P]
+            lib.moe_expert_matmul.restype = ctypes.c_int
+            lib.moe_expert_activation_backward_workspace_bytes.argtypes = [i32, i32, i32]
+            lib.moe_expert_activation_backward_workspace_bytes.restype = sz
+            lib.moe_expert_activation_backward.argtypes = [P, P, P, i32, i32, i32, i32, P, P, P, sz, P]
+            lib.moe_expert_activation_backward.restype = ctypes.c_int
+            lib.moe_expert_matmul_backward.argtypes = [P, P, P, P, i32, i32, i32, i32, P, P, i32, i32, P, P]
+            lib.moe_expert_matmul_backward.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -416,6 +424,114 @@ def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
         _current_stream() if stream is None else _stream(stream))
     if st:
         _raise("moe_expert_matmul_int8", st)
+
+
+MOE_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
+
+
+def _activation(fn: str, name: str) -> int:
+    code = MOE_ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"{fn}: activation must be one of {sorted(MOE_ACTIVATIONS)}, got {name!r}")
+    return code
+
+
+def moe_expert_matmul(x, weights, expert_offsets, out, bias=None, activation: str = "none",
+                      residual=None, pre=None, dev_error=None, stream=None) -> None:
+    """Packed bf16 rows times their experts' weights, with bias, activation and
+    residual in the same pass (see include/moe_layout.h)."""
+    rows, H = x.shape
+    act = _activation("moe_expert_matmul", activation)
+    if not (x.dtype is _bf16 and x.is_cuda and x.is_contiguous()
+            and weights.dtype is _bf16 and weights.is_cuda and weights.is_contiguous()
+            and expert_offsets.dtype is _i32 and expert_offsets.is_cuda and expert_offsets.is_contiguous()
+            and out.dtype is _bf16 and out.is_cuda and out.is_contiguous()):
+        _check_all((("x", x, torch.bfloat16), ("weights", weights, torch.bfloat16),
+                    ("expert_offsets", expert_offsets, torch.int32), ("out", out, torch.bfloat16)))
+    _check("bias", bias, torch.float32)
+    _check("residual", residual, torch.bfloat16)
+    _check("pre", pre, torch.bfloat16)
+    _check("dev_error", dev_error, torch.int32)
+    if weights.dim() != 3 or weights.shape[2] != H:
+        raise ValueError("moe_expert_matmul: argument sizes disagree")
+    E, N = weights.shape[0], weights.shape[1]
+    C = N // 2 if act == 3 else N
+    if expert_offsets.numel() < E + 1 or out.numel() < rows * C or out.shape[-1] != C \
+            or (bias is not None and bias.numel() != E * N) \
+            or (residual is not None and (residual.numel() < rows * C or residual.shape[-1] != C)) \
+            or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)):
+        raise ValueError("moe_expert_matmul: argument sizes disagree")
+    st = (_lib or load()).moe_expert_matmul(
+        x.data_ptr(), weights.data_ptr(), _ptr(bias), expert_offsets.data_ptr(), rows, H, N, E, act,
+        _ptr(residual), _ptr(pre), out.data_ptr(), _ptr(dev_error),
+        _current_stream() if stream is None else _stream(stream))
+    if st:
+        _raise("moe_expert_matmul", st)
+
+
+def moe_expert_activation_backward_workspace_bytes(rows: int, N: int, E: int) -> int:
+    return int(load().moe_expert_activation_backward_workspace_bytes(rows, N, E))
+
+
+def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, activation: str,
+                                   grad_bias=None, workspace=None, stream=None) -> None:
+    """Gradient at moe_expert_matmul's values before the activation, and its sum
+    over each expert's rows; grad_pre or grad_bias may be None (not wanted), and
+    pre with activation "none"."""
+    fn = "moe_expert_activation_backward"
+    act = _activation(fn, activation)
+    _check("pre", pre, torch.bfloat16)
+    _check("grad_out", grad_out, torch.bfloat16)
+    _check("grad_pre", grad_pre, torch.bfloat16)
+    _check("grad_bias", grad_bias, torch.float32)
+    _check("expert_offsets", expert_offsets, torch.int32)
+    rows, C = grad_out.shape
+    N = 2 * C if act == 3 else C
+    E = expert_offsets.numel() - 1
+    if grad_bias is not None:
+        E = grad_bias.shape[0]
+    if expert_offsets.numel() < E + 1 or (grad_bias is not None and grad_bias.numel() != E * N) \
+            or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)) \
+            or (grad_pre is not None and (grad_pre.numel() < rows * N or grad_pre.shape[-1] != N)):
+        raise ValueError(f"{fn}: argument sizes disagree")
+    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
+    st = (_lib or load()).moe_expert_activation_backward(
+        _ptr(pre), grad_out.data_ptr(), expert_offsets.data_ptr(), rows, N, E, act, _ptr(grad_pre),
+        _ptr(grad_bias), _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+        _current_stream() if stream is None else _stream(stream))
+    if st:
+        _raise(fn, st)
+
+
+def moe_expert_matmul_backward(grad_pre, x, weights, expert_offsets, grad_x=None, grad_weights=None,
+                               accumulate: bool = False, dev_error=None, stream=None) -> None:
+    """Gradients of moe_expert_matmul's product with respect to its rows and its
+    weights (bf16, or fp32 and then added to where `accumulate`); either may be
+    None (not wanted)."""
+    fn = "moe_expert_matmul_backward"
+    for name, t in (("grad_pre", grad_pre), ("x", x), ("weights", weights), ("grad_x", grad_x)):
+        _check(name, t, torch.bfloat16)
+    f32 = grad_weights is not None and grad_weights.dtype is _f32
+    _check("grad_weights", grad_weights, torch.float32 if f32 else torch.bfloat16)
+    _check("expert_offsets", expert_offsets, torch.int32)
+    _check("dev_error", dev_error, torch.int32)
+    rows, N = grad_pre.shape
+    like = grad_weights if weights is None else weights
+    if like is None or like.dim() != 3 or like.shape[1] != N:
+        raise ValueError(f"{fn}: argument sizes disagree")
+    E, _, H = like.shape
+    if expert_offsets.numel() < E + 1 \
+            or (x is not None and (x.numel() < rows * H or x.shape[-1] != H)) \
+            or (grad_x is not None and (grad_x.numel() < rows * H or grad_x.shape[-1] != H)) \
+            or (grad_weights is not None and tuple(grad_weights.shape) != (E, N, H)):
+        raise ValueError(f"{fn}: argument sizes disagree")
+    st = (_lib or load()).moe_expert_matmul_backward(
+        grad_pre.data_ptr(), _ptr(x), _ptr(weights), expert_offsets.data_ptr(), rows, H, N, E, _ptr(grad_x),
+        _ptr(grad_weights), int(f32), 1 if accumulate else 0, _ptr(dev_error),
+        _current_stream() if stream is None else _stream(stream))
+    if st:
+        _raise(fn, st)
 
 
 def moe_route_workspace_bytes(T: int, E: int) -> int:

@@ -50,6 +50,12 @@ bool route_sizes_ok(int32_t T, int32_t E, int32_t K)
 
 bool flag(int32_t v) { return v == 0 || v == 1; }
 
+bool product_sizes_ok(int32_t rows, int32_t H, int32_t N, int32_t E)
+{
+    return rows >= 0 && rows <= kMostSteps && H >= 8 && H <= 65536 && H % 8 == 0 && N >= 1 && E >= 1 &&
+           E <= MOE_MAX_EXPERTS && (int64_t)E * N <= (int64_t)kMostSteps;
+}
+
 }  // namespace
 
 extern "C" {
@@ -354,6 +360,90 @@ moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales, const 
         return MOE_ERR_ALIGNMENT;
     return cuda_status(moe::launch_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets,
                                                       rows, H, N, E, out, dev_error, stream));
+}
+
+moe_status_t moe_expert_matmul(const void *x, const void *weights, const float *bias,
+                               const int32_t *expert_offsets, int32_t rows, int32_t H, int32_t N,
+                               int32_t E, int32_t activation, const void *residual, void *pre,
+                               void *out, uint32_t *dev_error, cudaStream_t stream)
+{
+    const CallRange range("moe_expert_matmul");
+    if (!product_sizes_ok(rows, H, N, E) || activation < MOE_ACT_NONE || activation > MOE_ACT_SWIGLU ||
+        (activation == MOE_ACT_SWIGLU && N % 2 != 0))
+        return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !weights || !expert_offsets || !out) return MOE_ERR_INVALID_ARG;
+    const void *p16[] = {x, weights, residual, pre, out}, *p4[] = {bias, expert_offsets, dev_error};
+    for (const void *p : p16)
+        if (!aligned(p, 16)) return MOE_ERR_ALIGNMENT;
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return MOE_ERR_ALIGNMENT;
+    return cuda_status(moe::launch_expert_matmul(x, weights, bias, expert_offsets, rows, H, N, E, activation,
+                                                 residual, pre, out, dev_error, stream));
+}
+
+size_t moe_expert_activation_backward_workspace_bytes(int32_t rows, int32_t N, int32_t E)
+{
+    if (!product_sizes_ok(rows, 8, N, E)) return 0;
+    return moe::activation_backward_workspace_bytes(rows, N, E);
+}
+
+moe_status_t moe_expert_activation_backward(const void *pre, const void *grad_out,
+                                            const int32_t *expert_offsets, int32_t rows, int32_t N,
+                                            int32_t E, int32_t activation, void *grad_pre,
+                                            float *grad_bias, void *workspace,
+                                            size_t workspace_bytes, cudaStream_t stream)
+{
+    const CallRange range("moe_expert_activation_backward");
+    if (!product_sizes_ok(rows, 8, N, E) || activation < MOE_ACT_NONE || activation > MOE_ACT_SWIGLU ||
+        N % (activation == MOE_ACT_SWIGLU ? 16 : 8) != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (!expert_offsets || (!grad_pre && !grad_bias)) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (!grad_out || (!pre && activation != MOE_ACT_NONE))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(pre, 16) || !aligned(grad_out, 16) || !aligned(grad_pre, 16) || !aligned(expert_offsets, 4) ||
+        !aligned(grad_bias, 4))
+        return MOE_ERR_ALIGNMENT;
+    if (grad_bias) {
+        if (!workspace || workspace_bytes < moe::activation_backward_workspace_bytes(rows, N, E))
+            return MOE_ERR_WORKSPACE;
+        if (!aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
+    } else if (rows == 0) {
+        return MOE_OK;
+    }
+    return cuda_status(moe::launch_activation_backward(pre, grad_out, expert_offsets, rows, N, E, activation,
+                                                       grad_pre, grad_bias, workspace, stream));
+}
+
+moe_status_t moe_expert_matmul_backward(const void *grad_pre, const void *x, const void *weights,
+                                        const int32_t *expert_offsets, int32_t rows, int32_t H,
+                                        int32_t N, int32_t E, void *grad_x, void *grad_weights,
+                                        int32_t weights_f32, int32_t accumulate,
+                                        uint32_t *dev_error, cudaStream_t stream)
+{
+    const CallRange range("moe_expert_matmul_backward");
+    if (!product_sizes_ok(rows, H, N, E) || N % 8 != 0 || !flag(weights_f32) || !flag(accumulate) ||
+        (accumulate && !weights_f32))
+        return MOE_ERR_INVALID_ARG;
+    if ((!grad_x && !grad_weights) || !expert_offsets) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (!grad_pre || (grad_x && !weights) || (grad_weights && !x))) return MOE_ERR_INVALID_ARG;
+    const void *p16[] = {grad_pre, x, weights, grad_x, grad_weights}, *p4[] = {expert_offsets, dev_error};
+    for (const void *p : p16)
+        if (!aligned(p, 16)) return MOE_ERR_ALIGNMENT;
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return MOE_ERR_ALIGNMENT;
+    const bool rows_too = grad_x && rows > 0;
+    if (rows_too) {
+        const cudaError_t e = moe::launch_expert_matmul_rows(grad_pre, weights, expert_offsets, rows, H, N, E, grad_x,
+                                                             dev_error, stream);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    if (!grad_weights) return MOE_OK;
+    if (rows == 0) {                                   // nothing to multiply: an empty sum
+        if (accumulate) return MOE_OK;
+        return cuda_status(cudaMemsetAsync(grad_weights, 0, (size_t)E * N * H * (weights_f32 ? 4 : 2), stream));
+    }
+    return cuda_status(moe::launch_expert_matmul_weights(grad_pre, x, expert_offsets, rows, H, N, E, grad_weights,
+                                                         weights_f32, accumulate, dev_error, !rows_too, stream));
 }
 
 }  // extern "C"

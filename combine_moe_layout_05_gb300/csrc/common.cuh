@@ -76,6 +76,24 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t codes)
     return __half22float2(v);
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x to 2 ulp; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1/x to 1 ulp; 0 for an infinity.
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 __host__ __device__ constexpr int align4(int n) { return (n + 3) & ~3; }
 

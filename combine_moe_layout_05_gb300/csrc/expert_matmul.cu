@@ -1,0 +1,126 @@
+// expert_matmul.cu -- packed bf16 rows times their experts' weights, with bias,
+// activation and residual in the same pass (expert_matmul_common.cuh).
+#include "expert_matmul_common.cuh"
+
+namespace moe {
+namespace {
+
+template <bool G> using Wide = Shape<kForward, G, 2, 256, 6>;
+template <bool G> using Mid = Shape<kForward, G, 2, 128, 8>;
+template <bool G> using Narrow = Shape<kForward, G, 1, 32, 10>;
+template <bool G> using Split = Shape<kForward, G, 1, 32, 9, true>;
+
+// Clusters of 2, 4 and 8 splitting CTAs that the current device runs at a time,
+// looked up once for each device.
+template <bool G>
+cudaError_t split_clusters(int (&clusters)[3])
+{
+    using S = Split<G>;
+    constexpr int kMaxDevices = 64;
+    static std::mutex mu;
+    static int known[kMaxDevices][3];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const std::lock_guard<std::mutex> lock(mu);
+    auto *const kernel = &expert_matmul_kernel<S>;
+    const size_t smem = S::bytes(MOE_MAX_EXPERTS);
+    for (int i = 0; i < 3; ++i) {
+        int &n = known[dev][i];
+        if (n == 0) {
+            e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 << i);
+            cfg.blockDim = dim3(S::THREADS);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        clusters[i] = n;
+    }
+    return cudaSuccess;
+}
+
+template <bool G>
+cudaError_t launch(const void *x, const void *w, const int32_t *offsets, int rows, int H, int N, int E, const Store &st,
+                   uint32_t *dev_error, cudaStream_t stream, long long wait_limit, int stall)
+{
+    const int channels = G ? N / 2 : N;
+    int sms = 0;
+    cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    CUtensorMap map_w;
+    if (G) {                                           // 16 gate channels, then their 16 up channels
+        const uint64_t dims[4] = {(uint64_t)H, (uint64_t)channels, 2, (uint64_t)E};
+        const uint64_t strides[3] = {(uint64_t)H, (uint64_t)channels * H, (uint64_t)N * H};
+        const uint32_t box[4] = {kStep, 16, 2, 1};
+        if (!bf16_map(&map_w, w, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    } else if (!rows_map(&map_w, w, (uint64_t)E * N, H, kChannels)) {
+        return cudaErrorInvalidValue;
+    }
+    const Sizes z{rows, N, channels, H, E};
+    auto go = [&](auto shape, int parts) {
+        using S = decltype(shape);
+        RowMaps map_x;
+        if (!row_maps<S>(&map_x, x, rows, H)) return cudaErrorInvalidValue;
+        const int64_t tiles = most_tiles<S>(rows, E) * ceil_div(channels, S::OUT * S::CG);
+        return run<S>(map_w, map_x, offsets, z, st, tiles, sms, parts, dev_error, 1, wait_limit, stall, stream);
+    };
+    // Few tiles: share the contraction, as far as every tile's cluster runs at
+    // once and the steps saved outweigh the cluster's barriers.
+    const int64_t tiles = most_tiles<Split<G>>(rows, E) * ceil_div(channels, Split<G>::OUT);
+    const int steps = ceil_div(H, kStep);
+    if (tiles * 2 <= sms && steps >= 32) {
+        int clusters[3];
+        e = split_clusters<G>(clusters);
+        if (e != cudaSuccess) return e;
+        int parts = 1;
+        for (int p = 2; p <= 8 && steps >= 8 * p; p *= 2)
+            if (tiles <= clusters[p / 4]) parts = p;
+        if (parts > 1) return go(Split<G>{}, parts);
+    }
+    if (rows <= 16 * E) return go(Narrow<G>{}, 1);
+    return rows >= 192 * E ? go(Wide<G>{}, 1) : go(Mid<G>{}, 1);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_matmul(const void *x, const void *w, const float *bias, const int32_t *offsets, int rows,
+                                 int H, int N, int E, int activation, const void *residual, void *pre, void *out,
+                                 uint32_t *dev_error, cudaStream_t stream, int64_t wait_cycles, int stall)
+{
+    const long long limit = wait_cycles > 0 ? wait_cycles : kWaitLimitCycles;
+    const Store st{bias, static_cast<const __nv_bfloat16 *>(residual), static_cast<__nv_bfloat16 *>(pre), out,
+                   activation, 0, 0};
+    return activation == MOE_ACT_SWIGLU
+               ? launch<true>(x, w, offsets, rows, H, N, E, st, dev_error, stream, limit, stall)
+               : launch<false>(x, w, offsets, rows, H, N, E, st, dev_error, stream, limit, stall);
+}
+
+}  // namespace moe
+
+// Test hook, deliberately absent from the public header: the product with a
+// chosen bound on every wait (in clock cycles; 0: the default) and, in the
+// CTAs of the first tiles, one barrier that waits for an arrival that never
+// comes: stall 0 a step landed, 1 its slot free again, 2 landed in both CTAs of
+// a pair, 3 sums ready, 4 sums stored, 5 the other CTAs' sums (where the
+// contraction is split); anything else none.  A test uses it to see a bounded
+// wait expire: the kernel sets MOE_DEV_ERR_TIMEOUT and finishes, and the
+// context stays usable.  Arguments are checked by the caller (tests only).
+extern "C" __attribute__((visibility("default"))) int32_t
+moe_testing_expert_matmul(const void *x, const void *weights, const int32_t *expert_offsets, int32_t rows, int32_t H,
+                          int32_t N, int32_t E, int32_t activation, void *out, uint32_t *dev_error, int64_t wait_cycles,
+                          int32_t stall, cudaStream_t stream)
+{
+    const cudaError_t e = moe::launch_expert_matmul(x, weights, nullptr, expert_offsets, rows, H, N, E, activation, nullptr,
+                                                    nullptr, out, dev_error, stream, wait_cycles, stall);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -1,0 +1,75 @@
+// expert_matmul_backward.cu -- the gradients of the experts' product with
+// respect to the rows and to the weights (expert_matmul_common.cuh).
+#include "expert_matmul_common.cuh"
+
+namespace moe {
+namespace {
+
+using RowsWide = Shape<kRows, false, 2, 256, 6>;
+using RowsMid = Shape<kRows, false, 2, 128, 8>;
+using RowsNarrow = Shape<kRows, false, 1, 32, 10>;
+using Weights = Shape<kWeights, false, 2, 256, 6>;
+
+}  // namespace
+
+cudaError_t launch_expert_matmul_rows(const void *grad_pre, const void *w, const int32_t *offsets, int rows, int H,
+                                      int N, int E, void *grad_x, uint32_t *dev_error, cudaStream_t stream,
+                                      int64_t wait_cycles, int stall)
+{
+    const long long limit = wait_cycles > 0 ? wait_cycles : kWaitLimitCycles;
+    int sms = 0;
+    const cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    CUtensorMap map_w;                                 // [E, N, H]: past an expert's N are zeros, not the next one's
+    const uint64_t dims[3] = {(uint64_t)H, (uint64_t)N, (uint64_t)E}, strides[2] = {(uint64_t)H, (uint64_t)N * H};
+    const uint32_t box[3] = {64, kStep, 1};
+    if (!bf16_map(&map_w, w, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    const Sizes z{rows, N, H, N, E};
+    const Store st{nullptr, nullptr, nullptr, grad_x, MOE_ACT_NONE, 0, 0};
+    auto go = [&](auto shape) {
+        using S = decltype(shape);
+        RowMaps map_g;
+        if (!row_maps<S>(&map_g, grad_pre, rows, N)) return cudaErrorInvalidValue;
+        const int64_t tiles = most_tiles<S>(rows, E) * ceil_div(H, S::OUT * S::CG);
+        return run<S>(map_w, map_g, offsets, z, st, tiles, sms, 1, dev_error, 1, limit, stall, stream);
+    };
+    if (rows <= 16 * E) return go(RowsNarrow{});
+    return rows >= 192 * E ? go(RowsWide{}) : go(RowsMid{});
+}
+
+cudaError_t launch_expert_matmul_weights(const void *grad_pre, const void *x, const int32_t *offsets, int rows, int H,
+                                         int N, int E, void *grad_w, int f32, int accumulate, uint32_t *dev_error,
+                                         int clear, cudaStream_t stream, int64_t wait_cycles, int stall)
+{
+    const long long limit = wait_cycles > 0 ? wait_cycles : kWaitLimitCycles;
+    int sms = 0;
+    const cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    CUtensorMap map_x;
+    RowMaps map_g;
+    if (!rows_map(&map_x, x, rows, H, kStep) || !rows_map(&map_g.box[0], grad_pre, rows, N, kStep))
+        return cudaErrorInvalidValue;
+    for (int m = 1; m < kBoxes; ++m) map_g.box[m] = map_g.box[0];
+    const Sizes z{rows, N, H, 0, E};
+    const Store st{nullptr, nullptr, nullptr, grad_w, MOE_ACT_NONE, f32, accumulate};
+    const int64_t tiles = (int64_t)E * ceil_div(N, Weights::NT) * ceil_div(H, Weights::OUT * Weights::CG);
+    return run<Weights>(map_x, map_g, offsets, z, st, tiles, sms, 1, dev_error, clear, limit, stall, stream);
+}
+
+}  // namespace moe
+
+// Test hook, deliberately absent from the public header: one gradient (weights
+// != 0: the weights' in bf16, else the rows') with a bound on every wait and a
+// barrier held back, as moe_testing_expert_matmul has them.
+extern "C" __attribute__((visibility("default"))) int32_t
+moe_testing_expert_matmul_backward(const void *grad_pre, const void *other, const int32_t *expert_offsets, int32_t rows,
+                                   int32_t H, int32_t N, int32_t E, int32_t weights, void *out, uint32_t *dev_error,
+                                   int64_t wait_cycles, int32_t stall, cudaStream_t stream)
+{
+    const cudaError_t e =
+        weights ? moe::launch_expert_matmul_weights(grad_pre, other, expert_offsets, rows, H, N, E, out, 0, 0, dev_error, 1,
+                                                    stream, wait_cycles, stall)
+                : moe::launch_expert_matmul_rows(grad_pre, other, expert_offsets, rows, H, N, E, out, dev_error, stream,
+                                                 wait_cycles, stall);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -33,10 +33,7 @@
 // HBM-bound); 32768 skewed rows over 384 experts, 7168 -> 2048, 1.12 ms in a
 // burst, 1.20 under the cap (547 tiles of 60 rows on average, 600 to 700 cycles
 // a step; HBM takes 706 for the first tile of an expert, L2 feeds the others).
-#include "common.cuh"
-#include "internal.h"
-#include "moe_layout.h"
-#include "tensor.cuh"
+#include "expert_tiles.cuh"
 
 #include <mutex>
 #include <type_traits>
@@ -45,7 +42,6 @@ namespace moe {
 namespace {
 
 constexpr int kStep = 128;                 // bytes of the contraction a ring slot holds
-constexpr int kChannels = 128;             // channels a CTA
 constexpr int kTmemColumns = 512;
 constexpr int kMaxShared = 227 * 1024;
 
@@ -118,47 +114,6 @@ struct RowMaps {
     CUtensorMap box[kBoxes];    // 16, 32, 64, 128 rows
 };
 
-// One tile: the rows [row, row + valid) of expert e and the channels from
-// `channel`.  CTA r of a pair widens the rows from r * share; the share is
-// split into parts (a sum with an accumulator of its own), and n[p] counts the
-// pair's rows in part p: part 0 is the first n[0] / CG of each share.
-struct Tile {
-    int e, row, valid, n[2], channel;
-};
-
-// Experts' first rows and first tiles, in shared memory.
-struct Table {
-    const int *first_row;      // [E + 1]
-    const int *first_tile;     // [E + 1]
-};
-
-// Tile i, for a whole warp; at: its expert or one before it, and its expert
-// afterwards.  A warp goes through its tiles in order, so the search goes on
-// from the last one's expert, 32 experts a step.
-template <typename S>
-__device__ __forceinline__ Tile tile_of(const Table &t, int E, int channel_tiles, int i, int &at)
-{
-    const int tt = (int)((unsigned)i / (unsigned)channel_tiles);
-    for (unsigned passed = kFullMask; passed == kFullMask; at += __popc(passed)) {
-        const int e = at + 1 + (int)(threadIdx.x & 31);
-        passed = __ballot_sync(kFullMask, e < E && t.first_tile[e] <= tt);
-    }
-    const int lo = at;                                 // first_tile[lo] <= tt < first_tile[lo + 1]
-    const int base = t.first_tile[lo], tiles = t.first_tile[lo + 1] - base;
-    const int rows = t.first_row[lo + 1] - t.first_row[lo];
-    // an expert's rows are split evenly; a share is at most NT, so no tile is empty
-    const int share = ceil_div((int)((unsigned)(rows + tiles - 1) / (unsigned)tiles), S::QUANTUM) * S::QUANTUM;
-    Tile r;
-    r.e = uniform(lo);
-    r.row = uniform(t.first_row[lo] + (tt - base) * share);
-    r.valid = uniform(min(share, rows - (tt - base) * share));
-    const int n = ceil_div(r.valid, S::QUANTUM) * S::QUANTUM;
-    r.n[0] = S::PARTS == 1 ? n : ceil_div(n, 2 * S::QUANTUM) * S::QUANTUM;
-    r.n[1] = n - r.n[0];
-    r.channel = (i - tt * channel_tiles) * kChannels * S::CG;
-    return r;
-}
-
 // Two products at once.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
@@ -187,18 +142,6 @@ __device__ __forceinline__ void widen16(const uint4 &x, uint32_t *v)
     widen4(x.y, v[2], v[3]);
     widen4(x.z, v[4], v[5]);
     widen4(x.w, v[6], v[7]);
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // The instructions of one slot of widened operands: B's 64-wide blocks follow
@@ -283,39 +226,10 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     pdl_wait();
     pdl_trigger();
 
-    // Tiles an expert, then their running sum: thread t has experts 2t, 2t + 1.
-    {
-        static_assert(2 * S::THREADS > MOE_MAX_EXPERTS);
-        static_assert(S::WARPS * 4 <= 4 * S::SETS * 1024);
-        int *const warp_tiles = reinterpret_cast<int *>(generic + S::OFFTURN);      // not in use yet
-        int tiles[2], before = 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = 2 * tid + j;
-            tiles[j] = 0;
-            if (e <= E) {
-                const int lo = max(0, min(rows, offsets[e]));
-                first_row[e] = lo;
-                if (e < E) tiles[j] = ceil_div(max(0, min(rows, offsets[e + 1]) - lo), S::NT);
-            }
-        }
-        int sum = tiles[0] + tiles[1];
-        const int mine = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kFullMask, sum, o);
-            if (lane >= o) sum += v;
-        }
-        if (lane == 31) warp_tiles[warp] = sum;
-        tc_fence_before();
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) before += warp_tiles[w];
-        before += sum - mine;
-        if (2 * tid <= E) first_tile[2 * tid] = before;
-        if (2 * tid + 1 <= E) first_tile[2 * tid + 1] = before + tiles[0];
-    }
+    static_assert(S::WARPS * 4 <= 4 * S::SETS * 1024);
+    fill_table<S::THREADS, S::NT>(offsets, rows, E, first_row, first_tile,
+                                  reinterpret_cast<int *>(generic + S::OFFTURN));     // not in use yet
     if (dev_error && blockIdx.x == 0 && tid == 0) *dev_error = 0;
-    __syncthreads();
     if constexpr (S::CG == 2 || S::SPLIT) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = uniform(flags[0]);
@@ -730,24 +644,6 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     if (warp == 1) tmem_free<S::CG>(tmem, kTmemColumns);
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn()
-{
-    static std::once_flag once;
-    static EncodeFn fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeFn>(p);
-    });
-    return fn;
-}
-
 // [rows, H] bytes, in boxes of kStep bytes by `box` rows, 128-byte swizzle.
 bool byte_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t H, uint32_t box)
 {
@@ -758,13 +654,6 @@ bool byte_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t H, uint32
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, boxes, ones,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Tiles there can be at most: every expert's last one may be short.
-template <typename S>
-int64_t most_tiles(int rows, int N, int E)
-{
-    return ((int64_t)(rows < E ? rows : E) + rows / S::NT) * ceil_div(N, kChannels * S::CG);
 }
 
 template <typename S>
@@ -781,7 +670,7 @@ cudaError_t run(const void *x, const float *x_scales, const void *w, const float
     const size_t smem = S::bytes(E);
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(&expert_matmul_int8_kernel<S>), smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = most_tiles<S>(rows, N, E);
+    const int64_t tiles = most_tiles<S>(rows, E) * ceil_div(N, kChannels * S::CG);
     const int64_t groups = tiles < sms / (S::CG * parts) ? tiles : sms / (S::CG * parts);
     return launch_pdl_clusters(expert_matmul_int8_kernel<S>, dim3((unsigned)groups * S::CG * parts), dim3(S::THREADS),
                                smem, stream, S::CG * parts, map_w, map_x, x_scales, w_scales, offsets, rows, H, N, E,
@@ -843,7 +732,7 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
     // Few tiles: share the contraction, as far as every tile's cluster runs at
     // once and the steps saved outweigh the cluster's barriers (30 tiles of 4272:
     // 12.2 -> 9.3 us; 4 tiles of 992, 8 steps: 6.4 -> 7.2 us).
-    const int64_t tiles = most_tiles<Split>(rows, N, E);
+    const int64_t tiles = most_tiles<Split>(rows, E) * ceil_div(N, kChannels);
     const int steps = ceil_div(H, kStep);
     if (tiles * 2 <= sms && steps >= 16) {
         int clusters[3];

@@ -111,6 +111,25 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
                                       int H, int N, int E, void *out, uint32_t *dev_error,
                                       cudaStream_t stream, int64_t wait_cycles = 0, int stall = -1);
 
+// Packed bf16 rows times their experts' weights, with the epilogue; and the
+// product's two gradients (f32: grad_w is fp32; accumulate: and added to;
+// clear: dev_error starts at 0).  wait_cycles and stall as above.
+cudaError_t launch_expert_matmul(const void *x, const void *w, const float *bias, const int32_t *offsets, int rows,
+                                 int H, int N, int E, int activation, const void *residual, void *pre, void *out,
+                                 uint32_t *dev_error, cudaStream_t stream, int64_t wait_cycles = 0, int stall = -1);
+cudaError_t launch_expert_matmul_rows(const void *grad_pre, const void *w, const int32_t *offsets, int rows, int H,
+                                      int N, int E, void *grad_x, uint32_t *dev_error, cudaStream_t stream,
+                                      int64_t wait_cycles = 0, int stall = -1);
+cudaError_t launch_expert_matmul_weights(const void *grad_pre, const void *x, const int32_t *offsets, int rows, int H,
+                                         int N, int E, void *grad_w, int f32, int accumulate, uint32_t *dev_error,
+                                         int clear, cudaStream_t stream, int64_t wait_cycles = 0, int stall = -1);
+
+// The gradient at the values before the activation, and the bias gradient.
+size_t activation_backward_workspace_bytes(int rows, int N, int E);
+cudaError_t launch_activation_backward(const void *pre, const void *grad_out, const int32_t *offsets, int rows, int N,
+                                       int E, int activation, void *grad_pre, float *grad_bias, void *workspace,
+                                       cudaStream_t stream);
+
 // Router logits (bf16 != 0: bf16, else fp32) to ids, weights, counts and the
 // balance loss; and the gradient back to the logits.
 size_t route_workspace_bytes(int T, int E);

@@ -10,20 +10,10 @@
 namespace moe {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float from_float(float v, float) { return v; }
 __device__ __forceinline__ __nv_bfloat16 from_float(float v, __nv_bfloat16) { return __float2bfloat16_rn(v); }
-
-// 2^x to 2 ulp; results below 2^-126 are 0.
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Sum over the first `lanes` lanes, a power of two (the others get other sums).
 __device__ __forceinline__ float lanes_sum(float v, int lanes)

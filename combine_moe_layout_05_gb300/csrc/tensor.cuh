@@ -155,6 +155,20 @@ __device__ __forceinline__ void tile_load_2d(uint32_t dst, const CUtensorMap *ma
                  :: "r"(dst), "l"(map), "r"(c), "r"(r), "r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void tile_load_3d(uint32_t dst, const CUtensorMap *map, int c, int r, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(map), "r"(c), "r"(r), "r"(z), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tile_load_4d(uint32_t dst, const CUtensorMap *map, int c, int r, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 :: "r"(dst), "l"(map), "r"(c), "r"(r), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
@@ -202,6 +216,20 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_de
                      :: "r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
 
+// The same with A in shared memory too; both operands bf16 or both fp16.
+template <int CG>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate)
+{
+    if constexpr (CG == 1)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+}
+
 // One arrival on `bar` (of both CTAs of a pair) once the matrix instructions
 // issued so far have completed.
 template <int CG>
@@ -220,6 +248,22 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
 {
     return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Shared-memory operand whose rows lie along the contraction (MN-major): lines
+// of 128 bytes (64 rows' values of one step), 8 lines a group, groups 1024
+// bytes apart; the next 64 rows are `block` bytes on.
+__device__ __forceinline__ uint64_t operand_desc_mn(uint32_t addr, uint32_t block)
+{
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(block >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// kind::f16, A and B bf16, each K-major or not, D fp32.
+__device__ __forceinline__ uint32_t instruction_desc_bf16(int M, int N, bool a_mn, bool b_mn)
+{
+    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (uint32_t)(N >> 3) << 17 |
+           (uint32_t)(M >> 4) << 24;
 }
 
 // kind::f16, A and B fp16 and K-major, D fp32.
@@ -260,6 +304,26 @@ __device__ __forceinline__ void store_turned_x4(uint32_t row, uint32_t a, uint32
 {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
                  :: "r"(row), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// And back: thread 4i + j/2 gets word (i, j) from the rows that word (i, j) was
+// stored to.
+__device__ __forceinline__ void load_turned_x4(uint32_t row, uint32_t (&v)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(row) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 }  // namespace moe

@@ -18,9 +18,10 @@
  *    (described with that call) it keeps no state between calls.
  *  - moe_layout, moe_dispatch, moe_combine, moe_combine_fp8,
  *    moe_combine_rank_partial, moe_dispatch_send, moe_dispatch_recv,
- *    moe_layout_dispatch, moe_route, moe_route_backward, moe_dispatch_int8 and
- *    moe_expert_matmul_int8 are asynchronous on `stream` (0 = legacy default
- *    stream) and may be captured into a CUDA graph.
+ *    moe_layout_dispatch, moe_route, moe_route_backward, moe_dispatch_int8,
+ *    moe_expert_matmul_int8, moe_expert_matmul, moe_expert_activation_backward
+ *    and moe_expert_matmul_backward are asynchronous on `stream` (0 = legacy
+ *    default stream) and may be captured into a CUDA graph.
  *  - Arguments are checked on the host before anything is enqueued.  A
  *    failed check returns an error status and enqueues nothing.
  *  - Matrices are row-major and dense: a [rows, H] matrix has row stride H.
@@ -64,10 +65,17 @@ typedef enum moe_status {
 #define MOE_DEV_ERR_DUPLICATE    2u  /* some token lists one expert twice       */
 #define MOE_DEV_ERR_REGION_OVERFLOW 4u /* moe_dispatch_send: a rank's rows exceed
                                           its private + bulk capacity          */
-#define MOE_DEV_ERR_TIMEOUT 8u       /* moe_layout_dispatch,
-                                        moe_expert_matmul_int8: a bounded wait
-                                        between its blocks or warps expired;
-                                        outputs unspecified                    */
+#define MOE_DEV_ERR_TIMEOUT 8u       /* moe_layout_dispatch, moe_expert_matmul,
+                                        its backward and moe_expert_matmul_int8:
+                                        a bounded wait between the kernel's
+                                        blocks or warps expired; outputs
+                                        unspecified                            */
+
+/* Activations of moe_expert_matmul, a(z); s is the logistic function. */
+#define MOE_ACT_NONE 0    /* z                                                      */
+#define MOE_ACT_SILU 1    /* z s(z)                                                 */
+#define MOE_ACT_GELU 2    /* z s(2 sqrt(2/pi) (z + 0.044715 z^3)): GELU's tanh form */
+#define MOE_ACT_SWIGLU 3  /* gated: z[n] s(z[n]) z[N/2 + n], n < N/2                */
 
 /* Limits of this implementation. */
 #define MOE_MAX_EXPERTS 1024
@@ -491,6 +499,109 @@ MOE_API moe_status_t moe_expert_matmul_int8(const void *x, const float *x_scales
                                             const int32_t *expert_offsets, int32_t rows,
                                             int32_t H, int32_t N, int32_t E, void *out,
                                             uint32_t *dev_error, cudaStream_t stream);
+
+/*
+ * moe_expert_matmul -- the experts' matrix product on packed bf16 rows, with
+ * bias, activation and residual in the same pass.
+ *
+ * The page multiplies the packed rows with the experts' weights between
+ * dispatch and combine ("MoE all-to-all over EFA").  For the rows r of expert e,
+ * expert_offsets[e] <= r < expert_offsets[e+1]:
+ *
+ *   z[n]      = sum over h of x[r,h] * weights[e,n,h] + bias[e,n]    (fp32)
+ *   pre[r,n]  = bf16(z[n])
+ *   out[r,c]  = bf16(a(z)[c] + residual[r,c])      (RN, ties to even, rounded once)
+ *
+ * with a the activation (MOE_ACT_*).  MOE_ACT_SWIGLU takes z's first half as the
+ * gate and its second as what it opens: out has C = N/2 channels, else C = N.
+ * The activation takes z unrounded.  Rows outside all experts' ranges are not
+ * written.  E == 1 with offsets {0, rows} is the plain matrix product (a shared
+ * expert, whose residual may be the routed experts' sum).
+ *
+ * x              [rows,H] bf16.   weights [E,N,H] bf16 (a channel's H values together).
+ * bias           [E,N] fp32 or NULL (zeros), 4-byte aligned.
+ * expert_offsets [E+1] int32, moe_layout's; non-decreasing.  Offsets outside
+ *                [0, rows] are taken as the nearer end.
+ * residual       [rows,C] bf16 or NULL (zeros); may be out itself.
+ * pre            [rows,N] bf16 or NULL: what the gradient needs.
+ * out            [rows,C] bf16.  pre and out must not overlap the other inputs.
+ * x, weights, residual, pre and out are 16-byte aligned.
+ * dev_error      [1] uint32 or NULL.  Overwritten with 0, or with
+ *                MOE_DEV_ERR_TIMEOUT when a bounded wait (2 s) between the
+ *                kernel's warps expired; the outputs are then unspecified.
+ * 0 <= rows <= 2^31 - 65536, 8 <= H <= 65536 with H % 8 == 0, N >= 1 (even for
+ * MOE_ACT_SWIGLU), E*N <= 2^31 - 65536, 1 <= E <= MOE_MAX_EXPERTS.  rows == 0 is
+ * a no-op.  Asynchronous on `stream`; may be captured.
+ */
+MOE_API moe_status_t moe_expert_matmul(const void *x, const void *weights, const float *bias,
+                                       const int32_t *expert_offsets, int32_t rows, int32_t H,
+                                       int32_t N, int32_t E, int32_t activation,
+                                       const void *residual, void *pre, void *out,
+                                       uint32_t *dev_error, cudaStream_t stream);
+
+/*
+ * moe_expert_activation_backward -- from the gradient at moe_expert_matmul's
+ * out to the gradient at z, and its sum over each expert's rows.
+ *
+ *   grad_pre[r,n]  = bf16(g[r,n]),  g = grad_out[r,n] * a'(pre[r,n]); with
+ *                    MOE_ACT_SWIGLU, for c < N/2 and s the logistic function of
+ *                    pre[r,c]:  g[r,c] = grad_out[r,c] pre[r,N/2+c] s (1 + pre[r,c] (1 - s)),
+ *                    g[r,N/2+c] = grad_out[r,c] pre[r,c] s
+ *   grad_bias[e,n] = sum over the rows r of expert e of g[r,n]   (fp32, unrounded
+ *                    g; in an order that the sizes and offsets fix)
+ *
+ * (The residual's gradient is grad_out.)  Rows outside all experts' ranges are
+ * not written; an expert without rows gets zeros in grad_bias.
+ *
+ * pre        [rows,N] bf16, moe_expert_matmul's; may be NULL with MOE_ACT_NONE.
+ * grad_out   [rows,C] bf16.   expert_offsets as for moe_expert_matmul.
+ * grad_pre   [rows,N] bf16 or NULL (not wanted); may be pre itself, and without
+ *            MOE_ACT_SWIGLU grad_out itself.
+ * grad_bias  [E,N] fp32 or NULL (not wanted).  One of the two is wanted.
+ * workspace  with grad_bias: moe_expert_activation_backward_workspace_bytes
+ *            (0 for invalid sizes) bytes, 16-byte aligned; its contents on entry
+ *            do not matter, and it is in use until the stream passes this call.
+ * pre, grad_out and grad_pre are 16-byte aligned.  Sizes as for
+ * moe_expert_matmul, with N % 8 == 0 (N % 16 == 0 for MOE_ACT_SWIGLU).  rows == 0
+ * writes zeros to grad_bias.  Asynchronous on `stream`; may be captured.
+ */
+MOE_API size_t moe_expert_activation_backward_workspace_bytes(int32_t rows, int32_t N, int32_t E);
+
+MOE_API moe_status_t moe_expert_activation_backward(const void *pre, const void *grad_out,
+                                                    const int32_t *expert_offsets, int32_t rows,
+                                                    int32_t N, int32_t E, int32_t activation,
+                                                    void *grad_pre, float *grad_bias,
+                                                    void *workspace, size_t workspace_bytes,
+                                                    cudaStream_t stream);
+
+/*
+ * moe_expert_matmul_backward -- the gradients of moe_expert_matmul's product
+ * with respect to its rows and weights.
+ *
+ *   grad_x[r,h]         = bf16(sum over n of grad_pre[r,n] * weights[e,n,h])
+ *   grad_weights[e,n,h] = sum over the rows r of expert e of grad_pre[r,n] * x[r,h],
+ *                         in bf16, or in fp32 (weights_f32 == 1), where
+ *                         accumulate == 1 adds it to what grad_weights holds
+ *
+ * with fp32 sums.  Rows of grad_x outside all experts' ranges are not written;
+ * an expert without rows gets zeros in grad_weights (with accumulate, it is left
+ * as it is).
+ *
+ * grad_pre      [rows,N] bf16.   x [rows,H] bf16 (may be NULL without grad_weights).
+ * weights       [E,N,H] bf16 (may be NULL without grad_x).
+ * grad_x        [rows,H] bf16 or NULL (not wanted).
+ * grad_weights  [E,N,H] bf16 or fp32, or NULL (not wanted).  One of the two is wanted.
+ * All of these are 16-byte aligned; the outputs must not overlap the inputs.
+ * expert_offsets, dev_error and sizes as for moe_expert_matmul, with N % 8 == 0.
+ * rows == 0 writes zeros to grad_weights (without accumulate); dev_error is then
+ * not written.  Asynchronous on `stream`; may be captured.
+ */
+MOE_API moe_status_t moe_expert_matmul_backward(const void *grad_pre, const void *x,
+                                                const void *weights, const int32_t *expert_offsets,
+                                                int32_t rows, int32_t H, int32_t N, int32_t E,
+                                                void *grad_x, void *grad_weights,
+                                                int32_t weights_f32, int32_t accumulate,
+                                                uint32_t *dev_error, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
