@@ -8,7 +8,7 @@ dispatch and combine.  ``layer`` puts the calls together as an MoE layer: the
 router under autograd, and int8 experts.
 """
 from ._binding import (MOE_DEV_ERR_DUPLICATE, MOE_DEV_ERR_EXPERT_RANGE,
-                       MOE_ACTIVATIONS, MOE_DEV_ERR_REGION_OVERFLOW, MOE_DEV_ERR_TIMEOUT,
+                       MOE_ACTIVATIONS, MOE_SCORES, MOE_DEV_ERR_REGION_OVERFLOW, MOE_DEV_ERR_TIMEOUT,
                        LayoutBuffers, MoeError, declared_functions,
                        library_path, load, moe_combine, moe_combine_fp8,
                        moe_combine_rank_partial,
@@ -19,11 +19,13 @@ from ._binding import (MOE_DEV_ERR_DUPLICATE, MOE_DEV_ERR_EXPERT_RANGE,
                        moe_layout, moe_layout_dispatch,
                        moe_layout_dispatch_kernels, moe_layout_kernels, moe_layout_static,
                        moe_layout_workspace_bytes,
-                       moe_route, moe_route_backward, moe_route_workspace_bytes,
+                       moe_route, moe_route_backward, moe_route_grouped,
+                       moe_route_grouped_backward, moe_route_grouped_workspace_bytes,
+                       moe_route_workspace_bytes,
                        moe_status_string, RouteBuffers)
 
 __all__ = [
-    "MOE_ACTIVATIONS", "MOE_DEV_ERR_DUPLICATE", "MOE_DEV_ERR_EXPERT_RANGE", "MOE_DEV_ERR_REGION_OVERFLOW",
+    "MOE_ACTIVATIONS", "MOE_SCORES", "MOE_DEV_ERR_DUPLICATE", "MOE_DEV_ERR_EXPERT_RANGE", "MOE_DEV_ERR_REGION_OVERFLOW",
     "MOE_DEV_ERR_TIMEOUT",
     "LayoutBuffers",
     "MoeError", "declared_functions", "library_path", "load", "moe_combine",
@@ -32,6 +34,7 @@ __all__ = [
     "moe_expert_activation_backward_workspace_bytes", "moe_expert_matmul", "moe_expert_matmul_backward",
     "moe_expert_matmul_int8", "moe_dispatch_recv", "moe_dispatch_send", "moe_layout", "moe_layout_dispatch", "moe_layout_dispatch_kernels", "moe_layout_kernels", "moe_layout_static",
     "moe_layout_workspace_bytes",
-    "moe_route", "moe_route_backward", "moe_route_workspace_bytes",
+    "moe_route", "moe_route_backward", "moe_route_grouped", "moe_route_grouped_backward",
+    "moe_route_grouped_workspace_bytes", "moe_route_workspace_bytes",
     "moe_status_string", "RouteBuffers",
 ]

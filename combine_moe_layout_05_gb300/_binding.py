@@ -91,6 +91,14 @@ def load(path: str | None = None):
             lib.moe_dispatch_int8.restype = ctypes.c_int
             lib.moe_expert_matmul_int8.argtypes = [P, P, P, P, P, i32, i32, i32, i32, P, P, P]
             lib.moe_expert_matmul_int8.restype = ctypes.c_int
+            lib.moe_route_grouped_workspace_bytes.argtypes = [i32, i32]
+            lib.moe_route_grouped_workspace_bytes.restype = sz
+            lib.moe_route_grouped.argtypes = [P, i32, i32, i32, i32, i32, P, i32, i32, i32, i32, f32, f32,
+                                              P, P, P, P, P, P, P, sz, P]
+            lib.moe_route_grouped.restype = ctypes.c_int
+            lib.moe_route_grouped_backward.argtypes = [P, i32, i32, i32, i32, i32, i32, f32, f32, P, P, P,
+                                                       P, P, P, P]
+            lib.moe_route_grouped_backward.restype = ctypes.c_int
             lib.moe_expert_matmul.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, P, P, P, P, P]
             lib.moe_expert_matmul.restype = ctypes.c_int
             lib.moe_expert_activation_backward_workspace_bytes.argtypes = [i32, i32, i32]
@@ -613,6 +621,95 @@ def moe_route_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weig
         grad_logits.data_ptr(), _current_stream() if stream is None else _stream(stream))
     if st:
         _raise("moe_route_backward", st)
+
+
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _scoring(fn: str, name: str) -> int:
+    code = MOE_SCORES.get(name)
+    if code is None:
+        raise ValueError(f"{fn}: scoring must be one of {sorted(MOE_SCORES)}, got {name!r}")
+    return code
+
+
+def moe_route_grouped_workspace_bytes(T: int, E: int) -> int:
+    return int(load().moe_route_grouped_workspace_bytes(T, E))
+
+
+def moe_route_grouped(logits, bias, topk_ids, topk_weights, expert_counts, routed_tokens, loss,
+                      scoring: str = "sigmoid", groups: int = 1, top_groups: int = 1, group_top: int = 2,
+                      renormalize: bool = True, scale: float = 1.0, loss_coef: float = 1.0,
+                      token_mask=None, workspace=None, stream=None) -> None:
+    """moe_route with softmax or sigmoid scores, a bias for the choice alone (or
+    None) and groups of experts (see include/moe_layout.h)."""
+    fn = "moe_route_grouped"
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    bf16, score = _logits_type(fn, logits), _scoring(fn, scoring)
+    if not (logits.is_cuda and logits.is_contiguous()
+            and topk_ids.dtype is _i32 and topk_ids.is_cuda and topk_ids.is_contiguous()
+            and topk_weights.dtype is _f32 and topk_weights.is_cuda and topk_weights.is_contiguous()
+            and expert_counts.dtype is _i32 and expert_counts.is_cuda and expert_counts.is_contiguous()
+            and routed_tokens.dtype is _i32 and routed_tokens.is_cuda and routed_tokens.is_contiguous()
+            and loss.dtype is _f32 and loss.is_cuda and loss.is_contiguous()):
+        _check_all((("logits", logits, logits.dtype), ("topk_ids", topk_ids, torch.int32),
+                    ("topk_weights", topk_weights, torch.float32),
+                    ("expert_counts", expert_counts, torch.int32),
+                    ("routed_tokens", routed_tokens, torch.int32), ("loss", loss, torch.float32)))
+    _check("bias", bias, torch.float32)
+    if bias is not None and bias.numel() != E:
+        raise ValueError(f"{fn}: bias has the wrong size")
+    if token_mask is not None:
+        _check("token_mask", token_mask, torch.bool)
+        if token_mask.numel() != T:
+            raise ValueError(f"{fn}: token_mask has the wrong size")
+    if topk_ids.numel() != T * K or topk_weights.numel() != T * K or expert_counts.numel() < E \
+            or routed_tokens.numel() < 1 or loss.numel() < 1:
+        raise ValueError(f"{fn}: output arrays have the wrong size")
+    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
+    st = (_lib or load()).moe_route_grouped(
+        logits.data_ptr(), bf16, T, E, K, score, _ptr(bias), groups, top_groups, group_top,
+        1 if renormalize else 0, scale, loss_coef, _ptr(token_mask), topk_ids.data_ptr(),
+        topk_weights.data_ptr(), expert_counts.data_ptr(), routed_tokens.data_ptr(), loss.data_ptr(),
+        _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+        _current_stream() if stream is None else _stream(stream))
+    if st:
+        _raise(fn, st)
+
+
+def moe_route_grouped_backward(logits, topk_ids, expert_counts, routed_tokens, grad_weights, grad_loss,
+                               grad_logits, scoring: str = "sigmoid", renormalize: bool = True,
+                               scale: float = 1.0, loss_coef: float = 1.0, stream=None) -> None:
+    """Gradient of moe_route_grouped's weights and loss to the logits;
+    grad_weights or grad_loss may be None (zero)."""
+    fn = "moe_route_grouped_backward"
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    bf16, score = _logits_type(fn, logits), _scoring(fn, scoring)
+    if not (logits.is_cuda and logits.is_contiguous()
+            and grad_logits.dtype is logits.dtype and grad_logits.is_cuda and grad_logits.is_contiguous()
+            and topk_ids.dtype is _i32 and topk_ids.is_cuda and topk_ids.is_contiguous()
+            and expert_counts.dtype is _i32 and expert_counts.is_cuda and expert_counts.is_contiguous()
+            and routed_tokens.dtype is _i32 and routed_tokens.is_cuda and routed_tokens.is_contiguous()):
+        _check_all((("logits", logits, logits.dtype), ("grad_logits", grad_logits, logits.dtype),
+                    ("topk_ids", topk_ids, torch.int32),
+                    ("expert_counts", expert_counts, torch.int32),
+                    ("routed_tokens", routed_tokens, torch.int32)))
+    _check("grad_weights", grad_weights, torch.float32)
+    _check("grad_loss", grad_loss, torch.float32)
+    if topk_ids.numel() != T * K or expert_counts.numel() < E or routed_tokens.numel() < 1 \
+            or grad_logits.numel() != T * E \
+            or (grad_weights is not None and grad_weights.numel() != T * K) \
+            or (grad_loss is not None and grad_loss.numel() != 1):
+        raise ValueError(f"{fn}: argument sizes disagree")
+    st = (_lib or load()).moe_route_grouped_backward(
+        logits.data_ptr(), bf16, T, E, K, score, 1 if renormalize else 0, scale, loss_coef,
+        topk_ids.data_ptr(), expert_counts.data_ptr(), routed_tokens.data_ptr(), _ptr(grad_weights),
+        _ptr(grad_loss), grad_logits.data_ptr(), _current_stream() if stream is None else _stream(stream))
+    if st:
+        _raise(fn, st)
 
 
 class RouteBuffers:

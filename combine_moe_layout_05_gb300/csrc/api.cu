@@ -329,6 +329,60 @@ moe_status_t moe_route_backward(const void *logits, int32_t bf16, int32_t T, int
                                                   grad_weights, grad_loss, grad_logits, stream));
 }
 
+size_t moe_route_grouped_workspace_bytes(int32_t T, int32_t E)
+{
+    if (T < 0 || T > kMostSteps || E < 1 || E > MOE_MAX_EXPERTS) return 0;
+    return moe::route_grouped_workspace_bytes(T, E);
+}
+
+moe_status_t moe_route_grouped(const void *logits, int32_t bf16, int32_t T, int32_t E, int32_t K,
+                               int32_t scoring, const float *bias, int32_t groups,
+                               int32_t top_groups, int32_t group_top, int32_t renormalize,
+                               float scale, float loss_coef, const uint8_t *token_mask,
+                               int32_t *topk_ids, float *topk_weights, int32_t *expert_counts,
+                               int32_t *routed_tokens, float *loss, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream)
+{
+    const CallRange range("moe_route_grouped");
+    if (!route_sizes_ok(T, E, K) || !flag(bf16) || !flag(scoring) || !flag(renormalize)) return MOE_ERR_INVALID_ARG;
+    if (groups < 1 || groups > MOE_MAX_GROUPS || E % groups != 0 || top_groups < 1 || top_groups > groups ||
+        group_top < 1 || group_top > 2 || K > top_groups * (E / groups))
+        return MOE_ERR_INVALID_ARG;
+    if (!expert_counts || !routed_tokens || !loss) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!logits || !topk_ids || !topk_weights)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, bf16 ? 2 : 4)) return MOE_ERR_ALIGNMENT;
+    const void *p4[] = {bias, topk_ids, topk_weights, expert_counts, routed_tokens, loss};
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return MOE_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < moe::route_grouped_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
+    return cuda_status(moe::launch_route_grouped(logits, bf16, T, E, K, scoring == MOE_SCORE_SOFTMAX, bias, groups,
+                                                 top_groups, group_top, renormalize, scale, loss_coef, token_mask,
+                                                 topk_ids, topk_weights, expert_counts, routed_tokens, loss,
+                                                 workspace, stream));
+}
+
+moe_status_t moe_route_grouped_backward(const void *logits, int32_t bf16, int32_t T, int32_t E,
+                                        int32_t K, int32_t scoring, int32_t renormalize,
+                                        float scale, float loss_coef, const int32_t *topk_ids,
+                                        const int32_t *expert_counts, const int32_t *routed_tokens,
+                                        const float *grad_weights, const float *grad_loss,
+                                        void *grad_logits, cudaStream_t stream)
+{
+    const CallRange range("moe_route_grouped_backward");
+    if (!route_sizes_ok(T, E, K) || !flag(bf16) || !flag(scoring) || !flag(renormalize)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_ids || !expert_counts || !routed_tokens || !grad_logits)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, bf16 ? 2 : 4) || !aligned(grad_logits, bf16 ? 2 : 4)) return MOE_ERR_ALIGNMENT;
+    const void *p4[] = {topk_ids, expert_counts, routed_tokens, grad_weights, grad_loss};
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return MOE_ERR_ALIGNMENT;
+    return cuda_status(moe::launch_route_grouped_backward(logits, bf16, T, E, K, scoring == MOE_SCORE_SOFTMAX, renormalize,
+                                                          scale, loss_coef, topk_ids, expert_counts, routed_tokens,
+                                                          grad_weights, grad_loss, grad_logits, stream));
+}
+
 moe_status_t moe_dispatch_int8(const void *tokens, int32_t T, int32_t H, int32_t K,
                                const int32_t *dst_row, void *packed, float *scales,
                                cudaStream_t stream)

@@ -141,6 +141,17 @@ cudaError_t launch_route_backward(const void *logits, int bf16, int T, int E, in
                                   const int32_t *routed, const float *grad_weights,
                                   const float *grad_loss, void *grad, cudaStream_t stream);
 
+// The same with a choice of scores, a bias for the choice, and groups of experts.
+size_t route_grouped_workspace_bytes(int T, int E);
+cudaError_t launch_route_grouped(const void *logits, int bf16, int T, int E, int K, int softmax, const float *bias,
+                                 int groups, int top_groups, int group_top, int renorm, float scale, float coef,
+                                 const uint8_t *mask, int32_t *ids, float *weights, int32_t *counts, int32_t *routed,
+                                 float *loss, void *workspace, cudaStream_t stream);
+cudaError_t launch_route_grouped_backward(const void *logits, int bf16, int T, int E, int K, int softmax, int renorm,
+                                          float scale, float coef, const int32_t *ids, const int32_t *counts,
+                                          const int32_t *routed, const float *grad_weights, const float *grad_loss,
+                                          void *grad, cudaStream_t stream);
+
 // Layout and dispatch together: one fused kernel when
 // layout_dispatch_fused() says the batch is small enough, else the layout
 // kernels followed by the dispatch kernel.

@@ -18,8 +18,9 @@
  *    (described with that call) it keeps no state between calls.
  *  - moe_layout, moe_dispatch, moe_combine, moe_combine_fp8,
  *    moe_combine_rank_partial, moe_dispatch_send, moe_dispatch_recv,
- *    moe_layout_dispatch, moe_route, moe_route_backward, moe_dispatch_int8,
- *    moe_expert_matmul_int8, moe_expert_matmul, moe_expert_activation_backward
+ *    moe_layout_dispatch, moe_route, moe_route_backward, moe_route_grouped,
+ *    moe_route_grouped_backward, moe_dispatch_int8, moe_expert_matmul_int8,
+ *    moe_expert_matmul, moe_expert_activation_backward
  *    and moe_expert_matmul_backward are asynchronous on `stream` (0 = legacy
  *    default stream) and may be captured into a CUDA graph.
  *  - Arguments are checked on the host before anything is enqueued.  A
@@ -71,6 +72,10 @@ typedef enum moe_status {
                                         blocks or warps expired; outputs
                                         unspecified                            */
 
+/* Scores of moe_route_grouped. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
 /* Activations of moe_expert_matmul, a(z); s is the logistic function. */
 #define MOE_ACT_NONE 0    /* z                                                      */
 #define MOE_ACT_SILU 1    /* z s(z)                                                 */
@@ -80,6 +85,7 @@ typedef enum moe_status {
 /* Limits of this implementation. */
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 32
+#define MOE_MAX_GROUPS 32
 
 /* Human-readable name of a status code (static storage, never NULL). */
 MOE_API const char *moe_status_string(moe_status_t status);
@@ -439,6 +445,79 @@ MOE_API moe_status_t moe_route_backward(const void *logits, int32_t bf16, int32_
                                         const int32_t *routed_tokens, const float *grad_weights,
                                         const float *grad_loss, void *grad_logits,
                                         cudaStream_t stream);
+
+/*
+ * moe_route_grouped -- moe_route with softmax or sigmoid scores, a bias that
+ * takes part in the choice alone, and groups of experts.
+ *
+ * Open experts and routed tokens are moe_route's.  With x the logits:
+ *
+ *   s[t,e]  MOE_SCORE_SIGMOID: 1 / (1 + exp(-x[t,e])); MOE_SCORE_SOFTMAX:
+ *           moe_route's p[t,e]; 0 for an expert that is not open
+ *   c[t,e]  s[t,e] + bias[e] of an open expert: what the choice goes by
+ *   groups  expert e is in group e / (E / groups).  A group's value is the sum of
+ *           its group_top (1 or 2) largest c (of its one open expert, the one c);
+ *           the top_groups groups of largest value stay, ties to the lowest
+ *           index, and only their experts can be chosen.
+ *   topk_ids[t,:]      the K experts of largest c left, largest first, ties to
+ *                      the lowest index; -1 where fewer are open
+ *   topk_weights[t,k]  scale * s at topk_ids[t,k], s divided by the sum of the
+ *                      token's K first when renormalize == 1; 0 where topk_ids is -1
+ *   expert_counts, routed_tokens, loss   moe_route's, with p[t,e] = s[t,e] / sum
+ *                      over e' of s[t,e']
+ *
+ * The choice is that of exact arithmetic on the given logits and bias, as far as
+ * 64 bits tell two values apart (equal ones go by index): where fp32 might order
+ * two of them wrongly the token's values are computed again in 64 bits.  Scores,
+ * weights and sums are fp32, the sums in an order that the sizes and the
+ * alignment of logits fix.  A c that is NaN ranks below every number.  A NaN logit
+ * of an open expert makes the loss NaN, and the weights in which its score takes
+ * part; +inf is a score of 1 (sigmoid), or makes its token NaN (softmax).
+ *
+ * bias        [E] fp32 or NULL (zeros), 4-byte aligned; finite.  (A balance
+ *             bias is moved between steps by expert_counts, with any rule.)
+ * 1 <= groups <= MOE_MAX_GROUPS with E % groups == 0, 1 <= top_groups <= groups
+ * (equal: all experts), K <= top_groups * (E / groups).
+ * workspace   moe_route_grouped_workspace_bytes(T,E) bytes (0 for invalid sizes).
+ * All else, and the limits, as for moe_route.
+ */
+MOE_API size_t moe_route_grouped_workspace_bytes(int32_t T, int32_t E);
+
+MOE_API moe_status_t moe_route_grouped(const void *logits, int32_t bf16, int32_t T, int32_t E,
+                                       int32_t K, int32_t scoring, const float *bias,
+                                       int32_t groups, int32_t top_groups, int32_t group_top,
+                                       int32_t renormalize, float scale, float loss_coef,
+                                       const uint8_t *token_mask, int32_t *topk_ids,
+                                       float *topk_weights, int32_t *expert_counts,
+                                       int32_t *routed_tokens, float *loss, void *workspace,
+                                       size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * moe_route_grouped_backward -- the gradient of moe_route_grouped's weights and
+ * loss with respect to the logits.
+ *
+ * The choice and the counts are constants, so the bias and the groups play no
+ * part.  With dw = scale * grad_weights, S the sum of the token's scores, sK that
+ * of the chosen ones, a[e] = grad_loss * coef * E * expert_counts[e] / (K n^2):
+ *
+ *   g[t,e] = (a[e] - sum over j of p[t,j] a[j]) / S
+ *     + renormalize == 1:  (dw[t,k] - sum over j of s[t,j] dw[t,j] / sK) / sK  and
+ *     + renormalize == 0:  dw[t,k]                       at e = topk_ids[t,k]
+ *   grad_logits[t,e] = sigmoid:  s[t,e] (1 - s[t,e]) g[t,e]
+ *                      softmax:  s[t,e] (g[t,e] - sum over j of s[t,j] g[t,j])
+ *
+ * computed in fp32 and rounded once to the logits' type; the scores are computed
+ * again from the logits.  A token whose ids are all outside [0,E) gets zeros.
+ * Arguments, sizes and no-ops as for moe_route_backward.
+ */
+MOE_API moe_status_t moe_route_grouped_backward(const void *logits, int32_t bf16, int32_t T,
+                                                int32_t E, int32_t K, int32_t scoring,
+                                                int32_t renormalize, float scale, float loss_coef,
+                                                const int32_t *topk_ids,
+                                                const int32_t *expert_counts,
+                                                const int32_t *routed_tokens,
+                                                const float *grad_weights, const float *grad_loss,
+                                                void *grad_logits, cudaStream_t stream);
 
 /*
  * moe_dispatch_int8 -- moe_dispatch with rows quantised to int8.
