@@ -434,6 +434,10 @@ def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
         _raise("moe_expert_matmul_int8", st)
 
 
+def _fits(t, dtype) -> bool:
+    return t is None or (t.dtype is dtype and t.is_cuda and t.is_contiguous())
+
+
 MOE_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
 
 
@@ -448,33 +452,37 @@ def moe_expert_matmul(x, weights, expert_offsets, out, bias=None, activation: st
                       residual=None, pre=None, dev_error=None, stream=None) -> None:
     """Packed bf16 rows times their experts' weights, with bias, activation and
     residual in the same pass (see include/moe_layout.h)."""
+    fn = "moe_expert_matmul"
     rows, H = x.shape
-    act = _activation("moe_expert_matmul", activation)
+    act = MOE_ACTIVATIONS.get(activation)
+    if act is None:
+        act = _activation(fn, activation)
     if not (x.dtype is _bf16 and x.is_cuda and x.is_contiguous()
             and weights.dtype is _bf16 and weights.is_cuda and weights.is_contiguous()
             and expert_offsets.dtype is _i32 and expert_offsets.is_cuda and expert_offsets.is_contiguous()
-            and out.dtype is _bf16 and out.is_cuda and out.is_contiguous()):
+            and out.dtype is _bf16 and out.is_cuda and out.is_contiguous() and _fits(bias, _f32)
+            and _fits(residual, _bf16) and _fits(pre, _bf16) and _fits(dev_error, _i32)):
         _check_all((("x", x, torch.bfloat16), ("weights", weights, torch.bfloat16),
-                    ("expert_offsets", expert_offsets, torch.int32), ("out", out, torch.bfloat16)))
-    _check("bias", bias, torch.float32)
-    _check("residual", residual, torch.bfloat16)
-    _check("pre", pre, torch.bfloat16)
-    _check("dev_error", dev_error, torch.int32)
+                    ("expert_offsets", expert_offsets, torch.int32), ("out", out, torch.bfloat16),
+                    ("bias", bias, torch.float32), ("residual", residual, torch.bfloat16),
+                    ("pre", pre, torch.bfloat16), ("dev_error", dev_error, torch.int32)))
     if weights.dim() != 3 or weights.shape[2] != H:
-        raise ValueError("moe_expert_matmul: argument sizes disagree")
-    E, N = weights.shape[0], weights.shape[1]
+        raise ValueError(f"{fn}: argument sizes disagree")
+    E, N, _ = weights.shape
     C = N // 2 if act == 3 else N
     if expert_offsets.numel() < E + 1 or out.numel() < rows * C or out.shape[-1] != C \
             or (bias is not None and bias.numel() != E * N) \
             or (residual is not None and (residual.numel() < rows * C or residual.shape[-1] != C)) \
             or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)):
-        raise ValueError("moe_expert_matmul: argument sizes disagree")
+        raise ValueError(f"{fn}: argument sizes disagree")
     st = (_lib or load()).moe_expert_matmul(
-        x.data_ptr(), weights.data_ptr(), _ptr(bias), expert_offsets.data_ptr(), rows, H, N, E, act,
-        _ptr(residual), _ptr(pre), out.data_ptr(), _ptr(dev_error),
+        x.data_ptr(), weights.data_ptr(), None if bias is None else bias.data_ptr(), expert_offsets.data_ptr(),
+        rows, H, N, E, act, None if residual is None else residual.data_ptr(),
+        None if pre is None else pre.data_ptr(), out.data_ptr(),
+        None if dev_error is None else dev_error.data_ptr(),
         _current_stream() if stream is None else _stream(stream))
     if st:
-        _raise("moe_expert_matmul", st)
+        _raise(fn, st)
 
 
 def moe_expert_activation_backward_workspace_bytes(rows: int, N: int, E: int) -> int:
@@ -487,17 +495,17 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
     over each expert's rows; grad_pre or grad_bias may be None (not wanted), and
     pre with activation "none"."""
     fn = "moe_expert_activation_backward"
-    act = _activation(fn, activation)
-    _check("pre", pre, torch.bfloat16)
-    _check("grad_out", grad_out, torch.bfloat16)
-    _check("grad_pre", grad_pre, torch.bfloat16)
-    _check("grad_bias", grad_bias, torch.float32)
-    _check("expert_offsets", expert_offsets, torch.int32)
+    act = MOE_ACTIVATIONS.get(activation)
+    if act is None:
+        act = _activation(fn, activation)
+    if not (_fits(pre, _bf16) and _fits(grad_out, _bf16) and _fits(grad_pre, _bf16)
+            and _fits(grad_bias, _f32) and _fits(expert_offsets, _i32)):
+        _check_all((("pre", pre, torch.bfloat16), ("grad_out", grad_out, torch.bfloat16),
+                    ("grad_pre", grad_pre, torch.bfloat16), ("grad_bias", grad_bias, torch.float32),
+                    ("expert_offsets", expert_offsets, torch.int32)))
     rows, C = grad_out.shape
     N = 2 * C if act == 3 else C
-    E = expert_offsets.numel() - 1
-    if grad_bias is not None:
-        E = grad_bias.shape[0]
+    E = expert_offsets.numel() - 1 if grad_bias is None else grad_bias.shape[0]
     if expert_offsets.numel() < E + 1 or (grad_bias is not None and grad_bias.numel() != E * N) \
             or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)) \
             or (grad_pre is not None and (grad_pre.numel() < rows * N or grad_pre.shape[-1] != N)):
@@ -505,8 +513,9 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
     if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
     st = (_lib or load()).moe_expert_activation_backward(
-        _ptr(pre), grad_out.data_ptr(), expert_offsets.data_ptr(), rows, N, E, act, _ptr(grad_pre),
-        _ptr(grad_bias), _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+        None if pre is None else pre.data_ptr(), grad_out.data_ptr(), expert_offsets.data_ptr(), rows, N, E, act,
+        None if grad_pre is None else grad_pre.data_ptr(), None if grad_bias is None else grad_bias.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
         _current_stream() if stream is None else _stream(stream))
     if st:
         _raise(fn, st)
@@ -518,12 +527,13 @@ def moe_expert_matmul_backward(grad_pre, x, weights, expert_offsets, grad_x=None
     weights (bf16, or fp32 and then added to where `accumulate`); either may be
     None (not wanted)."""
     fn = "moe_expert_matmul_backward"
-    for name, t in (("grad_pre", grad_pre), ("x", x), ("weights", weights), ("grad_x", grad_x)):
-        _check(name, t, torch.bfloat16)
     f32 = grad_weights is not None and grad_weights.dtype is _f32
-    _check("grad_weights", grad_weights, torch.float32 if f32 else torch.bfloat16)
-    _check("expert_offsets", expert_offsets, torch.int32)
-    _check("dev_error", dev_error, torch.int32)
+    if not (_fits(grad_pre, _bf16) and _fits(x, _bf16) and _fits(weights, _bf16) and _fits(grad_x, _bf16)
+            and _fits(grad_weights, _f32 if f32 else _bf16) and _fits(expert_offsets, _i32) and _fits(dev_error, _i32)):
+        _check_all((("grad_pre", grad_pre, torch.bfloat16), ("x", x, torch.bfloat16),
+                    ("weights", weights, torch.bfloat16), ("grad_x", grad_x, torch.bfloat16),
+                    ("grad_weights", grad_weights, torch.float32 if f32 else torch.bfloat16),
+                    ("expert_offsets", expert_offsets, torch.int32), ("dev_error", dev_error, torch.int32)))
     rows, N = grad_pre.shape
     like = grad_weights if weights is None else weights
     if like is None or like.dim() != 3 or like.shape[1] != N:
@@ -532,11 +542,13 @@ def moe_expert_matmul_backward(grad_pre, x, weights, expert_offsets, grad_x=None
     if expert_offsets.numel() < E + 1 \
             or (x is not None and (x.numel() < rows * H or x.shape[-1] != H)) \
             or (grad_x is not None and (grad_x.numel() < rows * H or grad_x.shape[-1] != H)) \
-            or (grad_weights is not None and tuple(grad_weights.shape) != (E, N, H)):
+            or (grad_weights is not None and grad_weights.shape != like.shape):
         raise ValueError(f"{fn}: argument sizes disagree")
     st = (_lib or load()).moe_expert_matmul_backward(
-        grad_pre.data_ptr(), _ptr(x), _ptr(weights), expert_offsets.data_ptr(), rows, H, N, E, _ptr(grad_x),
-        _ptr(grad_weights), int(f32), 1 if accumulate else 0, _ptr(dev_error),
+        grad_pre.data_ptr(), None if x is None else x.data_ptr(), None if weights is None else weights.data_ptr(),
+        expert_offsets.data_ptr(), rows, H, N, E, None if grad_x is None else grad_x.data_ptr(),
+        None if grad_weights is None else grad_weights.data_ptr(), 1 if f32 else 0, 1 if accumulate else 0,
+        None if dev_error is None else dev_error.data_ptr(),
         _current_stream() if stream is None else _stream(stream))
     if st:
         _raise(fn, st)

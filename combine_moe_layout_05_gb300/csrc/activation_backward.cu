@@ -19,7 +19,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 128;                          // rows
 constexpr int kBlocks = 152 * 4;
 constexpr int kInFlight = 4;                         // rows
 
@@ -47,7 +46,7 @@ template <bool GATED, bool BIAS>
 __global__ void __launch_bounds__(kThreads)
 activation_backward_kernel(const __nv_bfloat16 *pre, const __nv_bfloat16 *grad_out, const int32_t *__restrict__ offsets,
                            int rows, int N, int E, int activation, __nv_bfloat16 *grad_pre,
-                           int32_t *__restrict__ first_chunk, float *__restrict__ partial, int most, int columns)
+                           int32_t *__restrict__ first_chunk, float *__restrict__ partial, int most, int columns, int chunk_rows)
 {
     constexpr int HALVES = GATED ? 2 : 1;
     extern __shared__ int32_t sm[];                  // BIAS: first rows, first chunks of the experts
@@ -58,17 +57,18 @@ activation_backward_kernel(const __nv_bfloat16 *pre, const __nv_bfloat16 *grad_o
     pdl_trigger();
     int chunks, begin = 0, end = 0;
     if constexpr (BIAS) {
-        fill_table<kThreads, kChunk>(offsets, rows, E, first_row, first_tile, warp_tiles);
+        fill_table<kThreads>(offsets, rows, E, chunk_rows, first_row, first_tile, warp_tiles);
         chunks = min(first_tile[E], most);           // more only where offsets decrease
         if (blockIdx.x == 0)
             for (int e = threadIdx.x; e <= E; e += kThreads) first_chunk[e] = min(first_tile[e], most);
     } else {
         begin = max(0, min(rows, offsets[0]));
         end = max(begin, min(rows, offsets[E]));
-        chunks = (int)((unsigned)(end - begin + kChunk - 1) / kChunk);
+        chunks = (int)((unsigned)(end - begin + chunk_rows - 1) / (unsigned)chunk_rows);
     }
     const int C = N / HALVES, strips = ceil_div(C, columns * 8);
-    const int tx = threadIdx.x & (columns - 1), ty = threadIdx.x / columns, lanes = kThreads / columns;
+    const int lanes = kThreads / columns;            // of rows; the threads past them have none
+    const int ty = threadIdx.x / columns, tx = threadIdx.x - ty * columns;
     const int64_t items = (int64_t)chunks * strips;
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         const int chunk = (int)(i / strips), c = ((int)(i - (int64_t)chunk * strips) * columns + tx) * 8;
@@ -77,16 +77,16 @@ activation_backward_kernel(const __nv_bfloat16 *pre, const __nv_bfloat16 *grad_o
             int e = 0;                               // first_tile[e] <= chunk < first_tile[e + 1]
             for (int step = 512; step > 0; step >>= 1)
                 if (e + step < E && first_tile[e + step] <= chunk) e += step;
-            row = first_row[e] + (chunk - first_tile[e]) * kChunk;
-            last = min(row + kChunk, first_row[e + 1]);
+            row = first_row[e] + (chunk - first_tile[e]) * chunk_rows;
+            last = min(row + chunk_rows, first_row[e + 1]);
         } else {
-            row = begin + chunk * kChunk;
-            last = min(row + kChunk, end);
+            row = begin + chunk * chunk_rows;
+            last = min(row + chunk_rows, end);
         }
         float sum[HALVES * 8];
 #pragma unroll
         for (int j = 0; j < HALVES * 8; ++j) sum[j] = 0.0f;
-        if (c < C)
+        if (c < C && ty < lanes)
             for (int r0 = row + ty; r0 < last; r0 += lanes * kInFlight) {
                 uint4 z[kInFlight][HALVES], dy[kInFlight];
 #pragma unroll
@@ -138,7 +138,7 @@ activation_backward_kernel(const __nv_bfloat16 *pre, const __nv_bfloat16 *grad_o
             __syncthreads();
             // HALVES * 8 * columns sums, thread by thread over the row lanes
             for (int k = threadIdx.x; k < HALVES * 8 * columns; k += kThreads) {
-                const int j = k / columns, x = k & (columns - 1);
+                const int j = k / columns, x = k - j * columns;
                 float v = 0.0f;
                 for (int y = 0; y < lanes; ++y) v += red[j][y * columns + x];
                 const int at = c - tx * 8 + x * 8 + (j & 7);
@@ -171,13 +171,30 @@ bias_finish_kernel(const int32_t *__restrict__ first_chunk, const float *__restr
 }
 
 size_t table_bytes(int E) { return ((size_t)(E + 1) * 4 + 255) / 256 * 256; }
-int64_t most_chunks(int rows, int E) { return (int64_t)(rows < E ? rows : E) + rows / kChunk; }
+
+// Threads along a row, eight columns each: strips of at most 64, of equal width.
+int columns_of(int C)
+{
+    const int vectors = ceil_div(C, 8), strips = ceil_div(vectors, 64);
+    return ceil_div(vectors, strips);
+}
+
+// Rows a chunk: as many as still give every block one (4662 rows of 1032 columns,
+// 48 experts: XX us with 128 rows, XX with 32).
+int rows_a_chunk(int rows, int N)
+{
+    int chunk = 128;
+    while (chunk > 32 && (int64_t)(rows / chunk) * ceil_div(N, columns_of(N) * 8) < kBlocks) chunk /= 2;
+    return chunk;
+}
+
+int64_t most_chunks(int rows, int E, int chunk) { return (int64_t)(rows < E ? rows : E) + rows / chunk; }
 
 }  // namespace
 
 size_t activation_backward_workspace_bytes(int rows, int N, int E)
 {
-    return table_bytes(E) + ((size_t)most_chunks(rows, E) * N * 4 + 255) / 256 * 256;
+    return table_bytes(E) + ((size_t)most_chunks(rows, E, rows_a_chunk(rows, N)) * N * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_activation_backward(const void *pre, const void *grad_out, const int32_t *offsets, int rows, int N,
@@ -186,9 +203,7 @@ cudaError_t launch_activation_backward(const void *pre, const void *grad_out, co
 {
     const bool gated = activation == MOE_ACT_SWIGLU;
     const int C = gated ? N / 2 : N;
-    int columns = 64;                                // threads along a row, eight columns each
-    while (columns > 1 && columns * 4 >= C) columns /= 2;
-    const int most = (int)most_chunks(rows, E);
+    const int columns = columns_of(C), chunk = rows_a_chunk(rows, N), most = (int)most_chunks(rows, E, chunk);
     const int64_t items = (int64_t)most * ceil_div(C, columns * 8);
     const dim3 grid((unsigned)(items < 1 ? 1 : items < kBlocks ? items : kBlocks));
     int32_t *const first = static_cast<int32_t *>(workspace);
@@ -198,7 +213,7 @@ cudaError_t launch_activation_backward(const void *pre, const void *grad_out, co
     const cudaError_t e = launch_pdl(kernel, grid, dim3(kThreads), grad_bias ? 2 * (size_t)(E + 1) * 4 : 0, stream,
                                      static_cast<const __nv_bfloat16 *>(pre), static_cast<const __nv_bfloat16 *>(grad_out),
                                      offsets, rows, N, E, activation, static_cast<__nv_bfloat16 *>(grad_pre), first, partial,
-                                     most, columns);
+                                     most, columns, chunk);
     if (e != cudaSuccess || !grad_bias) return e;
     return launch_pdl(bias_finish_kernel, dim3(ceil_div(N, 128), E), dim3(128), 0, stream, first, partial, N, grad_bias);
 }

@@ -5,10 +5,10 @@
 namespace moe {
 namespace {
 
-template <bool G> using Wide = Shape<kForward, G, 2, 256, 6>;
-template <bool G> using Mid = Shape<kForward, G, 2, 128, 8>;
-template <bool G> using Narrow = Shape<kForward, G, 1, 32, 10>;
-template <bool G> using Split = Shape<kForward, G, 1, 32, 9, true>;
+template <bool G> using Wide = Shape<kForward, G, 2, 256, 6, 2>;
+template <bool G> using Mid = Shape<kForward, G, 2, 128, 8, 2>;
+template <bool G> using Narrow = Shape<kForward, G, 1, 32, 10, 1>;
+template <bool G> using Split = Shape<kForward, G, 1, 32, 9, 1, true>;
 
 // Clusters of 2, 4 and 8 splitting CTAs that the current device runs at a time,
 // looked up once for each device.

@@ -5,10 +5,10 @@
 namespace moe {
 namespace {
 
-using RowsWide = Shape<kRows, false, 2, 256, 6>;
-using RowsMid = Shape<kRows, false, 2, 128, 8>;
-using RowsNarrow = Shape<kRows, false, 1, 32, 10>;
-using Weights = Shape<kWeights, false, 2, 256, 6>;
+using RowsWide = Shape<kRows, false, 2, 256, 6, 2>;
+using RowsMid = Shape<kRows, false, 2, 128, 8, 2>;
+using RowsNarrow = Shape<kRows, false, 1, 32, 10, 1>;
+using Weights = Shape<kWeights, false, 2, 256, 6, 4>;
 
 }  // namespace
 

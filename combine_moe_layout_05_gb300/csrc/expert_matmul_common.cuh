@@ -36,7 +36,7 @@ constexpr int kMaxShared = 227 * 1024;
 // CG: CTAs a tile.  NT: rows a tile at most.  STAGES: slots of the ring.
 // GATED: the channels come in pairs (gate and up), 16 of each in 32 lanes.
 // SPLIT: a cluster's CTAs each sum a share of the contraction.
-template <Pass PASS_, bool GATED_, int CG_, int NT_, int STAGES_, bool SPLIT_ = false>
+template <Pass PASS_, bool GATED_, int CG_, int NT_, int STAGES_, int SETS_, bool SPLIT_ = false>
 struct Shape {
     static constexpr Pass PASS = PASS_;
     static constexpr bool GATED = GATED_, SPLIT = SPLIT_;
@@ -49,7 +49,7 @@ struct Shape {
     static_assert(!GATED || PASS == kForward);
     static constexpr int A = kChannels * kStep * 2, B = BR * kStep * 2, SLOT = A + B;
     static constexpr int OUT = GATED ? kChannels / 2 : kChannels;      // output channels a CTA
-    static constexpr int SETS = CG;                    // sets of four warps that store, by turns of 16 rows
+    static constexpr int SETS = SETS_;                 // sets of four warps that store, by turns of 16 rows
     static constexpr int E0 = 4, WARPS = E0 + 4 * SETS, THREADS = WARPS * 32;
     static constexpr int BARS = 3 * STAGES + 4 + 1 + SPLIT;
     static constexpr int TMEM = 2 * NT;                // two accumulators
@@ -247,7 +247,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     if (warp == 1) tmem_alloc<S::CG>(smem_addr(flags), S::TMEM);
     pdl_wait();
     pdl_trigger();
-    fill_table<S::THREADS, S::NT>(offsets, z.rows, z.E, first_row, first_tile,
+    fill_table<S::THREADS>(offsets, z.rows, z.E, S::NT, first_row, first_tile,
                                   reinterpret_cast<int *>(generic + S::OFFTURN));     // not in use yet
     if (dev_error && clear && blockIdx.x == 0 && tid == 0) *dev_error = 0;
     if constexpr (S::CG == 2 || S::SPLIT) cluster_sync_all();
@@ -477,6 +477,29 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 }
                 continue;
             }
+            if (S::PASS == kWeights && st.f32) {
+                // A lane a channel: a column is 128 bytes of a row.
+                const int c = ch0 + lane;
+                float *const to = static_cast<float *>(st.out) + row0 * z.channels + c;
+                uint32_t v[16];
+                if (16 * set >= t.n) release();
+                for (int c0 = 16 * set; c0 < t.n; c0 += 16 * S::SETS) {
+                    tmem_load_x16(acc + c0, v);
+                    tmem_wait_ld();
+                    if (c0 + 16 * S::SETS >= t.n) release();
+                    float old[16];
+                    if (st.accumulate) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (c0 + j < t.valid && c < z.channels) old[j] = to[(size_t)(c0 + j) * z.channels];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c0 + j < t.valid && c < z.channels)
+                            to[(size_t)(c0 + j) * z.channels] = st.accumulate ? old[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+                }
+                continue;
+            }
             uint32_t next[16];
             if (16 * set >= t.n) release();
             else {
@@ -563,22 +586,9 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                             }
                     }
                 }
-                if (S::PASS == kWeights && st.f32) {
-                    float *const o = static_cast<float *>(st.out) + row * z.channels + ch0;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int r = 8 * (j >> 2 & 1) + 2 * (lane & 3) + (j & 1);
-                        const int c = 16 * (j >> 3) + 8 * (j >> 1 & 1) + (lane >> 2);
-                        if (r < left && ch0 + c < z.channels) {
-                            float *const to = o + (size_t)r * z.channels + c;
-                            *to = st.accumulate ? *to + v[j] : v[j];
-                        }
-                    }
-                } else {
-                    turn(v, LANES);
-                    store_rows<LANES, false>(turned, out + row * z.channels, z.channels, left, ch0, z.channels, vectors);
-                    __syncwarp();
-                }
+                turn(v, LANES);
+                store_rows<LANES, false>(turned, out + row * z.channels, z.channels, left, ch0, z.channels, vectors);
+                __syncwarp();
             }
         }
     }

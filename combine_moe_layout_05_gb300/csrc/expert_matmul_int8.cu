@@ -227,7 +227,7 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
     pdl_trigger();
 
     static_assert(S::WARPS * 4 <= 4 * S::SETS * 1024);
-    fill_table<S::THREADS, S::NT>(offsets, rows, E, first_row, first_tile,
+    fill_table<S::THREADS>(offsets, rows, E, S::NT, first_row, first_tile,
                                   reinterpret_cast<int *>(generic + S::OFFTURN));     // not in use yet
     if (dev_error && blockIdx.x == 0 && tid == 0) *dev_error = 0;
     if constexpr (S::CG == 2 || S::SPLIT) cluster_sync_all();

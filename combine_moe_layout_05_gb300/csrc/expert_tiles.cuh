@@ -29,12 +29,12 @@ struct Table {
     const int *first_tile;     // [E + 1]
 };
 
-// Fills the table, for a whole block of THREADS threads: tiles an expert, then
+// Fills the table, for a whole block of THREADS threads: tiles of NT rows an expert, then
 // their running sum; thread t has PER experts in a row.  warp_tiles: a word a
 // warp.  Ends with the block synchronised; tcgen05 work of before is ordered.
-template <int THREADS, int NT>
-__device__ __forceinline__ void fill_table(const int32_t *offsets, int rows, int E, int *first_row, int *first_tile,
-                                           int *warp_tiles)
+template <int THREADS>
+__device__ __forceinline__ void fill_table(const int32_t *offsets, int rows, int E, int NT, int *first_row,
+                                           int *first_tile, int *warp_tiles)
 {
     constexpr int PER = MOE_MAX_EXPERTS / THREADS + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -46,7 +46,7 @@ __device__ __forceinline__ void fill_table(const int32_t *offsets, int rows, int
         if (e <= E) {
             const int lo = max(0, min(rows, offsets[e]));
             first_row[e] = lo;
-            if (e < E) tiles[j] = ceil_div(max(0, min(rows, offsets[e + 1]) - lo), NT);
+            if (e < E) tiles[j] = (int)((unsigned)(max(0, min(rows, offsets[e + 1]) - lo) + NT - 1) / (unsigned)NT);
         }
         sum += tiles[j];
     }

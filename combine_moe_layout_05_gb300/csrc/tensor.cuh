@@ -298,6 +298,15 @@ __device__ __forceinline__ void tmem_load_16x16(uint32_t addr, uint32_t *v)
                  : "r"(addr) : "memory");
 }
 
+// 16 columns of a warp's 32 TMEM lanes, one lane a thread.
+__device__ __forceinline__ void tmem_load_x16(uint32_t addr, uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(addr) : "memory");
+}
+
 // Four 8 x 8 blocks of 16-bit words, turned: block q's word (i, j), held by
 // thread 4i + j/2, goes to word i of the row that thread 8q + j points at.
 __device__ __forceinline__ void store_turned_x4(uint32_t row, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
