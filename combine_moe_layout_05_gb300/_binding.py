@@ -438,6 +438,16 @@ def _fits(t, dtype) -> bool:
     return t is None or (t.dtype is dtype and t.is_cuda and t.is_contiguous())
 
 
+def _current_device() -> int:
+    return torch.cuda.current_device() if _get_device is None else _get_device()
+
+
+def _check_device(fn: str, t) -> None:
+    """A launch goes to the current device: refuse memory of another one."""
+    if t.is_cuda and t.get_device() != _current_device():
+        raise ValueError(f"{fn}: the tensors are on device {t.get_device()}, the current one is {_current_device()}")
+
+
 MOE_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
 
 
@@ -475,6 +485,7 @@ def moe_expert_matmul(x, weights, expert_offsets, out, bias=None, activation: st
             or (residual is not None and (residual.numel() < rows * C or residual.shape[-1] != C)) \
             or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)):
         raise ValueError(f"{fn}: argument sizes disagree")
+    _check_device(fn, x)
     st = (_lib or load()).moe_expert_matmul(
         x.data_ptr(), weights.data_ptr(), None if bias is None else bias.data_ptr(), expert_offsets.data_ptr(),
         rows, H, N, E, act, None if residual is None else residual.data_ptr(),
@@ -512,6 +523,7 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
         raise ValueError(f"{fn}: argument sizes disagree")
     if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
+    _check_device(fn, grad_out)
     st = (_lib or load()).moe_expert_activation_backward(
         None if pre is None else pre.data_ptr(), grad_out.data_ptr(), expert_offsets.data_ptr(), rows, N, E, act,
         None if grad_pre is None else grad_pre.data_ptr(), None if grad_bias is None else grad_bias.data_ptr(),
@@ -544,6 +556,7 @@ def moe_expert_matmul_backward(grad_pre, x, weights, expert_offsets, grad_x=None
             or (grad_x is not None and (grad_x.numel() < rows * H or grad_x.shape[-1] != H)) \
             or (grad_weights is not None and grad_weights.shape != like.shape):
         raise ValueError(f"{fn}: argument sizes disagree")
+    _check_device(fn, grad_pre)
     st = (_lib or load()).moe_expert_matmul_backward(
         grad_pre.data_ptr(), None if x is None else x.data_ptr(), None if weights is None else weights.data_ptr(),
         expert_offsets.data_ptr(), rows, H, N, E, None if grad_x is None else grad_x.data_ptr(),
@@ -681,6 +694,7 @@ def moe_route_grouped(logits, bias, topk_ids, topk_weights, expert_counts, route
         raise ValueError(f"{fn}: output arrays have the wrong size")
     if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
+    _check_device(fn, logits)
     st = (_lib or load()).moe_route_grouped(
         logits.data_ptr(), bf16, T, E, K, score, _ptr(bias), groups, top_groups, group_top,
         1 if renormalize else 0, scale, loss_coef, _ptr(token_mask), topk_ids.data_ptr(),
@@ -716,6 +730,7 @@ def moe_route_grouped_backward(logits, topk_ids, expert_counts, routed_tokens, g
             or (grad_weights is not None and grad_weights.numel() != T * K) \
             or (grad_loss is not None and grad_loss.numel() != 1):
         raise ValueError(f"{fn}: argument sizes disagree")
+    _check_device(fn, logits)
     st = (_lib or load()).moe_route_grouped_backward(
         logits.data_ptr(), bf16, T, E, K, score, 1 if renormalize else 0, scale, loss_coef,
         topk_ids.data_ptr(), expert_counts.data_ptr(), routed_tokens.data_ptr(), _ptr(grad_weights),

@@ -452,8 +452,9 @@ moe_status_t moe_expert_activation_backward(const void *pre, const void *grad_ou
     if (!product_sizes_ok(rows, 8, N, E) || activation < MOE_ACT_NONE || activation > MOE_ACT_SWIGLU ||
         N % (activation == MOE_ACT_SWIGLU ? 16 : 8) != 0)
         return MOE_ERR_INVALID_ARG;
-    if (!expert_offsets || (!grad_pre && !grad_bias)) return MOE_ERR_INVALID_ARG;
-    if (rows > 0 && (!grad_out || (!pre && activation != MOE_ACT_NONE))) return MOE_ERR_INVALID_ARG;
+    if (!expert_offsets) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && ((!grad_pre && !grad_bias) || !grad_out || (!pre && activation != MOE_ACT_NONE)))
+        return MOE_ERR_INVALID_ARG;
     if (!aligned(pre, 16) || !aligned(grad_out, 16) || !aligned(grad_pre, 16) || !aligned(expert_offsets, 4) ||
         !aligned(grad_bias, 4))
         return MOE_ERR_ALIGNMENT;
@@ -478,8 +479,8 @@ moe_status_t moe_expert_matmul_backward(const void *grad_pre, const void *x, con
     if (!product_sizes_ok(rows, H, N, E) || N % 8 != 0 || !flag(weights_f32) || !flag(accumulate) ||
         (accumulate && !weights_f32))
         return MOE_ERR_INVALID_ARG;
-    if ((!grad_x && !grad_weights) || !expert_offsets) return MOE_ERR_INVALID_ARG;
-    if (rows > 0 && (!grad_pre || (grad_x && !weights) || (grad_weights && !x))) return MOE_ERR_INVALID_ARG;
+    if (!expert_offsets) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && ((!grad_x && !grad_weights) || !grad_pre || (grad_x && !weights) || (grad_weights && !x))) return MOE_ERR_INVALID_ARG;
     const void *p16[] = {grad_pre, x, weights, grad_x, grad_weights}, *p4[] = {expert_offsets, dev_error};
     for (const void *p : p16)
         if (!aligned(p, 16)) return MOE_ERR_ALIGNMENT;

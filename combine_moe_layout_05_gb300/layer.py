@@ -1,9 +1,21 @@
-"""An MoE layer put together from the library's calls.
+"""MoE layers put together from the library's calls.
 
-``route`` is the router with its gradient (moe_route / moe_route_backward under
-autograd), for training and serving.  ``Int8Experts``, for serving, is a gated
-MLP whose experts' weights are int8 with a scale for each output channel.  It
-has no gradient, and refuses inputs that ask for one:
+``route`` and ``route_grouped`` are the routers with their gradients
+(moe_route / moe_route_grouped and their backward calls under autograd), for
+training and serving.  ``expert_linear`` is the experts' bf16 product with bias,
+activation and residual, under autograd, and ``Experts`` a gated MLP of them,
+with a shared expert where the model has one:
+
+    moe_layout           slots of the routing
+    moe_dispatch         rows packed by expert
+    moe_expert_matmul    gate and up projections, SwiGLU  [rows, I]
+    moe_expert_matmul    down projection                  [rows, H]
+    moe_combine          the routing-weighted sum         [T, H]
+    moe_expert_matmul    (shared) gate and up, SwiGLU; down, the routed sum its residual
+
+``Int8Experts``, for serving, is a gated MLP whose experts' weights are int8 with
+a scale for each output channel.  It has no gradient, and refuses inputs that
+ask for one:
 
     moe_layout           slots of the routing
     moe_dispatch_int8    rows to int8, packed by expert
@@ -62,6 +74,200 @@ def route(logits: torch.Tensor, K: int, renormalize: bool = True, loss_coef: flo
     (``topk_ids.masked_fill(full, -1)``); after an edit in place backward
     raises."""
     return _Route.apply(logits, K, renormalize, loss_coef, token_mask)
+
+
+class _RouteGrouped(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, K, scoring, groups, top_groups, group_top, renormalize, scale, loss_coef, token_mask):
+        T, E = logits.shape
+        logits, dev = logits.contiguous(), logits.device
+        i32 = dict(dtype=torch.int32, device=dev)
+        ids, counts, routed = torch.empty((T, K), **i32), torch.empty(E, **i32), torch.empty(1, **i32)
+        weights = torch.empty((T, K), dtype=torch.float32, device=dev)
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        workspace = torch.empty(moe.moe_route_grouped_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
+        moe.moe_route_grouped(logits, bias, ids, weights, counts, routed, loss, scoring, groups, top_groups, group_top,
+                              renormalize, scale, loss_coef, token_mask, workspace)
+        ctx.settings = scoring, renormalize, scale, loss_coef
+        ctx.save_for_backward(logits, ids, counts, routed)
+        ctx.mark_non_differentiable(ids, counts)
+        return ids, weights, counts, loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _ids, grad_weights, _counts, grad_loss):
+        logits, ids, counts, routed = ctx.saved_tensors
+        grad = torch.empty_like(logits)
+        moe.moe_route_grouped_backward(logits, ids, counts, routed, grad_weights.float().contiguous(),
+                                       grad_loss.float().reshape(1).contiguous(), grad, *ctx.settings)
+        return (grad,) + (None,) * 10
+
+
+def route_grouped(logits: torch.Tensor, K: int, bias: torch.Tensor | None = None, scoring: str = "sigmoid",
+                  groups: int = 1, top_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+                  scale: float = 1.0, loss_coef: float = 1.0, token_mask: torch.Tensor | None = None):
+    """Router logits [T, E] to (topk_ids, topk_weights, expert_counts, loss) as moe_route_grouped has
+    them; topk_weights and loss carry gradients to the logits, the bias (fp32, for the choice alone)
+    has none: ``move_balance_bias`` moves it.  As with ``route`` the outputs are not to be edited in place."""
+    if bias is not None:
+        bias = bias.detach()
+    return _RouteGrouped.apply(logits, bias, K, scoring, groups, top_groups, group_top, renormalize, scale, loss_coef,
+                               token_mask)
+
+
+def move_balance_bias(bias: torch.Tensor, expert_counts: torch.Tensor, rate: float) -> torch.Tensor:
+    """One step of the balance bias, in place: up by `rate` for experts below the mean of the counts,
+    down for those above it."""
+    counts = expert_counts.to(bias.dtype)
+    with torch.no_grad():
+        return bias.add_(torch.sign(counts.mean() - counts), alpha=rate)
+
+
+class _ExpertLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weights, expert_offsets, bias, activation, residual, error, train):
+        rows, (E, N, _) = x.shape[0], weights.shape
+        x, weights = x.contiguous(), weights.contiguous()
+        bias = None if bias is None else bias.contiguous()
+        residual = None if residual is None else residual.contiguous()
+        out = torch.empty((rows, N // 2 if activation == "swiglu" else N), dtype=torch.bfloat16, device=x.device)
+        pre = torch.empty((rows, N), dtype=torch.bfloat16, device=x.device) if train and activation != "none" else None
+        moe.moe_expert_matmul(x, weights, expert_offsets, out, bias, activation, residual, pre,
+                              None if error is None else error[:1])
+        ctx.activation, ctx.error = activation, error
+        ctx.save_for_backward(x, weights, expert_offsets, pre)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        x, weights, offsets, pre = ctx.saved_tensors
+        need_x, need_w, _, need_bias, _, need_residual = ctx.needs_input_grad[:6]
+        grad_out = grad_out.contiguous()
+        grad_x = grad_w = grad_bias = None
+        if need_x or need_w or need_bias:
+            rows, (E, N, _) = x.shape[0], weights.shape
+            grad_pre, workspace = grad_out, None
+            if need_bias:
+                grad_bias = torch.empty((E, N), dtype=torch.float32, device=x.device)
+                workspace = torch.empty(moe.moe_expert_activation_backward_workspace_bytes(rows, N, E),
+                                        dtype=torch.uint8, device=x.device)
+            if pre is not None:
+                grad_pre = torch.empty_like(pre)
+            if pre is not None or need_bias:
+                moe.moe_expert_activation_backward(pre, grad_out, offsets, None if pre is None else grad_pre,
+                                                   ctx.activation, grad_bias, workspace)
+            if need_x or need_w:
+                grad_x = torch.empty_like(x) if need_x else None
+                grad_w = torch.empty_like(weights) if need_w else None
+                moe.moe_expert_matmul_backward(grad_pre, x, weights, offsets, grad_x, grad_w,
+                                               dev_error=None if ctx.error is None else ctx.error[1:2])
+        return grad_x, grad_w, None, grad_bias, None, grad_out if need_residual else None, None, None
+
+
+def expert_linear(x: torch.Tensor, weights: torch.Tensor, expert_offsets: torch.Tensor,
+                  bias: torch.Tensor | None = None, activation: str = "none", residual: torch.Tensor | None = None,
+                  dev_error: torch.Tensor | None = None) -> torch.Tensor:
+    """Packed rows [rows, H] times their experts' weights [E, N, H] (both bf16) as moe_expert_matmul has
+    it, with gradients of x, weights, bias ([E, N]) and residual.  The rows of no expert are unspecified,
+    in the output and in x's gradient.  dev_error, [2] int32: the forward's error word and the backward's."""
+    train = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weights, bias))
+    least = 16 if activation == "swiglu" else 8
+    if train and weights.shape[1] % least:
+        raise ValueError(f"expert_linear: the gradient needs N % {least} == 0, N is {weights.shape[1]}")
+    return _ExpertLinear.apply(x, weights, expert_offsets, None if bias is None else bias.float(), activation, residual,
+                               dev_error, train)
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dst_row):
+        packed = torch.empty((dst_row.numel(), x.shape[1]), dtype=torch.bfloat16, device=x.device)
+        moe.moe_dispatch(x.contiguous(), dst_row, packed)
+        ctx.save_for_backward(dst_row)
+        return packed
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        dst_row, = ctx.saved_tensors
+        T, H = dst_row.shape[0], grad.shape[1]
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=grad.device)
+        # each token's K rows added up
+        moe.moe_combine(grad.contiguous(), torch.ones(dst_row.shape, dtype=torch.float32, device=grad.device), dst_row, out)
+        return out, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, topk_weights, dst_row):
+        out = torch.empty((dst_row.shape[0], rows.shape[1]), dtype=torch.bfloat16, device=rows.device)
+        topk_weights = topk_weights.contiguous()
+        moe.moe_combine(rows.contiguous(), topk_weights, dst_row, out)
+        ctx.save_for_backward(rows, topk_weights, dst_row)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        rows, weights, dst_row = ctx.saved_tensors
+        need_rows, need_weights, _ = ctx.needs_input_grad
+        kept, grad = dst_row >= 0, grad.float()
+        at = dst_row.clamp(min=0).long()
+        # an entry that has no row gets row 0's index with nothing in it: added, not copied
+        grad_rows = torch.zeros_like(rows) if need_rows else None
+        grad_weights = torch.empty_like(weights) if need_weights else None
+        for k in range(dst_row.shape[1]):
+            keep = kept[:, k, None]
+            if need_rows:
+                g = torch.where(keep, weights[:, k, None] * grad, 0.0)
+                grad_rows.index_add_(0, at[:, k], g.to(rows.dtype))
+            if need_weights:
+                y = torch.where(keep, rows[at[:, k]].float(), 0.0)
+                grad_weights[:, k] = (y * grad).sum(1)
+        return grad_rows, grad_weights, None
+
+
+class Experts:
+    """A layer of gated experts in bf16, for training and serving: gate_up [E, 2 I, H] and down [E, H, I],
+    with biases [E, 2 I] and [E, H] where the model has them.  shared: (gate_up [2 J, H], down [H, J]) of an
+    expert that every token goes through.
+
+    ``dev_error``, [9] int32 on the device, holds the last call's error words: the layout's
+    (MOE_DEV_ERR_EXPERT_RANGE where an id is -1), then for each of the four products the forward's and
+    the backward's, whose MOE_DEV_ERR_TIMEOUT says that the output or the gradient is unspecified."""
+
+    def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, gate_up_bias: torch.Tensor | None = None,
+                 down_bias: torch.Tensor | None = None, shared: tuple[torch.Tensor, torch.Tensor] | None = None,
+                 ranks: int = 1):
+        E, two_i, H = gate_up.shape
+        if down.shape != (E, H, two_i // 2) or two_i % 2:
+            raise ValueError("Experts: gate_up must be [E, 2 I, H] and down [E, H, I]")
+        if shared is not None and (shared[0].dim() != 2 or shared[0].shape[1] != H or shared[0].shape[0] % 2
+                                   or shared[1].shape != (H, shared[0].shape[0] // 2)):
+            raise ValueError("Experts: shared must be gate_up [2 J, H] and down [H, J]")
+        self.E, self.H, self.I, self.R = E, H, two_i // 2, ranks
+        self.gate_up, self.down = gate_up, down
+        self.gate_up_bias, self.down_bias, self.shared = gate_up_bias, down_bias, shared
+        self.dev_error = None
+
+    def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor) -> torch.Tensor:
+        """x [T, H] bf16 and its routing to [T, H] bf16."""
+        T, K, dev = x.shape[0], topk_ids.shape[1], x.device
+        self.dev_error = err = torch.zeros(9, dtype=torch.int32, device=dev)
+        lay = moe.LayoutBuffers(T, K, self.E, self.R, device=dev)
+        lay.dev_error = err[:1]
+        lay.run(topk_ids)
+        rows = _Dispatch.apply(x, lay.dst_row)
+        rows = expert_linear(rows, self.gate_up, lay.expert_offsets, self.gate_up_bias, "swiglu", dev_error=err[1:3])
+        rows = expert_linear(rows, self.down, lay.expert_offsets, self.down_bias, dev_error=err[3:5])
+        out = _Combine.apply(rows, topk_weights, lay.dst_row)
+        if self.shared is None:
+            return out
+        every = torch.zeros(2, dtype=torch.int32, device=dev)
+        every[1:].fill_(T)
+        mid = expert_linear(x, self.shared[0][None], every, None, "swiglu", dev_error=err[5:7])
+        return expert_linear(mid, self.shared[1][None], every, residual=out, dev_error=err[7:])
 
 
 class Int8Experts:
