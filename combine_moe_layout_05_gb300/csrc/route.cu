@@ -190,7 +190,7 @@ route_kernel(const L *__restrict__ logits, int T, int E, int any_k, int renorm,
             routed += numbers == 0 && picks > 0;
         }
     if (lane == 0) atomicAdd(&cnt[E], routed);
-    route_totals<kRouteWarps, SINGLE>(sums, cnt, inbox, E, K, part, o);
+    route_totals<kRouteWarps, SINGLE>(sums, E, cnt, inbox, E, K, part, o);
 }
 
 template <int NV, int W, typename L>

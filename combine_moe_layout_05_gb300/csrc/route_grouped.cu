@@ -84,40 +84,22 @@ __device__ __forceinline__ T group_value(T a, T b, int group_top)
     return group_top == 2 && b > -INFINITY ? a + b : a;
 }
 
-// A lane's NV values to and from a row of E in shared memory (VEC: E % 4 == 0, so
-// that rows start on 16 bytes).
-template <int NV, bool VEC>
-__device__ __forceinline__ void store_own(float *row, int E, int lane, const float (&v)[NV])
+// A lane's NV values to and from a row of 32 NV in shared memory.
+template <int NV>
+__device__ __forceinline__ void store_own(float *row, int lane, const float (&v)[NV])
 {
     static_assert(NV % 4 == 0);
 #pragma unroll
-    for (int j = 0; j < NV; j += 4) {
-        const int e = lane * NV + j;
-        if constexpr (VEC) {
-            if (e < E) *reinterpret_cast<float4 *>(row + e) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (e + i < E) row[e + i] = v[j + i];
-        }
-    }
+    for (int j = 0; j < NV; j += 4)
+        *reinterpret_cast<float4 *>(row + lane * NV + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
 }
 
-template <int NV, bool VEC>
-__device__ __forceinline__ void load_own(const float *row, int E, int lane, float (&v)[NV])
+template <int NV>
+__device__ __forceinline__ void load_own(const float *row, int lane, float (&v)[NV])
 {
 #pragma unroll
     for (int j = 0; j < NV; j += 4) {
-        const int e = lane * NV + j;
-        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if constexpr (VEC) {
-            if (e < E) q = *reinterpret_cast<const float4 *>(row + e);
-        } else {
-            if (e < E) q.x = row[e];
-            if (e + 1 < E) q.y = row[e + 1];
-            if (e + 2 < E) q.z = row[e + 2];
-            if (e + 3 < E) q.w = row[e + 3];
-        }
+        const float4 q = *reinterpret_cast<const float4 *>(row + lane * NV + j);
         v[j] = q.x;
         v[j + 1] = q.y;
         v[j + 2] = q.z;
@@ -482,19 +464,19 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
 {
     const int K = KT > 0 ? KT : any_k;
     constexpr int WARPS = kWarps, THREADS = WARPS * 32;
-    constexpr bool VEC = W > 1;
     extern __shared__ float sm[];
-    float *const sums = sm;                              // [WARPS][E]; until then a warp's keys
-    float *const rows = sums + (size_t)WARPS * E;        // [WARPS][E], a warp's logits
-    float *const bias = rows + (size_t)WARPS * E;        // [E]
-    int32_t *const cnt = reinterpret_cast<int32_t *>(bias + E);             // [E] and the routed tokens
+    constexpr int PITCH = 32 * NV;                       // a row's words: no lane's values are outside
+    float *const sums = sm;                              // [WARPS][PITCH]; until then a warp's keys
+    float *const rows = sums + WARPS * PITCH;            // [WARPS][PITCH], a warp's logits
+    float *const bias = rows + WARPS * PITCH;            // [PITCH], zeros from E on
+    int32_t *const cnt = reinterpret_cast<int32_t *>(bias + PITCH);         // [E] and the routed tokens
     uint32_t *const inbox = reinterpret_cast<uint32_t *>(cnt + E + 1);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     for (int e = threadIdx.x; e <= E; e += THREADS) cnt[e] = 0;
     pdl_wait();
     pdl_trigger();
-    for (int e = threadIdx.x; e < E; e += THREADS) bias[e] = r.bias ? r.bias[e] : 0.0f;
+    for (int e = threadIdx.x; e < PITCH; e += THREADS) bias[e] = r.bias && e < E ? r.bias[e] : 0.0f;
     constexpr bool kAhead = NV <= 8;
     const int stride = gridDim.x * WARPS;
     int t = blockIdx.x * WARPS + warp;
@@ -517,18 +499,20 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
     const bool whole = size % NV == 0 && ((size / NV) & (size / NV - 1)) == 0;
     const int group_lanes = whole ? size / NV : 32 >> (r.groups == 1 ? 0 : 32 - __clz(r.groups - 1));
     const int my_group = lane * NV / size, in_group = lane * NV - my_group * size;
-    float *const key_row = sums + warp * E, *const x_row = rows + warp * E;
+    float *const key_row = sums + warp * PITCH, *const x_row = rows + warp * PITCH;
     int routed = 0;                                      // tokens with a first pick (lane 0)
     float acc[NV], largest = 0.0f, low = INFINITY, high = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NV; ++j) acc[j] = 0.0f;
     {
         float b[NV];
-        load_own<NV, VEC>(bias, E, lane, b);
+        load_own<NV>(bias, lane, b);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (lane * NV + j < E) low = fminf(low, b[j]);
-            high = fmaxf(high, b[j]);
+            if (lane * NV + j < E) {
+                low = fminf(low, b[j]);
+                high = fmaxf(high, b[j]);
+            }
         }
     }
     low = -warp_max(-low);
@@ -592,12 +576,12 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
         }
         // key: what the picks go by; -inf where an expert is not open or its group is out
         float key[NV];
-        load_own<NV, VEC>(bias, E, lane, key);
+        load_own<NV>(bias, lane, key);
 #pragma unroll
         for (int j = 0; j < NV; ++j) key[j] = x[j] == -INFINITY ? x[j] : rankable(s[j] + key[j]);
         __syncwarp();                                    // the last token's are read
-        store_own<NV, VEC>(key_row, E, lane, key);
-        store_own<NV, VEC>(x_row, E, lane, x);
+        store_own<NV>(key_row, lane, key);
+        store_own<NV>(x_row, lane, x);
         Room room{0.0f, 0.0f};
         if (limited || !by_logits)
             room = room_of(r.softmax ? row.inv : fminf(fmaxf(warp_max(lane_max<NV>(key)) + largest, 0.0f), 1.0f), r.softmax,
@@ -646,7 +630,7 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
                                          row.m, largest, by_logits, kept);
             }
             // from shared memory, so that they need no registers past the call above
-            load_own<NV, VEC>(by_logits ? x_row : key_row, E, lane, key);
+            load_own<NV>(by_logits ? x_row : key_row, lane, key);
             if (whole) {
                 const bool in = kept >> (lane / group_lanes & 31) & 1;
 #pragma unroll
@@ -663,14 +647,14 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
                 }
             }
         } else if (by_logits) {
-            load_own<NV, VEC>(x_row, E, lane, key);
+            load_own<NV>(x_row, lane, key);
         }
         if (by_logits) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) key[j] = key[j] == -INFINITY ? key[j] : rankable(key[j] + 0.0f);
         }
         __syncwarp();
-        store_own<NV, VEC>(key_row, E, lane, key);
+        store_own<NV>(key_row, lane, key);
 
         float mine = -INFINITY;
         // Pick number `lane`: its key, and the lane that holds it (route.cu).
@@ -737,7 +721,7 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
         if (lane < picks && mine > -INFINITY) {
             int before = __popc(alike & ((1u << lane) - 1)), place = 0;
             float owners[NV];
-            load_own<NV, VEC>(key_row, E, from, owners);
+            load_own<NV>(key_row, from, owners);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const bool same = owners[j] == mine;
@@ -770,11 +754,10 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
     }
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if (lane * NV + j < E) sums[warp * E + lane * NV + j] = acc[j];
+    for (int j = 0; j < NV; ++j) key_row[lane * NV + j] = acc[j];
     if (lane == 0) atomicAdd(&cnt[E], routed);
-    if (single) route_totals<WARPS, true>(sums, cnt, inbox, E, K, part, o);
-    else route_totals<WARPS, false>(sums, cnt, inbox, E, K, part, o);
+    if (single) route_totals<WARPS, true>(sums, PITCH, cnt, inbox, E, K, part, o);
+    else route_totals<WARPS, false>(sums, PITCH, cnt, inbox, E, K, part, o);
 }
 
 template <int NV, int W, typename L>
@@ -783,7 +766,7 @@ cudaError_t run_grouped(const void *logits, int T, int E, int K, const Rules &r,
                         cudaStream_t s)
 {
     constexpr int WARPS = kWarps;
-    const size_t smem = route_smem<WARPS>(E) + (size_t)(WARPS + 1) * E * 4;
+    const size_t smem = route_smem<0>(E) + (2 * WARPS + 1) * 32 * NV * 4;
     const RouteOut o{counts, routed, loss, coef};
     const int single = single_blocks<WARPS>(T, E);
     constexpr int KT = W > 1 ? 8 : 0;                    // as in route.cu

@@ -36,13 +36,13 @@ size_t route_smem(int E)
     return ((size_t)(WARPS + 1) * E + 1 + 2 * (E + kSingleCluster) + kSingleCluster) * 4;
 }
 
-// For a whole block: sums [WARPS][E] each warp's, cnt [E] and the routed tokens
+// For a whole block: sums [WARPS][pitch] each warp's, cnt [E] and the routed tokens
 // the block's.  SINGLE: the grid is one cluster, which writes the results;
 // otherwise every cluster writes its totals to part[cluster]: E probability
 // sums, E counts and the routed tokens.  Ends the cluster barrier that the
 // kernel began (arrive) when it started.
 template <int WARPS, bool SINGLE>
-__device__ __forceinline__ void route_totals(const float *sums, const int32_t *cnt, uint32_t *inbox, int E, int K,
+__device__ __forceinline__ void route_totals(const float *sums, int pitch, const int32_t *cnt, uint32_t *inbox, int E, int K,
                                              uint32_t *part, const RouteOut &o)
 {
     constexpr int THREADS = WARPS * 32;
@@ -58,7 +58,7 @@ __device__ __forceinline__ void route_totals(const float *sums, const int32_t *c
     for (int e = threadIdx.x; e < E; e += THREADS) {
         float v = sums[e];
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w) v += sums[w * E + e];
+        for (int w = 1; w < WARPS; ++w) v += sums[w * pitch + e];
         const uint32_t to = cluster_addr(smem_addr(inbox + rank * box + e / blocks), e % blocks);
         st_cluster_u32(to, __float_as_uint(v));
         st_cluster_u32(to + 4 * share, (uint32_t)cnt[e]);
