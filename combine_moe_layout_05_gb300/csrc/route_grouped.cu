@@ -28,6 +28,8 @@ namespace {
 constexpr int kWarps = 8;                            // a block
 // Blocks a multiprocessor, by the registers of NV values a lane.
 constexpr int per_sm(int NV) { return NV <= 12 ? 3 : NV <= 16 ? 2 : 1; }
+// Words of a lane's sorted list: none where a lane has too many values to sort.
+constexpr int list_of(int NV) { return NV <= 16 ? NV + 4 : 0; }
 constexpr int kOpen = -2;                            // in a token's first id: chosen after the loop
 constexpr float kUnit = 5.9604645e-8f;               // 2^-24
 
@@ -41,6 +43,15 @@ struct Rules {
 __device__ __forceinline__ float rankable(float c) { return fmaxf(c, -FLT_MAX); }
 
 // The two largest of a warp's pairs a >= b (each lane's), over `lanes` lanes.
+__device__ __forceinline__ void top_two(float &a, float &b, int lanes)
+{
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+        const float a2 = __shfl_xor_sync(kFullMask, a, o), b2 = __shfl_xor_sync(kFullMask, b, o);
+        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+        a = fmaxf(a, a2);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ void top_two(T &a, T &b, int lanes)
 {
@@ -466,10 +477,12 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
     constexpr int WARPS = kWarps, THREADS = WARPS * 32;
     extern __shared__ float sm[];
     constexpr int PITCH = 32 * NV;                       // a row's words: no lane's values are outside
+    constexpr int LIST = list_of(NV);
     float *const sums = sm;                              // [WARPS][PITCH]; until then a warp's keys
     float *const rows = sums + WARPS * PITCH;            // [WARPS][PITCH], a warp's logits
     float *const bias = rows + WARPS * PITCH;            // [PITCH], zeros from E on
-    int32_t *const cnt = reinterpret_cast<int32_t *>(bias + PITCH);         // [E] and the routed tokens
+    float *const lists = bias + PITCH;                   // [WARPS][32][LIST], a lane's keys sorted, then -inf
+    int32_t *const cnt = reinterpret_cast<int32_t *>(lists + WARPS * 32 * LIST);        // [E] and the routed tokens
     uint32_t *const inbox = reinterpret_cast<uint32_t *>(cnt + E + 1);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -482,10 +495,13 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
     int t = blockIdx.x * WARPS + warp;
     float ahead[NV];
     uint8_t open = 1;
+    const L *next_row = logits + (size_t)t * E;
+    const size_t row_step = (size_t)stride * E, id_step = (size_t)stride * K;
     auto fetch = [&](int u) {
         if (u >= T) return;
-        load_row<NV, W>(logits + (size_t)u * E, E, lane, ahead);
+        load_row<NV, W>(next_row, E, lane, ahead);
         if (mask) open = mask[u];
+        next_row += row_step;
     };
     if constexpr (kAhead) fetch(t);
     __syncthreads();
@@ -522,20 +538,22 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
     bool again = false;                                  // some token's choice is open
 
     // A token's weights, counts and ids from lane k's expert and its score.
-    auto finish = [&](int t, int id, float w) {
+    auto finish = [&](size_t at, int id, float w) {
         if (r.renorm) {
             const float all = lanes_sum(w, k_lanes);
             if (all != 0.0f) w = __fdividef(w, all);
         }
         if (lane < K) {
-            ids[(size_t)t * K + lane] = id;
-            weights[(size_t)t * K + lane] = w * r.scale;
+            ids[at + lane] = id;
+            weights[at + lane] = w * r.scale;
         }
         if (id >= 0) atomicAdd(&cnt[id], 1);
         routed += id >= 0;
     };
 
-    for (; t < T; t += stride) {
+    // what fp32 cannot tell apart where scores may be up to 1
+    const Room most_room = room_of(1.0f, false, largest);
+    for (size_t first_id = (size_t)t * K; t < T; t += stride, first_id += id_step) {
         if constexpr (!kAhead) fetch(t);
         float x[NV];
 #pragma unroll
@@ -582,10 +600,7 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
         __syncwarp();                                    // the last token's are read
         store_own<NV>(key_row, lane, key);
         store_own<NV>(x_row, lane, x);
-        Room room{0.0f, 0.0f};
-        if (limited || !by_logits)
-            room = room_of(r.softmax ? row.inv : fminf(fmaxf(warp_max(lane_max<NV>(key)) + largest, 0.0f), 1.0f), r.softmax,
-                           largest);
+        Room room = r.softmax ? room_of(row.inv, true, largest) : most_room;
         bool unsure = false;
         if (limited) {
             float a = -INFINITY, c = -INFINITY;
@@ -612,22 +627,23 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
             if (lane >= r.groups) value = -INFINITY;
             // the best groups one by one; lane g has group g's value
             unsigned out = r.groups == 32 ? kFullMask : (1u << r.groups) - 1;
-            float rest = value, least = -INFINITY;
+            float rest = value, least = 0.0f;
             for (int k = 0; k < r.top_groups; ++k) {
-                const float best = warp_max(rest);
-                if (best > -INFINITY) least = best;
-                const unsigned at = __ballot_sync(kFullMask, rest == best) & out;
-                const int g = __ffs(at) - 1;
+                least = warp_max(rest);
+                const int g = __ffs(__ballot_sync(kFullMask, rest == least) & out) - 1;
                 out &= ~(1u << g);
                 if (lane == g) rest = -INFINITY;
             }
             unsigned kept = ~out;
-            const float most = warp_max(rest);
+            const float most = warp_max(rest);           // above -inf: so are all that stay
             if (most > -INFINITY && least - most <= room.groups) {
-                const unsigned close = __ballot_sync(kFullMask, value > -INFINITY && value >= least - room.groups &&
-                                                                    value <= most + room.groups);
-                unsure = !careful_groups(key_row, x_row, bias, E, group_lanes, (c > -INFINITY ? c : a) - room.keys, close, r,
-                                         row.m, largest, by_logits, kept);
+                if (!r.softmax) room = room_of(fminf(fmaxf(warp_max(a) + largest, 0.0f), 1.0f), false, largest);
+                if (least - most <= room.groups) {
+                    const unsigned close = __ballot_sync(kFullMask, value > -INFINITY && value >= least - room.groups &&
+                                                                        value <= most + room.groups);
+                    unsure = !careful_groups(key_row, x_row, bias, E, group_lanes, (c > -INFINITY ? c : a) - room.keys, close,
+                                             r, row.m, largest, by_logits, kept);
+                }
             }
             // from shared memory, so that they need no registers past the call above
             load_own<NV>(by_logits ? x_row : key_row, lane, key);
@@ -656,14 +672,20 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
         __syncwarp();
         store_own<NV>(key_row, lane, key);
 
+        // Pick number `lane`: its key, and the lane that holds it.  Each pick is one
+        // maximum over the lanes' best; its owner's next best comes from a sorted list.
         float mine = -INFINITY;
-        // Pick number `lane`: its key, and the lane that holds it (route.cu).
         int from = 0;
         float next[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) next[j] = key[j];
-        if constexpr (NV <= 16) sort_values<NV>(next);
-        float best = NV <= 16 ? next[0] : lane_max<NV>(next);
+        const float *list = lists + (warp * 32 + lane) * LIST;
+        if constexpr (LIST > 0) {
+            sort_values<NV>(next);
+            store_own<NV>(lists + warp * 32 * LIST + lane * (LIST - NV), lane, next);
+            lists[(warp * 32 + lane) * LIST + NV] = -INFINITY;
+        }
+        float best = LIST > 0 ? next[0] : lane_max<NV>(next);
         auto pick = [&](int k) {
             const float top = warp_max(best);
             const int owner = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
@@ -671,11 +693,8 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
                 mine = top;
                 from = owner;
             }
-            if constexpr (NV <= 16) {
-#pragma unroll
-                for (int j = 0; j + 1 < NV; ++j) next[j] = lane == owner ? next[j + 1] : next[j];
-                next[NV - 1] = lane == owner ? -INFINITY : next[NV - 1];
-                best = next[0];
+            if constexpr (LIST > 0) {
+                if (lane == owner && top > -INFINITY) best = *++list;
             } else if (lane == owner) {
                 int at = 0;
 #pragma unroll
@@ -697,14 +716,16 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
         // last one are picked too.
         int picks = K;
         bool near = false;
+        const float below = __shfl_down_sync(kFullMask, mine, 1);
         if (!by_logits) {
-            const float left = warp_max(best), below = __shfl_down_sync(kFullMask, mine, 1);
-            const float after = lane == K - 1 ? left : below;
-            near = __any_sync(kFullMask, lane < K && after > -INFINITY && mine - after <= room.keys);
-            if (near) {
-                const float last = __shfl_sync(kFullMask, mine, K - 1);
+            const float left = warp_max(best), after = lane == K - 1 ? left : below;
+            const float gap = lane < K && after > -INFINITY ? mine - after : INFINITY;
+            if (__any_sync(kFullMask, gap <= room.keys)) {
+                const float last = __shfl_sync(kFullMask, mine, K - 1), top = __shfl_sync(kFullMask, mine, 0);
+                if (!r.softmax) room = room_of(fminf(fmaxf(top + largest, 0.0f), 1.0f), false, largest);
+                near = __any_sync(kFullMask, gap <= room.keys);
 #pragma unroll 1
-                for (float top = left; top > -INFINITY && last - top <= room.keys; top = warp_max(best)) {
+                for (float next = left; near && next > -INFINITY && last - next <= room.keys; next = warp_max(best)) {
                     if (picks == 32) {
                         unsure = true;               // too many for a warp
                         break;
@@ -713,8 +734,11 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
                 }
             }
         }
-        // A pick's place among its owner's keys (equal ones were picked in order), and its logit.
-        const unsigned alike = __match_any_sync(kFullMask, __float_as_int(mine)) & __match_any_sync(kFullMask, from);
+        // A pick's place among its owner's keys, and its logit.  Equal keys are next to
+        // one another, and were picked in order.
+        unsigned alike = 0;
+        if (__any_sync(kFullMask, near || (below == mine && mine > -INFINITY)))
+            alike = __match_any_sync(kFullMask, __float_as_int(mine)) & __match_any_sync(kFullMask, from);
         __syncwarp();
         int id = -1;
         float chosen = -INFINITY;
@@ -722,11 +746,14 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
             int before = __popc(alike & ((1u << lane) - 1)), place = 0;
             float owners[NV];
             load_own<NV>(key_row, from, owners);
+            if (before == 0) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const bool same = owners[j] == mine;
-                if (same && before == 0) place = j;
-                before -= same;
+                for (int j = NV - 1; j >= 0; --j)
+                    if (owners[j] == mine) place = j;
+            } else {
+#pragma unroll 1
+                for (place = 0;; ++place)
+                    if (key_row[from * NV + place] == mine && before-- == 0) break;
             }
             id = from * NV + place;
             chosen = x_row[id];
@@ -737,10 +764,10 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
         }
         if (lane >= K) id = -1;
         if (!unsure) {
-            finish(t, id, id >= 0 ? score_of(chosen, r, row) : 0.0f);
+            finish(first_id, id, id >= 0 ? score_of(chosen, r, row) : 0.0f);
         } else {
             again = true;
-            if (lane == 0) ids[(size_t)t * K] = kOpen;
+            if (lane == 0) ids[first_id] = kOpen;
         }
     }
     if (again) {
@@ -749,7 +776,7 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
             if (ids[(size_t)t * K] != kOpen) continue;
             const L *const at = logits + (size_t)t * E;
             const Settled c = settle<L>(at, E, K, r, bias, largest, by_logits, key_row, x_row);
-            finish(t, c.id, c.score);
+            finish((size_t)t * K, c.id, c.score);
         }
     }
     __syncwarp();
@@ -766,7 +793,7 @@ cudaError_t run_grouped(const void *logits, int T, int E, int K, const Rules &r,
                         cudaStream_t s)
 {
     constexpr int WARPS = kWarps;
-    const size_t smem = route_smem<0>(E) + (2 * WARPS + 1) * 32 * NV * 4;
+    const size_t smem = route_smem<0>(E) + ((2 * WARPS + 1) * NV + WARPS * list_of(NV)) * 32 * 4;
     const RouteOut o{counts, routed, loss, coef};
     const int single = single_blocks<WARPS>(T, E);
     constexpr int KT = W > 1 ? 8 : 0;                    // as in route.cu
