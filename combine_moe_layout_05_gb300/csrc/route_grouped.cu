@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kWarps = 8;                            // a block
 // Blocks a multiprocessor, by the registers of NV values a lane.
-constexpr int per_sm(int NV) { return NV <= 12 ? 3 : NV <= 16 ? 2 : 1; }
+constexpr int per_sm(int NV) { return NV <= 8 ? 4 : NV <= 12 ? 3 : NV <= 16 ? 2 : 1; }
 // Words of a lane's sorted list: none where a lane has too many values to sort.
 constexpr int list_of(int NV) { return NV <= 16 ? NV + 4 : 0; }
 constexpr int kOpen = -2;                            // in a token's first id: chosen after the loop

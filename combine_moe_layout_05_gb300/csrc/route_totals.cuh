@@ -12,7 +12,7 @@ namespace moe {
 namespace {
 
 constexpr int kRouteCluster = 8;                    // blocks that add their sums up together
-constexpr int kMostClusters = 64;                   // that the finishing kernel adds up
+constexpr int kMostClusters = 96;                   // that the finishing kernel adds up
 constexpr int kSingleCluster = 8;                   // blocks of the form that needs one launch
 
 // The call's last sums, thread e for expert e: p and c are expert e's totals.
@@ -121,9 +121,10 @@ route_finish_kernel(const uint32_t *__restrict__ part, int clusters, int E, int 
     pdl_wait();
     pdl_trigger();
     const size_t row = 2 * (size_t)E + 1;
-    static_assert(kMostClusters <= 64);
+    static_assert(kMostClusters <= 96);
     int n = lane < clusters ? (int)part[lane * row + 2 * E] : 0;
     if (lane + 32 < clusters) n += (int)part[(lane + 32) * row + 2 * E];
+    if (lane + 64 < clusters) n += (int)part[(lane + 64) * row + 2 * E];
     float p = 0.0f;
     int c = 0;
     if (e < E) {
