@@ -62,7 +62,7 @@ cudaError_t launch(const void *x, const void *w, const int32_t *offsets, int row
         const uint64_t dims[4] = {(uint64_t)H, (uint64_t)channels, 2, (uint64_t)E};
         const uint64_t strides[3] = {(uint64_t)H, (uint64_t)channels * H, (uint64_t)N * H};
         const uint32_t box[4] = {kStep, 16, 2, 1};
-        if (!bf16_map(&map_w, w, 4, dims, strides, box)) return cudaErrorInvalidValue;
+        if (!tensor_map(&map_w, w, 4, dims, strides, box)) return cudaErrorInvalidValue;
     } else if (!rows_map(&map_w, w, (uint64_t)E * N, H, kChannels)) {
         return cudaErrorInvalidValue;
     }

@@ -8,7 +8,7 @@ namespace {
 using RowsWide = Shape<kRows, false, 2, 256, 6, 2>;
 using RowsMid = Shape<kRows, false, 2, 128, 8, 2>;
 using RowsNarrow = Shape<kRows, false, 1, 32, 10, 1>;
-using Weights = Shape<kWeights, false, 2, 256, 6, 4>;
+using Weights = Shape<kWeights, false, 2, 256, 5, 2>;
 
 }  // namespace
 
@@ -23,7 +23,7 @@ cudaError_t launch_expert_matmul_rows(const void *grad_pre, const void *w, const
     CUtensorMap map_w;                                 // [E, N, H]: past an expert's N are zeros, not the next one's
     const uint64_t dims[3] = {(uint64_t)H, (uint64_t)N, (uint64_t)E}, strides[2] = {(uint64_t)H, (uint64_t)N * H};
     const uint32_t box[3] = {64, kStep, 1};
-    if (!bf16_map(&map_w, w, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!tensor_map(&map_w, w, 3, dims, strides, box)) return cudaErrorInvalidValue;
     const Sizes z{rows, N, H, N, E};
     const Store st{nullptr, nullptr, nullptr, grad_x, MOE_ACT_NONE, 0, 0};
     auto go = [&](auto shape) {
@@ -45,15 +45,18 @@ cudaError_t launch_expert_matmul_weights(const void *grad_pre, const void *x, co
     int sms = 0;
     const cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    CUtensorMap map_x;
-    RowMaps map_g;
-    if (!rows_map(&map_x, x, rows, H, kStep) || !rows_map(&map_g.box[0], grad_pre, rows, N, kStep))
+    CUtensorMap map_g;
+    RowMaps map_x;
+    if (!rows_map(&map_g, grad_pre, rows, N, kStep) || !rows_map(&map_x.box[0], x, rows, H, kStep))
         return cudaErrorInvalidValue;
-    for (int m = 1; m < kBoxes; ++m) map_g.box[m] = map_g.box[0];
+    const uint64_t dims[3] = {(uint64_t)H, (uint64_t)N, (uint64_t)E}, strides[2] = {(uint64_t)H, (uint64_t)N * H};
+    const uint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
+    if (!tensor_map(&map_x.box[1], grad_w, 3, dims, strides, box, f32 != 0)) return cudaErrorInvalidValue;
+    for (int m = 2; m < kBoxes; ++m) map_x.box[m] = map_x.box[0];
     const Sizes z{rows, N, H, 0, E};
     const Store st{nullptr, nullptr, nullptr, grad_w, MOE_ACT_NONE, f32, accumulate};
-    const int64_t tiles = (int64_t)E * ceil_div(N, Weights::NT) * ceil_div(H, Weights::OUT * Weights::CG);
-    return run<Weights>(map_x, map_g, offsets, z, st, tiles, sms, 1, dev_error, clear, limit, stall, stream);
+    const int64_t tiles = (int64_t)E * ceil_div(H, Weights::NT) * ceil_div(N, Weights::OUT * Weights::CG);
+    return run<Weights>(map_g, map_x, offsets, z, st, tiles, sms, 1, dev_error, clear, limit, stall, stream);
 }
 
 }  // namespace moe

@@ -6,10 +6,10 @@
 //   kRows     grad_x[r, h]  = sum_n grad_pre[r, n] w[e, n, h]
 //   kWeights  grad_w[e, n, h] = sum over e's rows r of grad_pre[r, n] x[r, h]
 //
-// In each the instruction's M are 128 channels a CTA (256 a pair): output
-// channels, or the hidden size; an expert with one row still feeds 128 lanes.
-// Its N are a tile's rows (kWeights: rows of the weights), as many as are left,
-// rounded up.  Operands lie in shared memory as the copy engine's 128-byte
+// In each the instruction's M are 128 "channels" a CTA (256 a pair): output
+// channels, the hidden size, or (kWeights) the weights' rows; an expert with one
+// row still feeds 128 lanes.  Its N are a tile's "rows": packed rows, or (kWeights)
+// the hidden size, as many as are left, rounded up.  Operands lie in shared memory as the copy engine's 128-byte
 // swizzle leaves them, in the order that global memory has: along the
 // contraction (K-major) for x and the forward weights, across it (MN-major)
 // for the weights in kRows and for both operands in kWeights.
@@ -19,7 +19,8 @@
 // the first CTA that a step has landed, and in kWeights clears the rows of the
 // next expert in an expert's last step; 4 SETS add the bias, activate, add the
 // residual, turn the sums in shared memory and store them, while the other
-// accumulator is summed.
+// accumulator is summed.  In kWeights a lane of the sums is a row of the output,
+// so they go to memory as they come, a sector a lane.
 #pragma once
 
 #include "activation.cuh"
@@ -54,21 +55,23 @@ struct Shape {
     static constexpr int BARS = 3 * STAGES + 4 + 1 + SPLIT;
     static constexpr int TMEM = 2 * NT;                // two accumulators
     static_assert((TMEM & (TMEM - 1)) == 0 && TMEM >= 32 && TMEM <= 512);
-    // ring, 16 x 32 outputs of each storing warp, the other CTAs' sums (SPLIT:
-    // NT x 128 fp32), barriers, flags, expert table
+    // ring, 16 x 32 outputs (kWeights: 32 lines) of each storing warp, the other
+    // CTAs' sums (SPLIT: NT x 128 fp32), barriers, flags, expert table
+    static constexpr int TURN = PASS == kWeights ? 4096 : 1024;
     static constexpr int OFFTURN = STAGES * SLOT;
-    static constexpr int OFFBOX = OFFTURN + 4 * SETS * 1024;
+    static constexpr int OFFBOX = OFFTURN + 4 * SETS * TURN;
     static constexpr int OFFBAR = OFFBOX + SPLIT * NT * kChannels * 4;
     static constexpr int OFFTAB = OFFBAR + (BARS * 8 + 15) / 16 * 16 + 32;
     static constexpr int bytes(int E) { return OFFTAB + 2 * (E + 1) * 4; }
     static_assert(bytes(MOE_MAX_EXPERTS) <= kMaxShared);
-    static_assert(WARPS * 4 <= 4 * SETS * 1024);
+    static_assert(WARPS * 4 <= 4 * SETS * TURN);
+    static_assert(OFFTURN % 1024 == 0);
 };
 
 // Copies of rows come in these heights; a tile takes the one that covers its share.
 constexpr int kBoxes = 4, kLeastBox = 16;
 struct RowMaps {
-    CUtensorMap box[kBoxes];    // 16, 32, 64, 128 rows; kWeights: box[0] alone, 64 x 64
+    CUtensorMap box[kBoxes];    // 16, 32, 64, 128 rows; kWeights: 64 x 64, and the output's
 };
 
 // What is stored, and where.
@@ -81,9 +84,8 @@ struct Store {
     int f32, accumulate;            // kWeights: out is fp32; is added to
 };
 
-// The sizes of a product.  channels: of the output.  N: kForward, kRows: the
-// weights' rows an expert; kWeights: the same, cut into tiles.  depth: the
-// contraction's length (kWeights: each expert's rows).
+// The sizes of a product.  N: the weights' rows an expert.  channels: the length
+// of an output row.  depth: the contraction's length (kWeights: each expert's rows).
 struct Sizes {
     int rows, N, channels, depth, E;
 };
@@ -100,13 +102,15 @@ __device__ __forceinline__ Job job_of(const Table &t, const Sizes &z, int channe
 {
     Job j;
     if constexpr (S::PASS == kWeights) {
-        const int q = (int)((unsigned)i / (unsigned)channel_tiles);
-        j.e = (int)((unsigned)q / (unsigned)row_tiles);
-        j.row = (q - j.e * row_tiles) * S::NT;
-        j.valid = min(S::NT, z.N - j.row);
+        // tiles of the same rows of the weights follow each other: they are written
+        // about together, and memory likes its rows whole
+        const int q = (int)((unsigned)i / (unsigned)row_tiles);
+        j.e = (int)((unsigned)q / (unsigned)channel_tiles);
+        j.row = (i - q * row_tiles) * S::NT;
+        j.valid = min(S::NT, z.channels - j.row);
         j.share = ceil_div(j.valid, 128) * 64;
         j.n = 2 * j.share;
-        j.channel = (i - q * channel_tiles) * S::OUT * S::CG;
+        j.channel = (q - j.e * channel_tiles) * S::OUT * S::CG;
         j.first = uniform(t.first_row[j.e]);
         const int count = max(0, uniform(t.first_row[j.e + 1]) - j.first);
         j.steps = (int)((unsigned)(count + kStep - 1) / kStep);
@@ -255,7 +259,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     const uint32_t tmem = uniform(flags[0]);
 
     const Table table{first_row, first_tile};
-    const int channel_tiles = ceil_div(z.channels, S::OUT * S::CG), row_tiles = ceil_div(z.N, S::NT);
+    const int channel_tiles = ceil_div(S::PASS == kWeights ? z.N : z.channels, S::OUT * S::CG);
+    const int row_tiles = ceil_div(z.channels, S::NT);
     const int items = (S::PASS == kWeights ? z.E * row_tiles : uniform(first_tile[z.E])) * channel_tiles;
     auto job = [&](int i, int &at) {
         Job j = job_of<S>(table, z, channel_tiles, row_tiles, i, at);
@@ -392,7 +397,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         }
     } else if (warp >= S::E0) {
         const int quarter = warp & 3, set = (warp - S::E0) >> 2;
-        const uint32_t turned = base + S::OFFTURN + (warp - S::E0) * 1024;
+        const uint32_t turned = base + S::OFFTURN + (warp - S::E0) * S::TURN;
         constexpr int LANES = S::OUT / 4;              // output channels a warp
         __nv_bfloat16 *const out = static_cast<__nv_bfloat16 *>(st.out);
         const bool vectors = z.channels % 8 == 0;
@@ -401,8 +406,7 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         for (int i = group; i < items && ok; i += groups) {
             const Job t = job(i, at);
             const int ch0 = t.channel + (int)rank * S::OUT + quarter * LANES;
-            // row of the output that the tile's first is, and its element
-            const size_t row0 = S::PASS == kWeights ? (size_t)t.e * z.N + t.row : (size_t)t.row;
+            const size_t row0 = (size_t)t.row;
             float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if constexpr (S::PASS == kForward && !S::SPLIT)
                 if (st.bias) {
@@ -412,13 +416,79 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                         if (c < z.channels) bias[q] = st.bias[(size_t)t.e * z.N + c + (8 * q < LANES ? 0 : z.channels)];
                     }
                 }
-            if (S::PASS == kWeights && t.steps <= 0) {                 // an expert without rows
-                if (st.accumulate) continue;
-                for (int r = set; r < t.valid; r += S::SETS) {
-                    const int c = ch0 + lane;
-                    if (c >= z.channels) continue;
-                    if (st.f32) static_cast<float *>(st.out)[(row0 + r) * z.channels + c] = 0.0f;
-                    else out[(row0 + r) * z.channels + c] = __float2bfloat16_rn(0.0f);
+            if constexpr (S::PASS == kWeights) {
+                // A lane is a row of the output: 64 columns of 32 rows at a time go to
+                // shared memory and from there, as whole lines, to the output (plain
+                // stores of 64 bytes a row left the load/store unit 88 % busy and memory
+                // at 4.9 TB/s).
+                const bool none = t.steps <= 0;        // an expert without rows
+                if (none && st.accumulate) continue;
+                const int d = u & 1;
+                const uint32_t acc = tmem + d * S::NT + ((uint32_t)quarter << 21);
+                if (!none) {
+                    ok = __all_sync(kFullMask, mbar_wait_bounded(full_d(d), u >> 1 & 1, waits));
+                    ++u;
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                auto release = [&] {                   // all read: the accumulator is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && !none) mbar_arrive_pair(cluster_addr(empty_d(d), 0));
+                };
+                if (64 * set >= t.n) release();
+                for (int c0 = 64 * set; c0 < t.n; c0 += 64 * S::SETS) {
+                    uint32_t v[4][16];
+                    if (!none) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_load_x16(acc + c0 + 16 * q, v[q]);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 64; ++q) v[q >> 4][q & 15] = 0;
+                    }
+                    if (c0 + 64 * S::SETS >= t.n) release();
+                    const bool inside = c0 < t.valid && ch0 < z.N;
+                    const uint32_t row = turned + lane * 128;
+                    auto send = [&](int c) {
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (inside && t.row + c < z.channels) {
+                                if (st.accumulate) tile_add_3d(&map_b.box[1], t.row + c, ch0, t.e, turned);
+                                else tile_store_3d(&map_b.box[1], t.row + c, ch0, t.e, turned);
+                            }
+                            bulk_commit();
+                        }
+                    };
+                    auto settle = [&] {                // the last lines have been read from shared memory
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                    };
+                    if (st.f32) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            settle();
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const uint32_t *w = v[2 * h + (q >> 2)] + 4 * (q & 3);
+                                sts128(row + ((q ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+                            }
+                            send(c0 + 32 * h);
+                        }
+                    } else {
+                        settle();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint32_t *w = v[q >> 1] + 8 * (q & 1);
+                            uint32_t y[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                y[j] = pack_bf16x2_rn(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+                            sts128(row + ((q ^ (lane & 7)) << 4), y[0], y[1], y[2], y[3]);
+                        }
+                        send(c0);
+                    }
                 }
                 continue;
             }
@@ -474,29 +544,6 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                         if (st.residual) y += __bfloat162float(st.residual[(row0 + r) * z.channels + c]);
                         out[(row0 + r) * z.channels + c] = __float2bfloat16_rn(y);
                     }
-                }
-                continue;
-            }
-            if (S::PASS == kWeights && st.f32) {
-                // A lane a channel: a column is 128 bytes of a row.
-                const int c = ch0 + lane;
-                float *const to = static_cast<float *>(st.out) + row0 * z.channels + c;
-                uint32_t v[16];
-                if (16 * set >= t.n) release();
-                for (int c0 = 16 * set; c0 < t.n; c0 += 16 * S::SETS) {
-                    tmem_load_x16(acc + c0, v);
-                    tmem_wait_ld();
-                    if (c0 + 16 * S::SETS >= t.n) release();
-                    float old[16];
-                    if (st.accumulate) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c0 + j < t.valid && c < z.channels) old[j] = to[(size_t)(c0 + j) * z.channels];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c0 + j < t.valid && c < z.channels)
-                            to[(size_t)(c0 + j) * z.channels] = st.accumulate ? old[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
                 }
                 continue;
             }
@@ -591,6 +638,8 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 __syncwarp();
             }
         }
+        if constexpr (S::PASS == kWeights)
+            if (lane == 0) bulk_wait_all();            // given up or not, before the block leaves
     }
     __syncwarp();
     tc_fence_before();
@@ -601,10 +650,10 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     if (warp == 1) tmem_free<S::CG>(tmem, S::TMEM);
 }
 
-// A tensor of bf16, innermost dimension first; strides of the others in
+// A tensor of bf16 or fp32, innermost dimension first; strides of the others in
 // elements (multiples of 8); boxes of 128-byte lines, swizzled, zeros outside.
-bool bf16_map(CUtensorMap *map, const void *p, int rank, const uint64_t *dims, const uint64_t *strides,
-              const uint32_t *box)
+bool tensor_map(CUtensorMap *map, const void *p, int rank, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box, bool f32 = false)
 {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
@@ -614,9 +663,9 @@ bool bf16_map(CUtensorMap *map, const void *p, int rank, const uint64_t *dims, c
         d[i] = dims[i];
         b[i] = box[i];
         ones[i] = 1;
-        if (i > 0) s[i - 1] = strides[i - 1] * 2;
+        if (i > 0) s[i - 1] = strides[i - 1] * (f32 ? 4 : 2);
     }
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(p), d, s, b, ones,
+    return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(p), d, s, b, ones,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -626,7 +675,7 @@ bool rows_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t width, ui
 {
     const uint64_t dims[2] = {width, rows}, strides[1] = {width};
     const uint32_t boxes[2] = {kStep, box};
-    return bf16_map(map, p, 2, dims, strides, boxes);
+    return tensor_map(map, p, 2, dims, strides, boxes);
 }
 
 template <typename S>

@@ -169,6 +169,20 @@ __device__ __forceinline__ void tile_load_4d(uint32_t dst, const CUtensorMap *ma
                  :: "r"(dst), "l"(map), "r"(c), "r"(r), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
+// A tile from shared memory to a three-dimensional tensor, or added to what is
+// there; what lies outside the tensor is left out.  In the thread's bulk group.
+__device__ __forceinline__ void tile_store_3d(const CUtensorMap *map, int c, int r, int z, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 :: "l"(map), "r"(c), "r"(r), "r"(z), "r"(src) : "memory");
+}
+
+__device__ __forceinline__ void tile_add_3d(const CUtensorMap *map, int c, int r, int z, uint32_t src)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 :: "l"(map), "r"(c), "r"(r), "r"(z), "r"(src) : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
