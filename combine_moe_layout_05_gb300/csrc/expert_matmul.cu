@@ -75,10 +75,12 @@ cudaError_t launch(const void *x, const void *w, const int32_t *offsets, int row
         return run<S>(map_w, map_x, offsets, z, st, tiles, sms, parts, dev_error, 1, wait_limit, stall, stream);
     };
     // Few tiles: share the contraction, as far as every tile's cluster runs at
-    // once and the steps saved outweigh the cluster's barriers.
+    // once and the contraction is long enough for the cluster's exchange (16 or 32
+    // rows of one expert, shared out and not: 7168 -> 2048 15.8 and 19.5 us, 4096 ->
+    // 4096 11.9 and 12.3, 2048 -> 2048 9.6 and 7.8).
     const int64_t tiles = most_tiles<Split<G>>(rows, E) * ceil_div(channels, Split<G>::OUT);
     const int steps = ceil_div(H, kStep);
-    if (tiles * 2 <= sms && steps >= 32) {
+    if (tiles * 2 <= sms && steps >= 64) {
         int clusters[3];
         e = split_clusters<G>(clusters);
         if (e != cudaSuccess) return e;
@@ -87,8 +89,14 @@ cudaError_t launch(const void *x, const void *w, const int32_t *offsets, int row
             if (tiles <= clusters[p / 4]) parts = p;
         if (parts > 1) return go(Split<G>{}, parts);
     }
+    // By rows an expert, on average.  Narrow and Mid: 7.8 and 10.9 us at 16 rows of one
+    // expert (2048 -> 2048), equal to 3 % with 64 experts to 32 rows, where Narrow
+    // begins to read weights twice (94.1 and 85.4 us at 48).  Mid and Wide, 64 experts,
+    // 2048 -> 2048: 89.6 and 93.2 us at 96 rows each, 106 and 99 at 160, 381 and 338 at
+    // 1024; 512 -> 4096: 51.7 and 52.0 at 96, 59.4 and 57.1 at 160, 251 and 212 at 1024;
+    // skewed (48 experts, 2056 -> 1001): 42 and 48 us at 50 on average, 53 and 51 at 97.
     if (rows <= 16 * E) return go(Narrow<G>{}, 1);
-    return rows >= 192 * E ? go(Wide<G>{}, 1) : go(Mid<G>{}, 1);
+    return rows >= 96 * E ? go(Wide<G>{}, 1) : go(Mid<G>{}, 1);
 }
 
 }  // namespace

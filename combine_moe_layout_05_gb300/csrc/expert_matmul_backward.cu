@@ -33,8 +33,10 @@ cudaError_t launch_expert_matmul_rows(const void *grad_pre, const void *w, const
         const int64_t tiles = most_tiles<S>(rows, E) * ceil_div(H, S::OUT * S::CG);
         return run<S>(map_w, map_g, offsets, z, st, tiles, sms, 1, dev_error, 1, limit, stall, stream);
     };
+    // As for the product itself (64 experts, 2048 -> 2048, Mid and Wide: 85.4 and 85.0 us
+    // at 64 rows an expert, 88.4 and 87.2 at 96, 103 and 92.5 at 160, 392 and 339 at 1024).
     if (rows <= 16 * E) return go(RowsNarrow{});
-    return rows >= 192 * E ? go(RowsWide{}) : go(RowsMid{});
+    return rows >= 96 * E ? go(RowsWide{}) : go(RowsMid{});
 }
 
 cudaError_t launch_expert_matmul_weights(const void *grad_pre, const void *x, const int32_t *offsets, int rows, int H,
