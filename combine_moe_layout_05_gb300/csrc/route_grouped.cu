@@ -24,7 +24,6 @@
 namespace moe {
 namespace {
 
-
 constexpr int kWarps = 8;                            // a block
 // Blocks a multiprocessor, by the registers of NV values a lane.
 constexpr int per_sm(int NV) { return NV <= 8 ? 4 : NV <= 12 ? 3 : NV <= 16 ? 2 : 1; }
@@ -752,7 +751,7 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
                     if (owners[j] == mine) place = j;
             } else {
 #pragma unroll 1
-                for (place = 0;; ++place)
+                for (place = 0; place < NV - 1; ++place)
                     if (key_row[from * NV + place] == mine && before-- == 0) break;
             }
             id = from * NV + place;
