@@ -438,13 +438,12 @@ def _fits(t, dtype) -> bool:
     return t is None or (t.dtype is dtype and t.is_cuda and t.is_contiguous())
 
 
-def _current_device() -> int:
-    return torch.cuda.current_device() if _get_device is None else _get_device()
+_current_device = torch.cuda.current_device if _get_device is None else _get_device
 
 
-def _check_device(fn: str, t) -> None:
-    """A launch goes to the current device: refuse memory of another one."""
-    if t.is_cuda and t.get_device() != _current_device():
+def _refuse_device(fn: str, t) -> None:
+    """A launch goes to the current device: memory of another one is refused."""
+    if t.is_cuda:
         raise ValueError(f"{fn}: the tensors are on device {t.get_device()}, the current one is {_current_device()}")
 
 
@@ -485,7 +484,8 @@ def moe_expert_matmul(x, weights, expert_offsets, out, bias=None, activation: st
             or (residual is not None and (residual.numel() < rows * C or residual.shape[-1] != C)) \
             or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)):
         raise ValueError(f"{fn}: argument sizes disagree")
-    _check_device(fn, x)
+    if x.get_device() != _current_device():
+        _refuse_device(fn, x)
     st = (_lib or load()).moe_expert_matmul(
         x.data_ptr(), weights.data_ptr(), None if bias is None else bias.data_ptr(), expert_offsets.data_ptr(),
         rows, H, N, E, act, None if residual is None else residual.data_ptr(),
@@ -523,7 +523,8 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
         raise ValueError(f"{fn}: argument sizes disagree")
     if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
-    _check_device(fn, grad_out)
+    if grad_out.get_device() != _current_device():
+        _refuse_device(fn, grad_out)
     st = (_lib or load()).moe_expert_activation_backward(
         None if pre is None else pre.data_ptr(), grad_out.data_ptr(), expert_offsets.data_ptr(), rows, N, E, act,
         None if grad_pre is None else grad_pre.data_ptr(), None if grad_bias is None else grad_bias.data_ptr(),
@@ -556,7 +557,8 @@ def moe_expert_matmul_backward(grad_pre, x, weights, expert_offsets, grad_x=None
             or (grad_x is not None and (grad_x.numel() < rows * H or grad_x.shape[-1] != H)) \
             or (grad_weights is not None and grad_weights.shape != like.shape):
         raise ValueError(f"{fn}: argument sizes disagree")
-    _check_device(fn, grad_pre)
+    if grad_pre.get_device() != _current_device():
+        _refuse_device(fn, grad_pre)
     st = (_lib or load()).moe_expert_matmul_backward(
         grad_pre.data_ptr(), None if x is None else x.data_ptr(), None if weights is None else weights.data_ptr(),
         expert_offsets.data_ptr(), rows, H, N, E, None if grad_x is None else grad_x.data_ptr(),
@@ -671,7 +673,10 @@ def moe_route_grouped(logits, bias, topk_ids, topk_weights, expert_counts, route
     fn = "moe_route_grouped"
     T, E = logits.shape
     K = topk_ids.shape[1]
-    bf16, score = _logits_type(fn, logits), _scoring(fn, scoring)
+    bf16 = 0 if logits.dtype is _f32 else _logits_type(fn, logits)
+    score = MOE_SCORES.get(scoring)
+    if score is None:
+        score = _scoring(fn, scoring)
     if not (logits.is_cuda and logits.is_contiguous()
             and topk_ids.dtype is _i32 and topk_ids.is_cuda and topk_ids.is_contiguous()
             and topk_weights.dtype is _f32 and topk_weights.is_cuda and topk_weights.is_contiguous()
@@ -682,9 +687,10 @@ def moe_route_grouped(logits, bias, topk_ids, topk_weights, expert_counts, route
                     ("topk_weights", topk_weights, torch.float32),
                     ("expert_counts", expert_counts, torch.int32),
                     ("routed_tokens", routed_tokens, torch.int32), ("loss", loss, torch.float32)))
-    _check("bias", bias, torch.float32)
-    if bias is not None and bias.numel() != E:
-        raise ValueError(f"{fn}: bias has the wrong size")
+    if bias is not None:
+        _check("bias", bias, _f32)
+        if bias.numel() != E:
+            raise ValueError(f"{fn}: bias has the wrong size")
     if token_mask is not None:
         _check("token_mask", token_mask, torch.bool)
         if token_mask.numel() != T:
@@ -694,12 +700,14 @@ def moe_route_grouped(logits, bias, topk_ids, topk_weights, expert_counts, route
         raise ValueError(f"{fn}: output arrays have the wrong size")
     if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
-    _check_device(fn, logits)
+    if logits.get_device() != _current_device():
+        _refuse_device(fn, logits)
     st = (_lib or load()).moe_route_grouped(
-        logits.data_ptr(), bf16, T, E, K, score, _ptr(bias), groups, top_groups, group_top,
-        1 if renormalize else 0, scale, loss_coef, _ptr(token_mask), topk_ids.data_ptr(),
-        topk_weights.data_ptr(), expert_counts.data_ptr(), routed_tokens.data_ptr(), loss.data_ptr(),
-        _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+        logits.data_ptr(), bf16, T, E, K, score, None if bias is None else bias.data_ptr(), groups, top_groups,
+        group_top, 1 if renormalize else 0, scale, loss_coef, None if token_mask is None else token_mask.data_ptr(),
+        topk_ids.data_ptr(), topk_weights.data_ptr(), expert_counts.data_ptr(), routed_tokens.data_ptr(),
+        loss.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes,
         _current_stream() if stream is None else _stream(stream))
     if st:
         _raise(fn, st)
@@ -713,7 +721,10 @@ def moe_route_grouped_backward(logits, topk_ids, expert_counts, routed_tokens, g
     fn = "moe_route_grouped_backward"
     T, E = logits.shape
     K = topk_ids.shape[1]
-    bf16, score = _logits_type(fn, logits), _scoring(fn, scoring)
+    bf16 = 0 if logits.dtype is _f32 else _logits_type(fn, logits)
+    score = MOE_SCORES.get(scoring)
+    if score is None:
+        score = _scoring(fn, scoring)
     if not (logits.is_cuda and logits.is_contiguous()
             and grad_logits.dtype is logits.dtype and grad_logits.is_cuda and grad_logits.is_contiguous()
             and topk_ids.dtype is _i32 and topk_ids.is_cuda and topk_ids.is_contiguous()
@@ -723,18 +734,22 @@ def moe_route_grouped_backward(logits, topk_ids, expert_counts, routed_tokens, g
                     ("topk_ids", topk_ids, torch.int32),
                     ("expert_counts", expert_counts, torch.int32),
                     ("routed_tokens", routed_tokens, torch.int32)))
-    _check("grad_weights", grad_weights, torch.float32)
-    _check("grad_loss", grad_loss, torch.float32)
+    if grad_weights is not None:
+        _check("grad_weights", grad_weights, _f32)
+    if grad_loss is not None:
+        _check("grad_loss", grad_loss, _f32)
     if topk_ids.numel() != T * K or expert_counts.numel() < E or routed_tokens.numel() < 1 \
             or grad_logits.numel() != T * E \
             or (grad_weights is not None and grad_weights.numel() != T * K) \
             or (grad_loss is not None and grad_loss.numel() != 1):
         raise ValueError(f"{fn}: argument sizes disagree")
-    _check_device(fn, logits)
+    if logits.get_device() != _current_device():
+        _refuse_device(fn, logits)
     st = (_lib or load()).moe_route_grouped_backward(
         logits.data_ptr(), bf16, T, E, K, score, 1 if renormalize else 0, scale, loss_coef,
-        topk_ids.data_ptr(), expert_counts.data_ptr(), routed_tokens.data_ptr(), _ptr(grad_weights),
-        _ptr(grad_loss), grad_logits.data_ptr(), _current_stream() if stream is None else _stream(stream))
+        topk_ids.data_ptr(), expert_counts.data_ptr(), routed_tokens.data_ptr(),
+        None if grad_weights is None else grad_weights.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(),
+        grad_logits.data_ptr(), _current_stream() if stream is None else _stream(stream))
     if st:
         _raise(fn, st)
 

@@ -489,7 +489,7 @@ route_grouped_kernel(const L *__restrict__ logits, int T, int E, int any_k, cons
     pdl_wait();
     pdl_trigger();
     for (int e = threadIdx.x; e < PITCH; e += THREADS) bias[e] = r.bias && e < E ? r.bias[e] : 0.0f;
-    constexpr bool kAhead = NV <= 8;
+    constexpr bool kAhead = NV <= 4;                     // further a lane lacks the registers
     const int stride = gridDim.x * WARPS;
     int t = blockIdx.x * WARPS + warp;
     float ahead[NV];
