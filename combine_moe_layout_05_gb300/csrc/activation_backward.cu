@@ -12,6 +12,12 @@
 // order); a second kernel adds an expert's chunks up in order.  So a call's
 // results do not depend on timing, and the largest expert's rows are as many
 // chunks as they need.
+//
+// 131072 rows of 4096, gated, 128 experts: 420 us without the bias (6.4 TB/s), 438
+// with it, 10 of which are the second kernel.  4662 rows of 1032: 7.0 and 12.9 us,
+// starts and two rounds of loads; the second kernel and its launch are 6.
+// Two, three or four blocks a multiprocessor, with two or four rows in flight,
+// differ by 5 %.
 #include "activation.cuh"
 #include "expert_tiles.cuh"
 
@@ -180,7 +186,7 @@ int columns_of(int C)
 }
 
 // Rows a chunk: as many as still give every block one (4662 rows of 1032 columns,
-// 48 experts: XX us with 128 rows, XX with 32).
+// 48 experts, with the bias: 19.9 us with 128 rows, 12.9 with 32).
 int rows_a_chunk(int rows, int N)
 {
     int chunk = 128;

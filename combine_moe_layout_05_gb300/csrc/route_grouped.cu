@@ -15,6 +15,12 @@
 // and only the groups' values need the check.  What a rare path costs here is the
 // fetching of its instructions, and the call ends with its slowest block: a
 // choice in 64 bits of all that was open took 10 to 25 us of a call of 25.
+//
+// 16384 x 256 fp32, K = 8, bias, the best 4 of 8 groups: 28.5 us; without groups
+// and bias 24.3 (moe_route, with softmax: 19.0).  Issue slots bound it: 831
+// instructions a token (moe_route 478), of which the groups take 190, the scores
+// and keys 150, the picks 140; 32 warps a multiprocessor (24: 32.3 us, 16 in
+// larger blocks 30.9).  Some 8 us are the two launches.  One token: 4.7 us.
 #include "activation.cuh"
 #include "route_grouped.cuh"
 #include "route_totals.cuh"
