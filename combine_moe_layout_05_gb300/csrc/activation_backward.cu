@@ -155,25 +155,37 @@ activation_backward_kernel(const __nv_bfloat16 *pre, const __nv_bfloat16 *grad_o
     }
 }
 
-// Expert blockIdx.y's chunks in order, a thread a column.
-__global__ void __launch_bounds__(128)
+// Expert blockIdx.y's chunks: every kFinishLanes-th one by one thread, then the
+// threads of a column in order.
+constexpr int kFinishColumns = 64, kFinishLanes = 4;
+
+__global__ void __launch_bounds__(kFinishColumns * kFinishLanes)
 bias_finish_kernel(const int32_t *__restrict__ first_chunk, const float *__restrict__ partial, int N,
                    float *__restrict__ grad_bias)
 {
+    __shared__ float sums[kFinishLanes][kFinishColumns];
     pdl_wait();
     pdl_trigger();
-    const int n = blockIdx.x * 128 + threadIdx.x, e = blockIdx.y;
-    if (n >= N) return;
-    const int last = first_chunk[e + 1];
+    const int x = threadIdx.x % kFinishColumns, lane = threadIdx.x / kFinishColumns;
+    const int n = blockIdx.x * kFinishColumns + x, e = blockIdx.y, last = first_chunk[e + 1];
     float v = 0.0f;
-    for (int c0 = first_chunk[e]; c0 < last; c0 += 8) {
-        float p[8];
+    if (n < N)
+        for (int c0 = first_chunk[e] + lane; c0 < last; c0 += 8 * kFinishLanes) {
+            float p[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = c0 + j < last ? partial[(size_t)(c0 + j) * N + n] : 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                const int c = c0 + j * kFinishLanes;
+                p[j] = c < last ? partial[(size_t)c * N + n] : 0.0f;
+            }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v += p[j];
+            for (int j = 0; j < 8; ++j) v += p[j];
+        }
+    sums[lane][x] = v;
+    __syncthreads();
+    if (lane == 0 && n < N) {
+        for (int i = 1; i < kFinishLanes; ++i) v += sums[i][x];
+        grad_bias[(size_t)e * N + n] = v;
     }
-    grad_bias[(size_t)e * N + n] = v;
 }
 
 size_t table_bytes(int E) { return ((size_t)(E + 1) * 4 + 255) / 256 * 256; }
@@ -221,7 +233,8 @@ cudaError_t launch_activation_backward(const void *pre, const void *grad_out, co
                                      offsets, rows, N, E, activation, static_cast<__nv_bfloat16 *>(grad_pre), first, partial,
                                      most, columns, chunk);
     if (e != cudaSuccess || !grad_bias) return e;
-    return launch_pdl(bias_finish_kernel, dim3(ceil_div(N, 128), E), dim3(128), 0, stream, first, partial, N, grad_bias);
+    return launch_pdl(bias_finish_kernel, dim3(ceil_div(N, kFinishColumns), E), dim3(kFinishColumns * kFinishLanes), 0, stream,
+                      first, partial, N, grad_bias);
 }
 
 }  // namespace moe

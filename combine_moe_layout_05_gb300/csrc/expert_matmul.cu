@@ -10,45 +10,6 @@ template <bool G> using Mid = Shape<kForward, G, 2, 128, 8, 2>;
 template <bool G> using Narrow = Shape<kForward, G, 1, 32, 10, 1>;
 template <bool G> using Split = Shape<kForward, G, 1, 32, 9, 1, true>;
 
-// Clusters of 2, 4 and 8 splitting CTAs that the current device runs at a time,
-// looked up once for each device.
-template <bool G>
-cudaError_t split_clusters(int (&clusters)[3])
-{
-    using S = Split<G>;
-    constexpr int kMaxDevices = 64;
-    static std::mutex mu;
-    static int known[kMaxDevices][3];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    const std::lock_guard<std::mutex> lock(mu);
-    auto *const kernel = &expert_matmul_kernel<S>;
-    const size_t smem = S::bytes(MOE_MAX_EXPERTS);
-    for (int i = 0; i < 3; ++i) {
-        int &n = known[dev][i];
-        if (n == 0) {
-            e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
-            if (e != cudaSuccess) return e;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(2 << i);
-            cfg.blockDim = dim3(S::THREADS);
-            cfg.dynamicSmemBytes = smem;
-            cudaLaunchAttribute attr;
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = 2u << i;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-            if (e != cudaSuccess) return e;
-        }
-        clusters[i] = n;
-    }
-    return cudaSuccess;
-}
-
 template <bool G>
 cudaError_t launch(const void *x, const void *w, const int32_t *offsets, int rows, int H, int N, int E, const Store &st,
                    uint32_t *dev_error, cudaStream_t stream, long long wait_limit, int stall)
@@ -82,7 +43,7 @@ cudaError_t launch(const void *x, const void *w, const int32_t *offsets, int row
     const int steps = ceil_div(H, kStep);
     if (tiles * 2 <= sms && steps >= 64) {
         int clusters[3];
-        e = split_clusters<G>(clusters);
+        e = split_clusters<expert_matmul_kernel<Split<G>>>(Split<G>::THREADS, Split<G>::bytes(MOE_MAX_EXPERTS), clusters);
         if (e != cudaSuccess) return e;
         int parts = 1;
         for (int p = 2; p <= 8 && steps >= 8 * p; p *= 2)

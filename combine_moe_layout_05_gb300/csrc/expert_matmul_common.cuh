@@ -9,10 +9,11 @@
 // In each the instruction's M are 128 "channels" a CTA (256 a pair): output
 // channels, the hidden size, or (kWeights) the weights' rows; an expert with one
 // row still feeds 128 lanes.  Its N are a tile's "rows": packed rows, or (kWeights)
-// the hidden size, as many as are left, rounded up.  Operands lie in shared memory as the copy engine's 128-byte
-// swizzle leaves them, in the order that global memory has: along the
-// contraction (K-major) for x and the forward weights, across it (MN-major)
-// for the weights in kRows and for both operands in kWeights.
+// the hidden size, as many as are left, rounded up.  Operands lie in shared
+// memory as the copy engine's 128-byte swizzle leaves them, in the order that
+// global memory has: along the contraction (K-major) for x and the forward
+// weights, across it (MN-major) for the weights in kRows and for both operands in
+// kWeights.
 //
 // Warps of a CTA: one copies 64-wide steps of both operands into a ring; one
 // issues the matrix instructions (the pair's first CTA's); in a pair one tells

@@ -677,43 +677,6 @@ cudaError_t run(const void *x, const float *x_scales, const void *w, const float
                                static_cast<__nv_bfloat16 *>(out), dev_error, wait_limit, stall);
 }
 
-// Clusters of 2, 4 and 8 splitting CTAs that the current device runs at a time,
-// looked up once for each device.
-cudaError_t split_clusters(int (&clusters)[3])
-{
-    constexpr int kMaxDevices = 64;
-    static std::mutex mu;
-    static int known[kMaxDevices][3];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    const std::lock_guard<std::mutex> lock(mu);
-    auto *const kernel = &expert_matmul_int8_kernel<Split>;
-    const size_t smem = Split::bytes(MOE_MAX_EXPERTS);
-    for (int i = 0; i < 3; ++i) {
-        int &n = known[dev][i];
-        if (n == 0) {
-            e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
-            if (e != cudaSuccess) return e;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(2 << i);
-            cfg.blockDim = dim3(Split::THREADS);
-            cfg.dynamicSmemBytes = smem;
-            cudaLaunchAttribute attr;
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = 2u << i;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-            if (e != cudaSuccess) return e;
-        }
-        clusters[i] = n;
-    }
-    return cudaSuccess;
-}
-
 }  // namespace
 
 cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, const void *w,
@@ -736,7 +699,7 @@ cudaError_t launch_expert_matmul_int8(const void *x, const float *x_scales, cons
     const int steps = ceil_div(H, kStep);
     if (tiles * 2 <= sms && steps >= 16) {
         int clusters[3];
-        e = split_clusters(clusters);
+        e = split_clusters<expert_matmul_int8_kernel<Split>>(Split::THREADS, Split::bytes(MOE_MAX_EXPERTS), clusters);
         if (e != cudaSuccess) return e;
         int parts = 1;
         for (int p = 2; p <= 8 && steps >= 4 * p; p *= 2)

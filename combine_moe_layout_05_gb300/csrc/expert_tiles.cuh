@@ -1,6 +1,6 @@
 // expert_tiles.cuh -- how the grouped matrix products cut packed rows into
 // tiles: each expert's rows split evenly into tiles of at most S::NT rows, each
-// tile by kChannels * S::CG output channels; and the tensor maps' encoder.
+// tile by kChannels * S::CG output channels; and what their launches share.
 #pragma once
 
 #include <mutex>
@@ -101,6 +101,42 @@ template <typename S>
 int64_t most_tiles(int rows, int E)
 {
     return (int64_t)(rows < E ? rows : E) + rows / S::NT;
+}
+
+// Clusters of 2, 4 and 8 CTAs of KERNEL that the current device runs at a time,
+// looked up once for each device.
+template <auto *KERNEL>
+cudaError_t split_clusters(int threads, size_t smem, int (&clusters)[3])
+{
+    constexpr int kMaxDevices = 64;
+    static std::mutex mu;
+    static int known[kMaxDevices][3];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < 3; ++i) {
+        int &n = known[dev][i];
+        if (n == 0) {
+            e = allow_dynamic_smem(reinterpret_cast<const void *>(KERNEL), smem);
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 << i);
+            cfg.blockDim = dim3(threads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        clusters[i] = n;
+    }
+    return cudaSuccess;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
