@@ -3,8 +3,8 @@
 // u = 2 sqrt(2/pi) (z + 0.044715 z^3), since (1 + tanh v) / 2 = sigmoid(2 v).
 //
 // The sigmoid is one power of 2 and one reciprocal: a relative error of
-// (|u| + 6) 2^-24, far below the bf16 rounding of what is made of it.  Below
-// u = -87.3 it is 0, where the value itself is under 2^-126.
+// (1.3 |u| + 7) 2^-24, far below the bf16 rounding of what is made of it.  Below
+// u = -88 it is 0, where the value itself is under 2^-126.
 #pragma once
 
 #include "common.cuh"

@@ -7,7 +7,7 @@
 // by computed values, c = s + bias, where route.cu's goes by the logits
 // themselves: fp32 scores are off by a few units in the last place, and two
 // experts nearer than that could come out in the wrong order (of 16384 tokens
-// with 256 experts some 50 have such a pair).  So every choice is checked
+// with 256 experts some 15 have such a pair).  So every choice is checked
 // against a bound on its error, and where that fails the experts in question are
 // valued again: in sums of two floats (fixed_key), for they leave one token in
 // some 500 of these open again, which is then chosen in 64 bits after the loop
@@ -138,19 +138,21 @@ struct Room {
     float keys, groups;
 };
 
-// With u = 2^-24, scores of at most `top` and |c| <= top + largest: the power of
-// 2 is off by (|z| + 4) u of itself, z its argument's size (the product with
-// log2(e), and 2^-22 for the power).  That moves a logistic score by s (1 - s)
-// times as much, at most 1.3 u top where top is above 1/4 and 92 u top anywhere
-// (|z| <= 88); its sum adds u top and the reciprocal one ulp, 2 u top.  A softmax
-// score has (|z| + 4) u of its own, |z| top below 1, 7 + 4 from the sum's terms
-// (their mean |z| is below log 1024), 37 additions, and 4 ulp from the quotient:
-// below 64 u top.  The sum with the bias adds u (top + largest).  Two keys: twice
-// that; two groups' values: four times, and their own sums' roundings.  A tenth
-// is added for the products of errors.
+// With u = 2^-24, scores of at most `top` and |c| <= top + largest.  The power of
+// 2 is off by (1.22 |z| + 4) u of itself, z its argument's size (the product with
+// log2(e) and that number's rounding, and 2 ulp for the power).  That moves a
+// logistic score by s (1 - s) times as much: at most 1.3 u, and 112 u top where top
+// is small (|z| <= 88); its sum adds u top and the reciprocal one ulp, 2 u top.  A
+// softmax score, whose z is a rounded difference, has (2.22 |z| + 4) u of its own,
+// |z| top below 0.4; 20 from the sum's terms (their mean |z| is below log 1024),
+// 37 additions, 4 from the quotient and 1 from the product: below 70 u top.  The
+// sum with the bias adds u (top + largest).  Two keys: twice that; two groups'
+// values: four times, and their own sums' roundings.  A tenth is added for the
+// products of errors.
 __device__ __forceinline__ Room room_of(float top, bool softmax, float largest_bias)
 {
-    const float c = top + largest_bias, key = (softmax ? 64.0f : top > 0.25f ? 4.3f : 95.0f) * top + c;
+    const float c = top + largest_bias;
+    const float key = (softmax ? 70.0f * top : top > 0.25f ? 1.3f + 3.0f * top : 115.0f * top) + c;
     return {2.2f * kUnit * key, 4.4f * kUnit * (key + c)};
 }
 
@@ -178,7 +180,7 @@ __device__ __forceinline__ Two two_product(float a, float b)
 // follows, below 2^-10, in one.
 __device__ __forceinline__ Two two_exp(float a, float b, int &n)
 {
-    constexpr float kLn2 = 0.693145751953125f, kLn2Rest = 1.42860682030941723e-6f;       // 16 bits, and the rest
+    constexpr float kLn2 = 0.693145751953125f, kLn2Rest = 1.42860682030941723e-6f;       // 15 bits, and the rest
     constexpr float kSixth = 0.16666667163372040f, kSixthRest = -4.967053879e-9f;
     const float k = rintf(__fmul_rn(a, kLog2e));
     n = (int)k;
@@ -241,15 +243,16 @@ __device__ __noinline__ long long fixed_key(float x, float m, Two part, float b,
 }
 
 // The sum of a row's exp(x - m) as its reciprocal, for softmax with a bias
-// (without one it divides all alike): to 2^-31 of itself, in every lane.
+// (without one it divides all alike): added up as integers of 2^-50, to 2^-32 of
+// itself, in every lane.
 __device__ __noinline__ Two fixed_part(const float *row, int E, float m)
 {
     long long all = 0;
     for (int e = threadIdx.x & 31; e < E; e += 32)
-        if (row[e] > -INFINITY) all += fixed_key(row[e], m, {1.0f, 0.0f}, 0.0f, true);
+        if (row[e] > -INFINITY) all += fixed_key(row[e], m, {1024.0f, 0.0f}, 0.0f, true);
 #pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kFullMask, all, o);
-    constexpr float kOne = 1099511627776.0f;
+    constexpr float kOne = 1125899906842624.0f;      // 2^50
     const float h = __ll2float_rn(all);
     const Two part = two_reciprocal({h, __ll2float_rn(all - (long long)h)});
     return {part.h * kOne, part.l * kOne};

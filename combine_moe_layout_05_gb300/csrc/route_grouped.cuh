@@ -8,9 +8,9 @@ namespace moe {
 namespace {
 
 // The logistic function of x and of -x: one power of 2 of -|x|, one reciprocal.
-// Errors, with u = 2^-24: the product with log2(e) and its power |x| u + 4 u of
-// the power, the sum u, the reciprocal 2 u, the product u: at most (|x| + 8) u of
-// either value.  x = -inf: 0 and 1.
+// Errors, with u = 2^-24: the product with log2(e) 1.22 |x| u and its power 4 u of
+// the power, the sum u, the reciprocal 2 u, the product u: at most (1.22 |x| + 8) u
+// of either value.  x = -inf: 0 and 1.
 __device__ __forceinline__ float logistic(float x, float &rest)
 {
     const float e = exp2_approx(-fabsf(x) * kLog2e), r = rcp_approx(1.0f + e), q = e * r;

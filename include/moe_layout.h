@@ -468,8 +468,8 @@ MOE_API moe_status_t moe_route_backward(const void *logits, int32_t bf16, int32_
  *
  * The choice is that of exact arithmetic on the given logits and bias, as far as
  * 64 bits tell two values apart (equal ones go by index): where fp32 might order
- * two of them wrongly the token's values are computed again in 64 bits.  Scores,
- * weights and sums are fp32, the sums in an order that the sizes and the
+ * two of them wrongly they are computed again more finely.  Scores, weights and
+ * sums are fp32, the sums in an order that the sizes and the
  * alignment of logits fix.  A c that is NaN ranks below every number.  A NaN logit
  * of an open expert makes the loss NaN, and the weights in which its score takes
  * part; +inf is a score of 1 (sigmoid), or makes its token NaN (softmax).
