@@ -190,3 +190,40 @@ def test_second_derivatives_and_unfit_widths_are_refused():
     grad, = torch.autograd.grad(route_grouped(logits, 2)[1].square().sum(), logits, create_graph=True)
     with pytest.raises(RuntimeError):
         grad.sum().backward()
+
+
+def test_edits_of_what_the_gradient_needs_are_errors():
+    from combine_moe_layout_05_gb300.layer import expert_linear, route_grouped
+    g = torch.Generator(device="cuda").manual_seed(7)
+    o = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    x, w = leaf((4, 16), g, 1.0), leaf((1, 16, 16), g, 1.0)
+    rows = x * 1
+    out = expert_linear(rows, w, o, activation="silu")
+    rows.zero_()
+    with pytest.raises(RuntimeError):
+        out.float().sum().backward()
+    logits = torch.randn((4, 8), generator=g, device="cuda").requires_grad_()
+    ids, weights, counts, loss = route_grouped(logits, 2)
+    ids.fill_(0)
+    with pytest.raises(RuntimeError):
+        weights.sum().backward()
+
+
+def test_weights_gradients_of_two_batches_add_up():
+    """Autograd adds the second batch's gradients; each is one bf16 rounding off (2^-8), their sum another."""
+    from combine_moe_layout_05_gb300.layer import expert_linear
+    g = torch.Generator(device="cuda").manual_seed(8)
+    w = leaf((2, 32, 24), g, 1.0)
+    want = torch.zeros((2, 32, 24), dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for counts in ((30, 9), (0, 70)):
+        o = torch.tensor([0, counts[0], sum(counts)], dtype=torch.int32, device="cuda")
+        x, pull = leaf((sum(counts), 24), g, 1.0), torch.randn((sum(counts), 32), generator=g, device="cuda")
+        pull = pull.to(torch.bfloat16)
+        expert_linear(x, w, o).backward(pull)
+        for e in range(2):
+            r = slice(int(o[e]), int(o[e + 1]))
+            part = pull[r].double().t() @ x.detach()[r].double()
+            want[e] += part
+            size[e] += part.abs()
+    assert bool(((w.grad.double() - want).abs() <= 2.0 ** -8 * (size + want.abs()) * 1.01 + 1e-5).all())
