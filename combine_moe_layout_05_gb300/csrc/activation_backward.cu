@@ -13,8 +13,8 @@
 // results do not depend on timing, and the largest expert's rows are as many
 // chunks as they need.
 //
-// 131072 rows of 4096, gated, 128 experts: 420 us without the bias (6.4 TB/s), 438
-// with it, 10 of which are the second kernel.  4662 rows of 1032: 7.0 and 12.9 us,
+// 131072 rows of 4096, gated, 128 experts: 420 us without the bias (6.4 TB/s), 432
+// with it.  4662 rows of 1032: 7.0 and 12.9 us,
 // starts and two rounds of loads; the second kernel and its launch are 6.
 // Two, three or four blocks a multiprocessor, with two or four rows in flight,
 // differ by 5 %.

@@ -183,6 +183,8 @@ __device__ __forceinline__ void tile_add_3d(const CUtensorMap *map, int c, int r
                  :: "l"(map), "r"(c), "r"(r), "r"(z), "r"(src) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
