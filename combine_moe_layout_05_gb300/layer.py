@@ -235,7 +235,11 @@ class Experts:
 
     ``dev_error``, [9] int32 on the device, holds the last call's error words: the layout's
     (MOE_DEV_ERR_EXPERT_RANGE where an id is -1), then for each of the four products the forward's and
-    the backward's, whose MOE_DEV_ERR_TIMEOUT says that the output or the gradient is unspecified."""
+    the backward's, whose MOE_DEV_ERR_TIMEOUT says that the output or the gradient is unspecified.
+
+    A training step can be captured into a CUDA graph: after a warm-up on a side stream, with gradients
+    from torch.autograd.grad, and with no output of an eager call on the same leaves still alive, since
+    PyTorch cannot capture a backward pass that meets such a call's stream."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, gate_up_bias: torch.Tensor | None = None,
                  down_bias: torch.Tensor | None = None, shared: tuple[torch.Tensor, torch.Tensor] | None = None,

@@ -227,3 +227,39 @@ def test_weights_gradients_of_two_batches_add_up():
             want[e] += part
             size[e] += part.abs()
     assert bool(((w.grad.double() - want).abs() <= 2.0 ** -8 * (size + want.abs()) * 1.01 + 1e-5).all())
+
+
+def test_captured_training_step_replays():
+    """Forward and backward of the router, the experts and the shared expert in one graph, replayed on
+    new rows, against the same step run eagerly: the layer's sums have one order, so the same bits."""
+    from combine_moe_layout_05_gb300.layer import Experts, route_grouped
+    g = torch.Generator(device="cuda").manual_seed(9)
+    T, H, I, E, K = 50, 128, 72, 8, 2
+    leaves = [leaf(s, g, s[-1] ** -0.5) for s in ((E, 2 * I, H), (E, H, I), (2 * 40, H), (H, 40))]
+    leaves.append(leaf((E, 2 * I), g, 0.1, torch.float32))
+    router = leaf((E, H), g, H ** -0.5, torch.float32)
+    layer = Experts(leaves[0], leaves[1], leaves[4], shared=(leaves[2], leaves[3]))
+    static, pull = leaf((T, H), g, 1.0), torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+
+    def step():
+        ids, weights, _, loss = route_grouped(static.float() @ router.t(), K, groups=2, top_groups=1)
+        out = layer(static, ids, weights)
+        grads = torch.autograd.grad((out.float() * pull).sum() + loss, leaves + [router, static])
+        return [out.detach(), loss.detach()] + list(grads)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (1, 2):
+        rows = torch.randn((T, H), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+        with torch.no_grad():
+            static.copy_(rows)
+        graph.replay()
+        # copies: the eager step below is another call of the same layer
+        held = [t.clone() for t in got]
+        for a, b in zip(held, step()):
+            assert torch.equal(a, b)
