@@ -501,10 +501,11 @@ def moe_expert_activation_backward_workspace_bytes(rows: int, N: int, E: int) ->
 
 
 def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, activation: str,
-                                   grad_bias=None, workspace=None, stream=None) -> None:
+                                   grad_bias=None, workspace=None, stream=None, E: int | None = None) -> None:
     """Gradient at moe_expert_matmul's values before the activation, and its sum
     over each expert's rows; grad_pre or grad_bias may be None (not wanted), and
-    pre with activation "none"."""
+    pre with activation "none".  E, the number of experts, is grad_bias's; without
+    that it has to be given where expert_offsets is longer than E + 1."""
     fn = "moe_expert_activation_backward"
     act = MOE_ACTIVATIONS.get(activation)
     if act is None:
@@ -516,7 +517,8 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
                     ("expert_offsets", expert_offsets, torch.int32)))
     rows, C = grad_out.shape
     N = 2 * C if act == 3 else C
-    E = expert_offsets.numel() - 1 if grad_bias is None else grad_bias.shape[0]
+    if E is None:
+        E = expert_offsets.numel() - 1 if grad_bias is None else grad_bias.shape[0]
     if expert_offsets.numel() < E + 1 or (grad_bias is not None and grad_bias.numel() != E * N) \
             or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)) \
             or (grad_pre is not None and (grad_pre.numel() < rows * N or grad_pre.shape[-1] != N)):

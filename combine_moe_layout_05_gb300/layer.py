@@ -156,7 +156,7 @@ class _ExpertLinear(torch.autograd.Function):
                 grad_pre = torch.empty_like(pre)
             if pre is not None or need_bias:
                 moe.moe_expert_activation_backward(pre, grad_out, offsets, None if pre is None else grad_pre,
-                                                   ctx.activation, grad_bias, workspace)
+                                                   ctx.activation, grad_bias, workspace, E=E)
             if need_x or need_w:
                 grad_x = torch.empty_like(x) if need_x else None
                 grad_w = torch.empty_like(weights) if need_w else None

@@ -1,0 +1,113 @@
+"""expert_linear and Experts on the CPU, with stand-ins for the library's calls that
+compute what the calls do by PyTorch in 32 bits, from the same arguments and with
+the same readings of them.  Gradients of two calls that differ only in what the
+calls do not use are equal."""
+import pytest
+import torch
+
+from combine_moe_layout_05_gb300 import _binding, layer
+
+bf16 = torch.bfloat16
+
+
+def _activate(z, activation):
+    if activation == "swiglu":
+        a, u = z.chunk(2, 1)
+        return a * torch.sigmoid(a) * u
+    if activation == "gelu":
+        return torch.nn.functional.gelu(z, approximate="tanh")
+    return z * torch.sigmoid(z) if activation == "silu" else z
+
+
+def _ranges(offsets, E, rows):
+    o = [max(0, min(rows, v)) for v in offsets.tolist()[:E + 1]]
+    return [(e, slice(o[e], o[e + 1])) for e in range(E) if o[e + 1] > o[e]]
+
+
+class _Products:
+    """Stand-ins for the bf16 experts' calls; `timeouts` names the error words (of the calls in
+    order: forward products, then backward ones) that are set."""
+
+    def __init__(self):
+        self.words = []
+
+    def matmul(self, x, weights, expert_offsets, out, bias=None, activation="none", residual=None, pre=None, dev_error=None,
+               stream=None):
+        out.fill_(-77.0)
+        for e, r in _ranges(expert_offsets, weights.shape[0], x.shape[0]):
+            z = x[r].float() @ weights[e].float().t() + (0 if bias is None else bias.view(weights.shape[:2])[e])
+            if pre is not None:
+                pre[r] = z.to(bf16)
+            y = _activate(z, activation)
+            out[r] = (y if residual is None else y + residual[r].float()).to(bf16)
+        if dev_error is not None:
+            dev_error.fill_(0)
+            self.words.append(dev_error)
+
+    def activation_backward(self, pre, grad_out, expert_offsets, grad_pre, activation, grad_bias=None, workspace=None,
+                            stream=None, E=None):
+        if E is None:
+            E = expert_offsets.numel() - 1 if grad_bias is None else grad_bias.shape[0]
+        o = expert_offsets.tolist()
+        # without the bias the calls' own reading: one run of rows, from the first expert's to the last one's
+        parts = _ranges(expert_offsets, E, grad_out.shape[0]) if grad_bias is not None else [(0, slice(o[0], max(o[0], o[E])))]
+        if grad_pre is not None:
+            grad_pre.fill_(-77.0)
+        if grad_bias is not None:
+            grad_bias.zero_()
+        for e, r in parts:
+            z = grad_out[r].float() if pre is None else pre[r].float()
+            with torch.enable_grad():
+                z.requires_grad_()
+                g, = torch.autograd.grad(_activate(z, activation), z, grad_out[r].float())
+            if grad_pre is not None:
+                grad_pre[r] = g.to(bf16)
+            if grad_bias is not None:
+                grad_bias[e] = g.sum(0)
+
+    def matmul_backward(self, grad_pre, x, weights, expert_offsets, grad_x=None, grad_weights=None, accumulate=False,
+                        dev_error=None, stream=None):
+        if grad_x is not None:
+            grad_x.fill_(-77.0)
+        if grad_weights is not None:
+            grad_weights.zero_()
+        for e, r in _ranges(expert_offsets, weights.shape[0], x.shape[0]):
+            if grad_x is not None:
+                grad_x[r] = (grad_pre[r].float() @ weights[e].float()).to(bf16)
+            if grad_weights is not None:
+                grad_weights[e] = (grad_pre[r].float().t() @ x[r].float()).to(bf16)
+        if dev_error is not None:
+            dev_error.fill_(0)
+            self.words.append(dev_error)
+
+
+@pytest.fixture
+def products(monkeypatch):
+    p = _Products()
+    monkeypatch.setattr(_binding, "moe_expert_matmul", p.matmul)
+    monkeypatch.setattr(_binding, "moe_expert_activation_backward", p.activation_backward)
+    monkeypatch.setattr(_binding, "moe_expert_matmul_backward", p.matmul_backward)
+    monkeypatch.setattr(_binding, "moe_expert_activation_backward_workspace_bytes", lambda rows, N, E: 256)
+    return p
+
+
+def _leaf(shape, seed, dtype=bf16):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dtype).requires_grad_()
+
+
+@pytest.mark.parametrize("activation", ["none", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("tail", [[0, 0, 0], [9, 9], [4], [1 << 30]])
+def test_offsets_longer_than_the_experts(products, activation, with_bias, tail):
+    """What follows the first E + 1 offsets is not read, forward or backward."""
+    counts, H, N = [4, 0, 5], 8, 16
+    exact = torch.tensor([0, 4, 4, 9], dtype=torch.int32)
+
+    def step(offsets):
+        x, w = _leaf((9, H), 1), _leaf((len(counts), N, H), 2)
+        b = _leaf((len(counts), N), 3, torch.float32) if with_bias else None
+        out = layer.expert_linear(x, w, offsets, b, activation)
+        out.backward(torch.ones_like(out))
+        return [out.detach(), x.grad, w.grad] + ([b.grad] if with_bias else [])
+    for a, c in zip(step(exact), step(torch.cat([exact, torch.tensor(tail, dtype=torch.int32)]))):
+        assert torch.equal(a, c)

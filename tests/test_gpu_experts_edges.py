@@ -1,0 +1,66 @@
+"""The bf16 experts' calls and expert_linear where their arguments are unusual:
+offsets longer than the experts.  Calls that differ only in what is not used have
+to give the same bits."""
+import pytest
+import torch
+
+import combine_moe_layout_05_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from combine_moe_layout_05_gb300 import build
+    build.build()
+    moe.load()
+
+
+def normal(shape, seed, std=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(shape, dtype=dtype, device="cuda").normal_(0.0, std, generator=g)
+
+
+def longer(offsets, tail):
+    return torch.cat([offsets, torch.tensor(tail, dtype=torch.int32, device="cuda")])
+
+
+TAILS = [[0, 0, 0], [70, 70], [4], [0] * 1200]
+
+
+@pytest.mark.parametrize("activation", ["none", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("tail", TAILS)
+def test_offsets_longer_than_the_experts(activation, with_bias, tail):
+    from combine_moe_layout_05_gb300.layer import expert_linear
+    exact = torch.tensor([0, 40, 40, 70], dtype=torch.int32, device="cuda")
+
+    def step(offsets):
+        x, w = normal((70, 72), 1).requires_grad_(), normal((3, 96, 72), 2, 0.1).requires_grad_()
+        b = normal((3, 96), 3, dtype=torch.float32).requires_grad_() if with_bias else None
+        out = expert_linear(x, w, offsets, b, activation)
+        out.backward(normal(out.shape, 4))
+        return [out.detach(), x.grad, w.grad] + ([b.grad] if with_bias else [])
+    for a, c in zip(step(exact), step(longer(exact, tail))):
+        assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("activation", ["none", "swiglu"])
+@pytest.mark.parametrize("tail", TAILS)
+def test_activation_gradient_of_given_experts(activation, tail):
+    exact = torch.tensor([2, 40, 40, 68], dtype=torch.int32, device="cuda")
+    pre, dy = normal((70, 64), 1), normal((70, 32 if activation == "swiglu" else 64), 2)
+
+    def call(offsets, **kw):
+        out = torch.full_like(pre, -77.0)
+        moe.moe_expert_activation_backward(pre, dy, offsets, out, activation, **kw)
+        return out
+    want = call(exact)
+    assert bool((want[:2] == -77.0).all()) and bool((want[68:] == -77.0).all()) and not bool((want[2:68] == -77.0).all(1).any())
+    assert torch.equal(want, call(longer(exact, tail), E=3)) and torch.equal(want, call(exact, E=3))
+    with pytest.raises(ValueError):
+        call(exact, E=4)
+    with pytest.raises(ValueError):                      # the bias gradient's experts are another number
+        call(exact, E=2, grad_bias=torch.empty((3, 64), device="cuda"))
