@@ -25,10 +25,12 @@ __device__ __forceinline__ float gelu(float z) { return z * sigmoid_approx(gelu_
 // d/dz of z * sigmoid(u(z)) = s + z s (1 - s) u'(z).
 __device__ __forceinline__ float silu_slope(float z, float s) { return fmaf(z * s, 1.0f - s, s); }
 
+// From |z| = 11 on s is 0 or 1, and so is the slope; z^2 stays finite, since 0
+// times an infinity would be NaN (from 1.8e19 on).
 __device__ __forceinline__ float gelu_slope(float z)
 {
     const float s = sigmoid_approx(gelu_argument(z));
-    return fmaf(z * s * (1.0f - s), fmaf(3.0f * kGelu * kGeluCube, z * z, kGelu), s);
+    return fmaf(z * s * (1.0f - s), fmaf(3.0f * kGelu * kGeluCube, fminf(z * z, 1e30f), kGelu), s);
 }
 
 }  // namespace

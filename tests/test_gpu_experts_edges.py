@@ -1,6 +1,6 @@
 """The bf16 experts' calls and expert_linear where their arguments are unusual:
-offsets longer than the experts.  Calls that differ only in what is not used have
-to give the same bits."""
+offsets longer than the experts, values near the type's largest.  Calls that differ
+only in what is not used have to give the same bits."""
 import pytest
 import torch
 
@@ -64,3 +64,17 @@ def test_activation_gradient_of_given_experts(activation, tail):
         call(exact, E=4)
     with pytest.raises(ValueError):                      # the bias gradient's experts are another number
         call(exact, E=2, grad_bias=torch.empty((3, 64), device="cuda"))
+
+
+@pytest.mark.parametrize("activation", ["silu", "gelu", "swiglu"])
+def test_slopes_at_the_largest_values(activation):
+    """Beyond |z| = 100 the slope is 1 or 0 to more than fp32's digits: SiLU's rest is below 1e-41, GELU's 0."""
+    far = torch.tensor([100.0, 1e4, 1e10, 1.5e19, 2e19, 1e25, 1e38, 3.3895e38, 0.0], device="cuda")
+    z = torch.cat([far, -far]).to(torch.bfloat16).repeat(8, 1).t().contiguous()        # [18, 8]
+    rows, dy = z.shape[0], normal(z.shape, 1)
+    pre = z if activation != "swiglu" else torch.cat([z, torch.full_like(z, 2.0)], 1)
+    o, out = torch.tensor([0, rows], dtype=torch.int32, device="cuda"), torch.empty_like(pre)
+    moe.moe_expert_activation_backward(pre, dy, o, out, activation)
+    slope = torch.where(z > 0, 1.0, 0.0) + torch.where(z == 0, 0.5, 0.0)
+    want = dy.double() * slope.double() * (2 if activation == "swiglu" else 1)
+    assert bool(((out[:, :8].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-37).all())
