@@ -675,19 +675,14 @@ expert_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
 bool tensor_map(CUtensorMap *map, const void *p, int rank, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box, bool f32 = false)
 {
-    const EncodeFn fn = encode_fn();
-    if (!fn) return false;
     cuuint64_t d[4], s[3];
-    cuuint32_t b[4], ones[4];
+    cuuint32_t b[4];
     for (int i = 0; i < rank; ++i) {
         d[i] = dims[i];
         b[i] = box[i];
-        ones[i] = 1;
         if (i > 0) s[i - 1] = strides[i - 1] * (f32 ? 4 : 2);
     }
-    return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(p), d, s, b, ones,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, p, d, s, b);
 }
 
 // [rows, width] in boxes of 64 by `box` rows.

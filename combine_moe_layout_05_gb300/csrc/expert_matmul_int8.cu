@@ -647,13 +647,9 @@ expert_matmul_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __gri
 // [rows, H] bytes, in boxes of kStep bytes by `box` rows, 128-byte swizzle.
 bool byte_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t H, uint32_t box)
 {
-    const EncodeFn fn = encode_fn();
-    if (!fn) return false;
     const cuuint64_t dims[2] = {H, rows}, strides[1] = {H};
-    const cuuint32_t boxes[2] = {kStep, box}, ones[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, boxes, ones,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t boxes[2] = {kStep, box};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, strides, boxes);
 }
 
 template <typename S>

@@ -157,5 +157,24 @@ EncodeFn encode_fn()
     return fn;
 }
 
+// A tensor map of boxes of 128-byte lines, swizzled, zeros outside.  Unlike a launch
+// the driver's call does not make the device's context the calling thread's, and
+// fails in a thread that has none yet (autograd's, whose first work is a gradient
+// here): cudaSetDevice does, and the call is made again.
+bool encode_tiled(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *p, const cuuint64_t *dims,
+                  const cuuint64_t *strides, const cuuint32_t *box)
+{
+    static const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    auto encode = [&] {
+        return fn(map, type, rank, const_cast<void *>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (encode()) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
+}
+
 }  // namespace
 }  // namespace moe
