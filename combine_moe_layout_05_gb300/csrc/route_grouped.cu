@@ -26,6 +26,7 @@
 #include "route_totals.cuh"
 
 #include <cfloat>
+#include <limits>
 
 namespace moe {
 namespace {
@@ -93,11 +94,15 @@ __device__ __forceinline__ void insert(long long v, float x, long long &a, float
     }
 }
 
-// A group's value from its largest two (-inf: no open expert).
+// A group's value from its largest two (-inf: no open expert).  NaN keys hold the
+// type's lowest value, and so does a value with one in it: behind every number's,
+// before a group without an open expert.  A sum past the type's range is cut there.
 template <typename T>
 __device__ __forceinline__ T group_value(T a, T b, int group_top)
 {
-    return group_top == 2 && b > -INFINITY ? a + b : a;
+    constexpr T kLast = std::numeric_limits<T>::lowest();
+    if (group_top != 2 || !(b > -INFINITY)) return a;
+    return b > kLast ? max(min(a + b, -kLast), kLast) : b;
 }
 
 // A lane's NV values to and from a row of 32 NV in shared memory.
@@ -221,11 +226,12 @@ __device__ __forceinline__ long long fixed40(Two a)
 // |x| (softmax: m - x) is below 80 and |b| below 2^16: the logistic function of x,
 // or exp(x - m) times `part`, plus b.
 constexpr long long kFixedRoom = 1 << 10;            // keys nearer than this, and sums of two, are left open
+constexpr long long kNanKey = -(1ll << 60);          // below every number's
 constexpr long long kNoKey = -(1ll << 62);           // below every key and sum of two
 
 __device__ __noinline__ long long fixed_key(float x, float m, Two part, float b, bool softmax)
 {
-    if (x != x) return -(1ll << 60);                 // below every number's
+    if (x != x) return kNanKey;
     const Two z = softmax ? two_sum(x, -m) : Two{-x, 0.0f};
     int n;
     Two s = two_exp(z.h, z.l, n);
@@ -293,7 +299,7 @@ __device__ __noinline__ bool careful_groups(const float *keys, const float *row,
         insert(u2, ux2, u, ux, v, vx);
         insert(v2, vx2, u, ux, v, vx);
     }
-    if (r.group_top == 2 && v > kNoKey) u += v;
+    if (r.group_top == 2 && v > kNoKey) u = v > kNanKey ? u + v : v;
     else vx = 0.0f;
     u = __shfl_sync(kFullMask, u, lane * group_lanes & 31);      // lane g has group g's
     ux = __shfl_sync(kFullMask, ux, lane * group_lanes & 31);
@@ -306,9 +312,9 @@ __device__ __noinline__ bool careful_groups(const float *keys, const float *row,
         const long long o = __shfl_sync(kFullMask, u, h);
         const float ox = __shfl_sync(kFullMask, ux, h), oy = __shfl_sync(kFullMask, vx, h);
         before += o > u || (o == u && h < lane);
-        // equal by the same logits, or only nearer than the errors
+        // equal by the same logits or by a NaN, or only nearer than the errors
         open |= (close >> lane & 1) && h != lane && o - u <= kFixedRoom && u - o <= kFixedRoom &&
-                !(by_logits && ox == ux && oy == vx);
+                !(by_logits && ox == ux && oy == vx) && o != kNanKey;
     }
     const int places = __popc(kept & close);
     kept = (kept & ~close) | __ballot_sync(kFullMask, (close >> lane & 1) && before < places);
@@ -362,7 +368,7 @@ template <typename L>
 __device__ __noinline__ Settled settle(const L *logits, int E, int K, const Rules r, const float *bias, float largest,
                                        bool by_logits, float *keys, float *row)
 {
-    constexpr double kNan = -(double)FLT_MAX;
+    constexpr double kNan = std::numeric_limits<double>::lowest();
     const int lane = threadIdx.x & 31, size = E / r.groups;
     const bool limited = r.top_groups < r.groups;
     float m = -INFINITY;
@@ -394,7 +400,7 @@ __device__ __noinline__ Settled settle(const L *logits, int E, int K, const Rule
     const Room room = room_of(r.softmax ? inv : fminf(fmaxf(warp_max(top) + largest, 0.0f), 1.0f), r.softmax, largest);
     auto exact = [&](int e) {
         const double x = row[e], c = (r.softmax ? exp(x - (double)m) / sum : 1.0 / (1.0 + exp(-x))) + (double)bias[e];
-        return c >= kNan ? c : kNan;
+        return c > -INFINITY ? c : kNan;
     };
     __syncwarp();
     unsigned kept = kFullMask;
@@ -452,7 +458,7 @@ __device__ __noinline__ Settled settle(const L *logits, int E, int K, const Rule
         n += __popc(all);
         __syncwarp();
     }
-    auto exact_key = [&](int e) { return by_logits ? (double)rankable(row[e]) : exact(e); };
+    auto exact_key = [&](int e) { return !by_logits ? exact(e) : row[e] == row[e] ? (double)row[e] : kNan; };
     int mine = -1;                                   // what lane k is given, candidate by candidate
     for (int a0 = 0; a0 < n; a0 += 32) {
         const int i = a0 + lane, e = i < n ? list[i] : -1;

@@ -470,7 +470,10 @@ MOE_API moe_status_t moe_route_backward(const void *logits, int32_t bf16, int32_
  * 64 bits tell two values apart (equal ones go by index): where fp32 might order
  * two of them wrongly they are computed again more finely.  Scores, weights and
  * sums are fp32, the sums in an order that the sizes and the
- * alignment of logits fix.  A c that is NaN ranks below every number.  A NaN logit
+ * alignment of logits fix.  A c that is NaN ranks below every number, and so does
+ * a group's value with a NaN in it, before a group without an open expert; such
+ * ones are equal.  Where the bias is the same for all, experts go by their logits,
+ * NaN behind the numbers (fp32's lowest value ranks with it).  A NaN logit
  * of an open expert makes the loss NaN, and the weights in which its score takes
  * part; +inf is a score of 1 (sigmoid), or makes its token NaN (softmax).
  *
