@@ -378,7 +378,7 @@ def moe_combine_fp8(expert_out, expert_scales, topk_weights, dst_row, out,
 
 # The calls below test their tensors in place: a function call for each would
 # cost as much as the tests, and a small call waits for its host side.
-_bf16, _f32, _i32, _i8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
+_bf16, _f32, _i32, _i8, _bool = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.bool
 
 
 def _check_all(pairs) -> None:
@@ -434,17 +434,30 @@ def moe_expert_matmul_int8(x, x_scales, weights, w_scales, expert_offsets, out,
         _raise("moe_expert_matmul_int8", st)
 
 
-def _fits(t, dtype) -> bool:
-    return t is None or (t.dtype is dtype and t.is_cuda and t.is_contiguous())
+def _fits(t, dtype, dev: int) -> bool:
+    return t is None or (t.dtype is dtype and t.get_device() == dev and t.is_contiguous())
 
 
 _current_device = torch.cuda.current_device if _get_device is None else _get_device
 
 
-def _refuse_device(fn: str, t) -> None:
+def _refuse_other_devices(fn: str, tensors) -> None:
     """A launch goes to the current device: memory of another one is refused."""
-    if t.is_cuda:
-        raise ValueError(f"{fn}: the tensors are on device {t.get_device()}, the current one is {_current_device()}")
+    for name, t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != _current_device():
+            raise ValueError(f"{fn}: {name} is on device {t.get_device()}, the current one is {_current_device()}")
+
+
+def _check_here(fn: str, tensors) -> None:
+    """The error of the first (name, tensor, dtype) that does not fit or is on another device."""
+    _check_all(tensors)
+    _refuse_other_devices(fn, [t[:2] for t in tensors])
+
+
+def _check_workspace(fn: str, workspace) -> None:
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
+    _refuse_other_devices(fn, (("workspace", workspace),))
 
 
 MOE_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
@@ -466,15 +479,16 @@ def moe_expert_matmul(x, weights, expert_offsets, out, bias=None, activation: st
     act = MOE_ACTIVATIONS.get(activation)
     if act is None:
         act = _activation(fn, activation)
-    if not (x.dtype is _bf16 and x.is_cuda and x.is_contiguous()
-            and weights.dtype is _bf16 and weights.is_cuda and weights.is_contiguous()
-            and expert_offsets.dtype is _i32 and expert_offsets.is_cuda and expert_offsets.is_contiguous()
-            and out.dtype is _bf16 and out.is_cuda and out.is_contiguous() and _fits(bias, _f32)
-            and _fits(residual, _bf16) and _fits(pre, _bf16) and _fits(dev_error, _i32)):
-        _check_all((("x", x, torch.bfloat16), ("weights", weights, torch.bfloat16),
-                    ("expert_offsets", expert_offsets, torch.int32), ("out", out, torch.bfloat16),
-                    ("bias", bias, torch.float32), ("residual", residual, torch.bfloat16),
-                    ("pre", pre, torch.bfloat16), ("dev_error", dev_error, torch.int32)))
+    dev = x.get_device()
+    if not (x.dtype is _bf16 and dev >= 0 and dev == _current_device() and x.is_contiguous()
+            and weights.dtype is _bf16 and weights.get_device() == dev and weights.is_contiguous()
+            and expert_offsets.dtype is _i32 and expert_offsets.get_device() == dev and expert_offsets.is_contiguous()
+            and out.dtype is _bf16 and out.get_device() == dev and out.is_contiguous() and _fits(bias, _f32, dev)
+            and _fits(residual, _bf16, dev) and _fits(pre, _bf16, dev) and _fits(dev_error, _i32, dev)):
+        _check_here(fn, (("x", x, torch.bfloat16), ("weights", weights, torch.bfloat16),
+                         ("expert_offsets", expert_offsets, torch.int32), ("out", out, torch.bfloat16),
+                         ("bias", bias, torch.float32), ("residual", residual, torch.bfloat16),
+                         ("pre", pre, torch.bfloat16), ("dev_error", dev_error, torch.int32)))
     if weights.dim() != 3 or weights.shape[2] != H:
         raise ValueError(f"{fn}: argument sizes disagree")
     E, N, _ = weights.shape
@@ -484,8 +498,6 @@ def moe_expert_matmul(x, weights, expert_offsets, out, bias=None, activation: st
             or (residual is not None and (residual.numel() < rows * C or residual.shape[-1] != C)) \
             or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)):
         raise ValueError(f"{fn}: argument sizes disagree")
-    if x.get_device() != _current_device():
-        _refuse_device(fn, x)
     st = (_lib or load()).moe_expert_matmul(
         x.data_ptr(), weights.data_ptr(), None if bias is None else bias.data_ptr(), expert_offsets.data_ptr(),
         rows, H, N, E, act, None if residual is None else residual.data_ptr(),
@@ -510,11 +522,12 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
     act = MOE_ACTIVATIONS.get(activation)
     if act is None:
         act = _activation(fn, activation)
-    if not (_fits(pre, _bf16) and _fits(grad_out, _bf16) and _fits(grad_pre, _bf16)
-            and _fits(grad_bias, _f32) and _fits(expert_offsets, _i32)):
-        _check_all((("pre", pre, torch.bfloat16), ("grad_out", grad_out, torch.bfloat16),
-                    ("grad_pre", grad_pre, torch.bfloat16), ("grad_bias", grad_bias, torch.float32),
-                    ("expert_offsets", expert_offsets, torch.int32)))
+    dev = grad_out.get_device()
+    if not (dev >= 0 and dev == _current_device() and _fits(pre, _bf16, dev) and _fits(grad_out, _bf16, dev)
+            and _fits(grad_pre, _bf16, dev) and _fits(grad_bias, _f32, dev) and _fits(expert_offsets, _i32, dev)):
+        _check_here(fn, (("pre", pre, torch.bfloat16), ("grad_out", grad_out, torch.bfloat16),
+                         ("grad_pre", grad_pre, torch.bfloat16), ("grad_bias", grad_bias, torch.float32),
+                         ("expert_offsets", expert_offsets, torch.int32)))
     rows, C = grad_out.shape
     N = 2 * C if act == 3 else C
     if E is None:
@@ -523,10 +536,8 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
             or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)) \
             or (grad_pre is not None and (grad_pre.numel() < rows * N or grad_pre.shape[-1] != N)):
         raise ValueError(f"{fn}: argument sizes disagree")
-    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
-    if grad_out.get_device() != _current_device():
-        _refuse_device(fn, grad_out)
+    if workspace is not None:
+        _check_workspace(fn, workspace)
     st = (_lib or load()).moe_expert_activation_backward(
         None if pre is None else pre.data_ptr(), grad_out.data_ptr(), expert_offsets.data_ptr(), rows, N, E, act,
         None if grad_pre is None else grad_pre.data_ptr(), None if grad_bias is None else grad_bias.data_ptr(),
@@ -543,12 +554,15 @@ def moe_expert_matmul_backward(grad_pre, x, weights, expert_offsets, grad_x=None
     None (not wanted)."""
     fn = "moe_expert_matmul_backward"
     f32 = grad_weights is not None and grad_weights.dtype is _f32
-    if not (_fits(grad_pre, _bf16) and _fits(x, _bf16) and _fits(weights, _bf16) and _fits(grad_x, _bf16)
-            and _fits(grad_weights, _f32 if f32 else _bf16) and _fits(expert_offsets, _i32) and _fits(dev_error, _i32)):
-        _check_all((("grad_pre", grad_pre, torch.bfloat16), ("x", x, torch.bfloat16),
-                    ("weights", weights, torch.bfloat16), ("grad_x", grad_x, torch.bfloat16),
-                    ("grad_weights", grad_weights, torch.float32 if f32 else torch.bfloat16),
-                    ("expert_offsets", expert_offsets, torch.int32), ("dev_error", dev_error, torch.int32)))
+    dev = grad_pre.get_device()
+    if not (dev >= 0 and dev == _current_device() and _fits(grad_pre, _bf16, dev) and _fits(x, _bf16, dev)
+            and _fits(weights, _bf16, dev) and _fits(grad_x, _bf16, dev)
+            and _fits(grad_weights, _f32 if f32 else _bf16, dev) and _fits(expert_offsets, _i32, dev)
+            and _fits(dev_error, _i32, dev)):
+        _check_here(fn, (("grad_pre", grad_pre, torch.bfloat16), ("x", x, torch.bfloat16),
+                         ("weights", weights, torch.bfloat16), ("grad_x", grad_x, torch.bfloat16),
+                         ("grad_weights", grad_weights, torch.float32 if f32 else torch.bfloat16),
+                         ("expert_offsets", expert_offsets, torch.int32), ("dev_error", dev_error, torch.int32)))
     rows, N = grad_pre.shape
     like = grad_weights if weights is None else weights
     if like is None or like.dim() != 3 or like.shape[1] != N:
@@ -559,8 +573,6 @@ def moe_expert_matmul_backward(grad_pre, x, weights, expert_offsets, grad_x=None
             or (grad_x is not None and (grad_x.numel() < rows * H or grad_x.shape[-1] != H)) \
             or (grad_weights is not None and grad_weights.shape != like.shape):
         raise ValueError(f"{fn}: argument sizes disagree")
-    if grad_pre.get_device() != _current_device():
-        _refuse_device(fn, grad_pre)
     st = (_lib or load()).moe_expert_matmul_backward(
         grad_pre.data_ptr(), None if x is None else x.data_ptr(), None if weights is None else weights.data_ptr(),
         expert_offsets.data_ptr(), rows, H, N, E, None if grad_x is None else grad_x.data_ptr(),
@@ -679,31 +691,28 @@ def moe_route_grouped(logits, bias, topk_ids, topk_weights, expert_counts, route
     score = MOE_SCORES.get(scoring)
     if score is None:
         score = _scoring(fn, scoring)
-    if not (logits.is_cuda and logits.is_contiguous()
-            and topk_ids.dtype is _i32 and topk_ids.is_cuda and topk_ids.is_contiguous()
-            and topk_weights.dtype is _f32 and topk_weights.is_cuda and topk_weights.is_contiguous()
-            and expert_counts.dtype is _i32 and expert_counts.is_cuda and expert_counts.is_contiguous()
-            and routed_tokens.dtype is _i32 and routed_tokens.is_cuda and routed_tokens.is_contiguous()
-            and loss.dtype is _f32 and loss.is_cuda and loss.is_contiguous()):
-        _check_all((("logits", logits, logits.dtype), ("topk_ids", topk_ids, torch.int32),
-                    ("topk_weights", topk_weights, torch.float32),
-                    ("expert_counts", expert_counts, torch.int32),
-                    ("routed_tokens", routed_tokens, torch.int32), ("loss", loss, torch.float32)))
-    if bias is not None:
-        _check("bias", bias, _f32)
-        if bias.numel() != E:
-            raise ValueError(f"{fn}: bias has the wrong size")
-    if token_mask is not None:
-        _check("token_mask", token_mask, torch.bool)
-        if token_mask.numel() != T:
-            raise ValueError(f"{fn}: token_mask has the wrong size")
+    dev = logits.get_device()
+    if not (dev >= 0 and dev == _current_device() and logits.is_contiguous()
+            and topk_ids.dtype is _i32 and topk_ids.get_device() == dev and topk_ids.is_contiguous()
+            and topk_weights.dtype is _f32 and topk_weights.get_device() == dev and topk_weights.is_contiguous()
+            and expert_counts.dtype is _i32 and expert_counts.get_device() == dev and expert_counts.is_contiguous()
+            and routed_tokens.dtype is _i32 and routed_tokens.get_device() == dev and routed_tokens.is_contiguous()
+            and loss.dtype is _f32 and loss.get_device() == dev and loss.is_contiguous()
+            and _fits(bias, _f32, dev) and _fits(token_mask, _bool, dev)):
+        _check_here(fn, (("logits", logits, logits.dtype), ("topk_ids", topk_ids, torch.int32),
+                         ("topk_weights", topk_weights, torch.float32),
+                         ("expert_counts", expert_counts, torch.int32),
+                         ("routed_tokens", routed_tokens, torch.int32), ("loss", loss, torch.float32),
+                         ("bias", bias, torch.float32), ("token_mask", token_mask, torch.bool)))
+    if bias is not None and bias.numel() != E:
+        raise ValueError(f"{fn}: bias has the wrong size")
+    if token_mask is not None and token_mask.numel() != T:
+        raise ValueError(f"{fn}: token_mask has the wrong size")
     if topk_ids.numel() != T * K or topk_weights.numel() != T * K or expert_counts.numel() < E \
             or routed_tokens.numel() < 1 or loss.numel() < 1:
         raise ValueError(f"{fn}: output arrays have the wrong size")
-    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
-    if logits.get_device() != _current_device():
-        _refuse_device(fn, logits)
+    if workspace is not None:
+        _check_workspace(fn, workspace)
     st = (_lib or load()).moe_route_grouped(
         logits.data_ptr(), bf16, T, E, K, score, None if bias is None else bias.data_ptr(), groups, top_groups,
         group_top, 1 if renormalize else 0, scale, loss_coef, None if token_mask is None else token_mask.data_ptr(),
@@ -727,26 +736,23 @@ def moe_route_grouped_backward(logits, topk_ids, expert_counts, routed_tokens, g
     score = MOE_SCORES.get(scoring)
     if score is None:
         score = _scoring(fn, scoring)
-    if not (logits.is_cuda and logits.is_contiguous()
-            and grad_logits.dtype is logits.dtype and grad_logits.is_cuda and grad_logits.is_contiguous()
-            and topk_ids.dtype is _i32 and topk_ids.is_cuda and topk_ids.is_contiguous()
-            and expert_counts.dtype is _i32 and expert_counts.is_cuda and expert_counts.is_contiguous()
-            and routed_tokens.dtype is _i32 and routed_tokens.is_cuda and routed_tokens.is_contiguous()):
-        _check_all((("logits", logits, logits.dtype), ("grad_logits", grad_logits, logits.dtype),
-                    ("topk_ids", topk_ids, torch.int32),
-                    ("expert_counts", expert_counts, torch.int32),
-                    ("routed_tokens", routed_tokens, torch.int32)))
-    if grad_weights is not None:
-        _check("grad_weights", grad_weights, _f32)
-    if grad_loss is not None:
-        _check("grad_loss", grad_loss, _f32)
+    dev = logits.get_device()
+    if not (dev >= 0 and dev == _current_device() and logits.is_contiguous()
+            and grad_logits.dtype is logits.dtype and grad_logits.get_device() == dev and grad_logits.is_contiguous()
+            and topk_ids.dtype is _i32 and topk_ids.get_device() == dev and topk_ids.is_contiguous()
+            and expert_counts.dtype is _i32 and expert_counts.get_device() == dev and expert_counts.is_contiguous()
+            and routed_tokens.dtype is _i32 and routed_tokens.get_device() == dev and routed_tokens.is_contiguous()
+            and _fits(grad_weights, _f32, dev) and _fits(grad_loss, _f32, dev)):
+        _check_here(fn, (("logits", logits, logits.dtype), ("grad_logits", grad_logits, logits.dtype),
+                         ("topk_ids", topk_ids, torch.int32),
+                         ("expert_counts", expert_counts, torch.int32),
+                         ("routed_tokens", routed_tokens, torch.int32),
+                         ("grad_weights", grad_weights, torch.float32), ("grad_loss", grad_loss, torch.float32)))
     if topk_ids.numel() != T * K or expert_counts.numel() < E or routed_tokens.numel() < 1 \
             or grad_logits.numel() != T * E \
             or (grad_weights is not None and grad_weights.numel() != T * K) \
             or (grad_loss is not None and grad_loss.numel() != 1):
         raise ValueError(f"{fn}: argument sizes disagree")
-    if logits.get_device() != _current_device():
-        _refuse_device(fn, logits)
     st = (_lib or load()).moe_route_grouped_backward(
         logits.data_ptr(), bf16, T, E, K, score, 1 if renormalize else 0, scale, loss_coef,
         topk_ids.data_ptr(), expert_counts.data_ptr(), routed_tokens.data_ptr(),

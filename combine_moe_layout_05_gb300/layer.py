@@ -258,6 +258,7 @@ class Experts:
     def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor) -> torch.Tensor:
         """x [T, H] bf16 and its routing to [T, H] bf16."""
         T, K, dev = x.shape[0], topk_ids.shape[1], x.device
+        moe._refuse_other_devices("Experts", (("x", x), ("topk_ids", topk_ids), ("topk_weights", topk_weights)))
         self.dev_error = err = torch.zeros(9, dtype=torch.int32, device=dev)
         lay = moe.LayoutBuffers(T, K, self.E, self.R, device=dev)
         lay.dev_error = err[:1]
