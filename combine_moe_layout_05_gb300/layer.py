@@ -169,14 +169,20 @@ def expert_linear(x: torch.Tensor, weights: torch.Tensor, expert_offsets: torch.
                   bias: torch.Tensor | None = None, activation: str = "none", residual: torch.Tensor | None = None,
                   dev_error: torch.Tensor | None = None) -> torch.Tensor:
     """Packed rows [rows, H] times their experts' weights [E, N, H] (both bf16) as moe_expert_matmul has
-    it, with gradients of x, weights, bias ([E, N]) and residual.  The rows of no expert are unspecified,
+    it, with gradients of x, weights, bias (E * N values) and residual.  The rows of no expert are unspecified,
     in the output and in x's gradient.  dev_error, [2] int32: the forward's error word and the backward's."""
     train = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weights, bias))
     least = 16 if activation == "swiglu" else 8
     if train and weights.shape[1] % least:
         raise ValueError(f"expert_linear: the gradient needs N % {least} == 0, N is {weights.shape[1]}")
-    return _ExpertLinear.apply(x, weights, expert_offsets, None if bias is None else bias.float(), activation, residual,
-                               dev_error, train)
+    E, N, _ = weights.shape
+    if bias is not None:
+        bias = bias.float()
+        if bias.shape != (E, N) and bias.numel() == E * N:
+            bias = bias.reshape(E, N)
+    if residual is not None and residual.shape[:-1] != x.shape[:1] and residual.numel() >= x.shape[0] * residual.shape[-1]:
+        residual = residual.reshape(-1, residual.shape[-1])[:x.shape[0]]     # rows to spare: their gradient is 0
+    return _ExpertLinear.apply(x, weights, expert_offsets, bias, activation, residual, dev_error, train)
 
 
 class _Dispatch(torch.autograd.Function):

@@ -111,3 +111,25 @@ def test_offsets_longer_than_the_experts(products, activation, with_bias, tail):
         return [out.detach(), x.grad, w.grad] + ([b.grad] if with_bias else [])
     for a, c in zip(step(exact), step(torch.cat([exact, torch.tensor(tail, dtype=torch.int32)]))):
         assert torch.equal(a, c)
+
+
+def test_bias_and_residual_of_other_shapes(products):
+    """What the product takes by its size (a flat bias, a residual with rows to spare) has its own shape's gradient."""
+    E, rows, H, N = 2, 6, 8, 16
+    o = torch.tensor([0, 4, 6], dtype=torch.int32)
+
+    def step(bias_shape, residual_shape):
+        x, w = _leaf((rows, H), 1), _leaf((E, N, H), 2)
+        b = _leaf((E, N), 3, torch.float32).detach().reshape(bias_shape).requires_grad_()
+        r = torch.zeros(residual_shape, dtype=bf16)
+        r.view(-1)[:rows * N] = _leaf((rows, N), 4).detach().view(-1)
+        r.requires_grad_()
+        out = layer.expert_linear(x, w, o, b, "silu", r)
+        out.backward(_leaf((rows, N), 5).detach())
+        assert b.grad.shape == torch.Size(bias_shape) and r.grad.shape == torch.Size(residual_shape)
+        assert not r.grad.view(-1)[rows * N:].any()
+        return [out.detach(), x.grad, w.grad, b.grad.view(-1), r.grad.view(-1)[:rows * N]]
+    want = step((E, N), (rows, N))
+    for bias_shape, residual_shape in (((E * N,), (rows, N)), ((E, 1, N), (rows + 3, N)), ((E, N), (2, rows, N)), ((N, E), (3, 4, N))):
+        for a, c in zip(want, step(bias_shape, residual_shape)):
+            assert torch.equal(a, c)
