@@ -241,7 +241,10 @@ class Experts:
 
     ``dev_error``, [9] int32 on the device, holds the last call's error words: the layout's
     (MOE_DEV_ERR_EXPERT_RANGE where an id is -1), then for each of the four products the forward's and
-    the backward's, whose MOE_DEV_ERR_TIMEOUT says that the output or the gradient is unspecified.
+    the backward's, whose MOE_DEV_ERR_TIMEOUT says that the output or the gradient is unspecified.  Every
+    call has words of its own, and its backward pass writes there: a step that makes several calls before
+    it goes back gives each its words (``experts(x, ids, weights, dev_error=words[i])``), or keeps
+    ``dev_error`` after each.
 
     A training step can be captured into a CUDA graph: after a warm-up on a side stream, with gradients
     from torch.autograd.grad, and with no output of an eager call on the same leaves still alive, since
@@ -261,11 +264,19 @@ class Experts:
         self.gate_up_bias, self.down_bias, self.shared = gate_up_bias, down_bias, shared
         self.dev_error = None
 
-    def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor) -> torch.Tensor:
-        """x [T, H] bf16 and its routing to [T, H] bf16."""
+    def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                 dev_error: torch.Tensor | None = None) -> torch.Tensor:
+        """x [T, H] bf16 and its routing to [T, H] bf16.  dev_error, [9] int32: where this call and its
+        backward pass write their error words (None: a new tensor); they are set to 0 first."""
         T, K, dev = x.shape[0], topk_ids.shape[1], x.device
         moe._refuse_other_devices("Experts", (("x", x), ("topk_ids", topk_ids), ("topk_weights", topk_weights)))
-        self.dev_error = err = torch.zeros(9, dtype=torch.int32, device=dev)
+        if dev_error is None:
+            dev_error = torch.zeros(9, dtype=torch.int32, device=dev)
+        elif dev_error.shape != (9,) or dev_error.dtype != torch.int32 or dev_error.device != dev:
+            raise ValueError("Experts: dev_error must be [9] int32 on x's device")
+        else:
+            dev_error.zero_()
+        self.dev_error = err = dev_error
         lay = moe.LayoutBuffers(T, K, self.E, self.R, device=dev)
         lay.dev_error = err[:1]
         lay.run(topk_ids)

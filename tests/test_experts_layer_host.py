@@ -25,11 +25,10 @@ def _ranges(offsets, E, rows):
 
 
 class _Products:
-    """Stand-ins for the bf16 experts' calls; `timeouts` names the error words (of the calls in
-    order: forward products, then backward ones) that are set."""
+    """Stand-ins for the bf16 experts' calls.  late: the backward products report a wait that ran out."""
 
     def __init__(self):
-        self.words = []
+        self.late = False
 
     def matmul(self, x, weights, expert_offsets, out, bias=None, activation="none", residual=None, pre=None, dev_error=None,
                stream=None):
@@ -42,7 +41,6 @@ class _Products:
             out[r] = (y if residual is None else y + residual[r].float()).to(bf16)
         if dev_error is not None:
             dev_error.fill_(0)
-            self.words.append(dev_error)
 
     def activation_backward(self, pre, grad_out, expert_offsets, grad_pre, activation, grad_bias=None, workspace=None,
                             stream=None, E=None):
@@ -77,8 +75,27 @@ class _Products:
             if grad_weights is not None:
                 grad_weights[e] = (grad_pre[r].float().t() @ x[r].float()).to(bf16)
         if dev_error is not None:
-            dev_error.fill_(0)
-            self.words.append(dev_error)
+            dev_error.fill_(_binding.MOE_DEV_ERR_TIMEOUT if self.late else 0)
+
+
+def _layout(topk_ids, E, R, expert_counts, expert_offsets, rank_offsets, src_token, dst_row, dev_error=None, workspace=None,
+            stream=None):
+    flat = topk_ids.reshape(-1).long()
+    expert_offsets[0] = 0
+    expert_offsets[1:] = torch.cumsum(torch.bincount(flat, minlength=E), 0)
+    dst = torch.empty_like(flat)
+    dst[torch.argsort(flat, stable=True)] = torch.arange(flat.numel())
+    dst_row.copy_(dst.view(topk_ids.shape))
+    if dev_error is not None:
+        dev_error.fill_(0)
+
+
+def _dispatch(tokens, dst_row, packed, scales=None, fp8=False, stream=None):
+    packed[dst_row.reshape(-1).long()] = tokens.repeat_interleave(dst_row.shape[1], 0)
+
+
+def _combine(expert_out, topk_weights, dst_row, out, stream=None):
+    out.copy_((expert_out[dst_row.long()].float() * topk_weights[..., None]).sum(1))
 
 
 @pytest.fixture
@@ -88,6 +105,10 @@ def products(monkeypatch):
     monkeypatch.setattr(_binding, "moe_expert_activation_backward", p.activation_backward)
     monkeypatch.setattr(_binding, "moe_expert_matmul_backward", p.matmul_backward)
     monkeypatch.setattr(_binding, "moe_expert_activation_backward_workspace_bytes", lambda rows, N, E: 256)
+    monkeypatch.setattr(_binding, "moe_layout", _layout)
+    monkeypatch.setattr(_binding, "moe_layout_workspace_bytes", lambda T, K, E: 256)
+    monkeypatch.setattr(_binding, "moe_dispatch", _dispatch)
+    monkeypatch.setattr(_binding, "moe_combine", _combine)
     return p
 
 
@@ -133,3 +154,33 @@ def test_bias_and_residual_of_other_shapes(products):
     for bias_shape, residual_shape in (((E * N,), (rows, N)), ((E, 1, N), (rows + 3, N)), ((E, N), (2, rows, N)), ((N, E), (3, 4, N))):
         for a, c in zip(want, step(bias_shape, residual_shape)):
             assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_error_words_of_two_calls_before_their_backward_passes(products, given):
+    """Two micro-batches forward, then both back: each one's words say what became of its gradients."""
+    E, T, K, H, N = 4, 6, 2, 16, 16
+    g = torch.Generator().manual_seed(1)
+    experts = layer.Experts(_leaf((E, 2 * N, H), 1), _leaf((E, H, N), 2), shared=(_leaf((2 * N, H), 3), _leaf((H, N), 4)))
+    words = torch.full((2, 9), 7, dtype=torch.int32)
+    outs, kept = [], []
+    for i in range(2):
+        ids = torch.rand((T, E), generator=g).argsort(1)[:, :K].to(torch.int32)
+        x = _leaf((T, H), 5 + i)
+        outs.append(experts(x, ids, torch.full((T, K), 0.5), **(dict(dev_error=words[i]) if given else {})))
+        kept.append(experts.dev_error)
+        assert experts.dev_error.tolist() == [0] * 9 and (not given or words[i].tolist() == [0] * 9)
+    late = _binding.MOE_DEV_ERR_TIMEOUT
+    products.late = True
+    outs[0].float().sum().backward()
+    products.late = False
+    outs[1].float().sum().backward()
+    want = [[0] + [0, late] * 4, [0] * 9]
+    assert [k.tolist() for k in kept] == want and (not given or words.tolist() == want)
+
+
+@pytest.mark.parametrize("words", [torch.zeros(8, dtype=torch.int32), torch.zeros(9), torch.zeros((1, 9), dtype=torch.int32)])
+def test_unfit_error_words_are_refused(products, words):
+    experts = layer.Experts(_leaf((2, 16, 8), 1), _leaf((2, 8, 8), 2))
+    with pytest.raises(ValueError):
+        experts(_leaf((3, 8), 3), torch.zeros((3, 1), dtype=torch.int32), torch.ones((3, 1)), dev_error=words)
