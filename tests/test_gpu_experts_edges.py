@@ -1,6 +1,8 @@
 """The bf16 experts' calls and expert_linear where their arguments are unusual:
 offsets longer than the experts, values near the type's largest.  Calls that differ
 only in what is not used have to give the same bits."""
+import math
+
 import pytest
 import torch
 
@@ -78,3 +80,48 @@ def test_slopes_at_the_largest_values(activation):
     slope = torch.where(z > 0, 1.0, 0.0) + torch.where(z == 0, 0.5, 0.0)
     want = dy.double() * slope.double() * (2 if activation == "swiglu" else 1)
     assert bool(((out[:, :8].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-37).all())
+
+
+def slope(z, activation):
+    """a'(z) in 64 bits and the magnitude of its terms."""
+    if activation == "none":
+        return torch.ones_like(z), torch.ones_like(z)
+    if activation == "gelu":
+        k, c = 2 * math.sqrt(2 / math.pi), 0.044715
+        s = torch.sigmoid(k * (z + c * z ** 3))
+        return s + z * s * (1 - s) * k * (1 + 3 * c * z * z), 1 + z.abs() * (1 + z * z)
+    s = torch.sigmoid(z)
+    return s * (1 + z * (1 - s)), 1 + z.abs()
+
+
+@pytest.mark.parametrize("activation", ["none", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("N", [16, 64, 528, 4112])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 17, 1], [127, 128, 129, 0, 700], [4] * 256])
+def test_every_activation_gradient_is_within_its_bound(counts, N, activation, with_bias):
+    """Each value, so that a NaN is outside: terms that cancel to 2^-17 of their magnitudes (the sigmoid's
+    relative error is below (|u| + 6) 2^-24, |z| < 60 here), then one rounding to bf16."""
+    E, rows, C = len(counts), sum(counts), N // 2 if activation == "swiglu" else N
+    o = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+    z, dy = normal((rows, N), N, 2.0), normal((rows, C), N + 1)
+    out, gb = torch.full_like(z, float("nan")), torch.full((E, N), float("nan"), device="cuda") if with_bias else None
+    ws = torch.empty(moe.moe_expert_activation_backward_workspace_bytes(rows, N, E), dtype=torch.uint8, device="cuda")
+    moe.moe_expert_activation_backward(z, dy, o, out, activation, grad_bias=gb, workspace=ws)
+    g, z = dy.double(), z.double()
+    if activation == "swiglu":
+        a, u = z.chunk(2, 1)
+        d, m = slope(a, "silu")
+        s = torch.sigmoid(a)
+        want, size = torch.cat([g * u * d, g * a * s], 1), torch.cat([(g * u).abs() * m, (g * a).abs()], 1)
+    else:
+        d, m = slope(z, activation)
+        want, size = g * d, g.abs() * m
+    off = 1.01 * 2.0 ** -17 * size
+    assert bool(((out.double() - want).abs() <= off + 2.0 ** -8 * want.abs()).all())
+    if with_bias:
+        e = torch.repeat_interleave(torch.arange(E, device="cuda"), torch.tensor(counts, device="cuda"))
+
+        def per_expert(t):
+            return torch.zeros((E, N), dtype=torch.float64, device="cuda").index_add_(0, e, t)
+        room = per_expert(off) + 1.01 * torch.tensor(counts, device="cuda")[:, None] * 2.0 ** -24 * per_expert(want.abs())
+        assert bool(((gb.double() - per_expert(want)).abs() <= room).all())
