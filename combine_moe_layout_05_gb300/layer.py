@@ -123,13 +123,20 @@ def move_balance_bias(bias: torch.Tensor, expert_counts: torch.Tensor, rate: flo
         return bias.add_(torch.sign(counts.mean() - counts), alpha=rate)
 
 
+def _whole(t: torch.Tensor) -> torch.Tensor:
+    """Contiguous and on 16 bytes, as the calls need a matrix.  A view into a larger buffer may be neither,
+    and gradients come as such views too (torch.cat's): it is copied."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _ExpertLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weights, expert_offsets, bias, activation, residual, error, train):
         rows, (E, N, _) = x.shape[0], weights.shape
-        x, weights = x.contiguous(), weights.contiguous()
+        x, weights = _whole(x), _whole(weights)
         bias = None if bias is None else bias.contiguous()
-        residual = None if residual is None else residual.contiguous()
+        residual = None if residual is None else _whole(residual)
         out = torch.empty((rows, N // 2 if activation == "swiglu" else N), dtype=torch.bfloat16, device=x.device)
         pre = torch.empty((rows, N), dtype=torch.bfloat16, device=x.device) if train and activation != "none" else None
         moe.moe_expert_matmul(x, weights, expert_offsets, out, bias, activation, residual, pre,
@@ -143,7 +150,7 @@ class _ExpertLinear(torch.autograd.Function):
     def backward(ctx, grad_out):
         x, weights, offsets, pre = ctx.saved_tensors
         need_x, need_w, _, need_bias, _, need_residual = ctx.needs_input_grad[:6]
-        grad_out = grad_out.contiguous()
+        grad_out = _whole(grad_out)
         grad_x = grad_w = grad_bias = None
         if need_x or need_w or need_bias:
             rows, (E, N, _) = x.shape[0], weights.shape
@@ -189,7 +196,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, dst_row):
         packed = torch.empty((dst_row.numel(), x.shape[1]), dtype=torch.bfloat16, device=x.device)
-        moe.moe_dispatch(x.contiguous(), dst_row, packed)
+        moe.moe_dispatch(_whole(x), dst_row, packed)
         ctx.save_for_backward(dst_row)
         return packed
 
@@ -200,7 +207,7 @@ class _Dispatch(torch.autograd.Function):
         T, H = dst_row.shape[0], grad.shape[1]
         out = torch.empty((T, H), dtype=torch.bfloat16, device=grad.device)
         # each token's K rows added up
-        moe.moe_combine(grad.contiguous(), torch.ones(dst_row.shape, dtype=torch.float32, device=grad.device), dst_row, out)
+        moe.moe_combine(_whole(grad), torch.ones(dst_row.shape, dtype=torch.float32, device=grad.device), dst_row, out)
         return out, None
 
 
@@ -209,7 +216,7 @@ class _Combine(torch.autograd.Function):
     def forward(ctx, rows, topk_weights, dst_row):
         out = torch.empty((dst_row.shape[0], rows.shape[1]), dtype=torch.bfloat16, device=rows.device)
         topk_weights = topk_weights.contiguous()
-        moe.moe_combine(rows.contiguous(), topk_weights, dst_row, out)
+        moe.moe_combine(_whole(rows), topk_weights, dst_row, out)
         ctx.save_for_backward(rows, topk_weights, dst_row)
         return out
 

@@ -10,6 +10,13 @@ from combine_moe_layout_05_gb300 import _binding, layer
 bf16 = torch.bfloat16
 
 
+def _aligned(*tensors):
+    """The calls refuse matrices that do not start on 16 bytes."""
+    for t in tensors:
+        if t is not None and t.data_ptr() % 16:
+            raise _binding.MoeError("stand-in", 2)
+
+
 def _activate(z, activation):
     if activation == "swiglu":
         a, u = z.chunk(2, 1)
@@ -32,6 +39,7 @@ class _Products:
 
     def matmul(self, x, weights, expert_offsets, out, bias=None, activation="none", residual=None, pre=None, dev_error=None,
                stream=None):
+        _aligned(x, weights, out, residual, pre)
         out.fill_(-77.0)
         for e, r in _ranges(expert_offsets, weights.shape[0], x.shape[0]):
             z = x[r].float() @ weights[e].float().t() + (0 if bias is None else bias.view(weights.shape[:2])[e])
@@ -46,6 +54,7 @@ class _Products:
                             stream=None, E=None):
         if E is None:
             E = expert_offsets.numel() - 1 if grad_bias is None else grad_bias.shape[0]
+        _aligned(pre, grad_out, grad_pre)
         o = expert_offsets.tolist()
         # without the bias the calls' own reading: one run of rows, from the first expert's to the last one's
         parts = _ranges(expert_offsets, E, grad_out.shape[0]) if grad_bias is not None else [(0, slice(o[0], max(o[0], o[E])))]
@@ -65,6 +74,7 @@ class _Products:
 
     def matmul_backward(self, grad_pre, x, weights, expert_offsets, grad_x=None, grad_weights=None, accumulate=False,
                         dev_error=None, stream=None):
+        _aligned(grad_pre, x, weights, grad_x, grad_weights)
         if grad_x is not None:
             grad_x.fill_(-77.0)
         if grad_weights is not None:
@@ -91,15 +101,18 @@ def _layout(topk_ids, E, R, expert_counts, expert_offsets, rank_offsets, src_tok
 
 
 def _dispatch(tokens, dst_row, packed, scales=None, fp8=False, stream=None):
+    _aligned(tokens, packed)
     packed[dst_row.reshape(-1).long()] = tokens.repeat_interleave(dst_row.shape[1], 0)
 
 
 def _combine(expert_out, topk_weights, dst_row, out, stream=None):
+    _aligned(expert_out, out)
     out.copy_((expert_out[dst_row.long()].float() * topk_weights[..., None]).sum(1))
 
 
 @pytest.fixture
 def products(monkeypatch):
+    monkeypatch.setattr(_binding, "moe_status_string", str)
     p = _Products()
     monkeypatch.setattr(_binding, "moe_expert_matmul", p.matmul)
     monkeypatch.setattr(_binding, "moe_expert_activation_backward", p.activation_backward)
@@ -184,3 +197,49 @@ def test_unfit_error_words_are_refused(products, words):
     experts = layer.Experts(_leaf((2, 16, 8), 1), _leaf((2, 8, 8), 2))
     with pytest.raises(ValueError):
         experts(_leaf((3, 8), 3), torch.zeros((3, 1), dtype=torch.int32), torch.ones((3, 1)), dev_error=words)
+
+
+def _off(t):
+    """The same values two bytes off the 16-byte grid, and contiguous."""
+    flat = torch.zeros(t.numel() + 8, dtype=t.dtype)
+    at = 1 + (-flat.data_ptr() // t.element_size()) % 8
+    flat[at:at + t.numel()] = t.detach().reshape(-1)
+    return flat[at:at + t.numel()].view(t.shape)
+
+
+@pytest.mark.parametrize("activation", ["none", "silu", "swiglu"])
+def test_tensors_off_the_16_byte_grid(products, activation):
+    """Inputs that are views into larger buffers, and gradients that autograd hands on as such views (of
+    torch.cat's, here behind three other values)."""
+    E, rows, H, N = 2, 6, 8, 16
+    C = N // 2 if activation == "swiglu" else N
+    o = torch.tensor([0, 4, 6], dtype=torch.int32)
+
+    def step(at, tail):
+        x, w, r = (at(_leaf(s, i).detach()).requires_grad_() for i, s in enumerate(((rows, H), (E, N, H), (rows, C))))
+        out = layer.expert_linear(x, w, o, None, activation, r)
+        tail(out).backward()
+        return [out.detach(), x.grad, w.grad, r.grad]
+    pull = _leaf((rows * C,), 9).detach()
+
+    def behind_others(out):
+        return (torch.cat([torch.zeros(3, dtype=bf16), out.reshape(-1)])[3:] * pull).sum()
+    want = step(lambda t: t, lambda out: (out.reshape(-1) * pull).sum())
+    for got in (step(_off, lambda out: (out.reshape(-1) * pull).sum()), step(lambda t: t, behind_others), step(_off, behind_others)):
+        assert all(torch.equal(a, c) for a, c in zip(want, got))
+
+
+def test_experts_off_the_16_byte_grid(products):
+    E, T, K, H, N = 4, 6, 2, 16, 16
+    ids = torch.rand((T, E), generator=torch.Generator().manual_seed(1)).argsort(1)[:, :K].to(torch.int32)
+    pull = _leaf((T * H,), 9).detach()
+
+    def step(at, front):
+        leaves = [at(_leaf(s, i).detach()).requires_grad_() for i, s in
+                  enumerate(((E, 2 * N, H), (E, H, N), (2 * N, H), (H, N), (T, H)))]
+        out = layer.Experts(leaves[0], leaves[1], shared=(leaves[2], leaves[3]))(leaves[4], ids, torch.full((T, K), 0.5))
+        (torch.cat([torch.zeros(front, dtype=bf16), out.reshape(-1)])[front:] * pull).sum().backward()
+        return [out.detach()] + [t.grad for t in leaves]
+    want = step(lambda t: t, 8)
+    for at in (lambda t: t, _off):
+        assert all(torch.equal(a, c) for a, c in zip(want, step(at, 3)))

@@ -125,3 +125,46 @@ def test_every_activation_gradient_is_within_its_bound(counts, N, activation, wi
             return torch.zeros((E, N), dtype=torch.float64, device="cuda").index_add_(0, e, t)
         room = per_expert(off) + 1.01 * torch.tensor(counts, device="cuda")[:, None] * 2.0 ** -24 * per_expert(want.abs())
         assert bool(((gb.double() - per_expert(want)).abs() <= room).all())
+
+
+def off_the_grid(t):
+    """The same values, contiguous, two bytes past a multiple of 16."""
+    flat = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+    flat[1:] = t.reshape(-1)
+    return flat[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("activation", ["none", "swiglu"])
+def test_tensors_and_gradients_off_the_16_byte_grid(activation):
+    """Views into larger buffers, and gradients that torch.cat hands on as such views."""
+    from combine_moe_layout_05_gb300.layer import expert_linear
+    rows, H, N = 50, 72, 96
+    C = N // 2 if activation == "swiglu" else N
+    o = torch.tensor([0, 20, 50], dtype=torch.int32, device="cuda")
+    pull = normal((rows * C,), 9)
+
+    def step(at, front):
+        x, w, r = (at(normal(s, i)).requires_grad_() for i, s in enumerate(((rows, H), (2, N, H), (rows, C))))
+        out = expert_linear(x, w, o, None, activation, r)
+        (torch.cat([pull.new_zeros(front), out.reshape(-1)])[front:] * pull).sum().backward()
+        return [out.detach(), x.grad, w.grad, r.grad]
+    want = step(lambda t: t, 8)
+    for at, front in ((off_the_grid, 8), (lambda t: t, 3), (off_the_grid, 3)):
+        assert all(torch.equal(a, c) for a, c in zip(want, step(at, front)))
+
+
+@pytest.mark.parametrize("activation", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_activation_gradient_in_its_own_gradients_place(activation, with_bias):
+    """grad_pre may be grad_out itself where not gated."""
+    o = torch.tensor([2, 100, 100, 297], dtype=torch.int32, device="cuda")
+    pre, dy = normal((300, 264), 1), normal((300, 264), 2)
+    ws = torch.empty(moe.moe_expert_activation_backward_workspace_bytes(300, 264, 3), dtype=torch.uint8, device="cuda")
+
+    def call(to, src):
+        gb = torch.zeros((3, 264), device="cuda") if with_bias else None
+        moe.moe_expert_activation_backward(pre, src, o, to, activation, grad_bias=gb, workspace=ws)
+        return gb
+    want, place = dy.clone(), dy.clone()
+    a, b = call(want, dy), call(place, place)
+    assert torch.equal(want, place) and (not with_bias or torch.equal(a, b))
