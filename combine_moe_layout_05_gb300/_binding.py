@@ -455,7 +455,7 @@ def _check_here(fn: str, tensors) -> None:
 
 
 def _check_workspace(fn: str, workspace) -> None:
-    if not (workspace.is_cuda and workspace.is_contiguous()):
+    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
     _refuse_other_devices(fn, (("workspace", workspace),))
 
@@ -524,10 +524,12 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
         act = _activation(fn, activation)
     dev = grad_out.get_device()
     if not (dev >= 0 and dev == _current_device() and _fits(pre, _bf16, dev) and _fits(grad_out, _bf16, dev)
-            and _fits(grad_pre, _bf16, dev) and _fits(grad_bias, _f32, dev) and _fits(expert_offsets, _i32, dev)):
+            and _fits(grad_pre, _bf16, dev) and _fits(grad_bias, _f32, dev) and _fits(expert_offsets, _i32, dev)
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
         _check_here(fn, (("pre", pre, torch.bfloat16), ("grad_out", grad_out, torch.bfloat16),
                          ("grad_pre", grad_pre, torch.bfloat16), ("grad_bias", grad_bias, torch.float32),
                          ("expert_offsets", expert_offsets, torch.int32)))
+        _check_workspace(fn, workspace)
     rows, C = grad_out.shape
     N = 2 * C if act == 3 else C
     if E is None:
@@ -536,8 +538,6 @@ def moe_expert_activation_backward(pre, grad_out, expert_offsets, grad_pre, acti
             or (pre is not None and (pre.numel() < rows * N or pre.shape[-1] != N)) \
             or (grad_pre is not None and (grad_pre.numel() < rows * N or grad_pre.shape[-1] != N)):
         raise ValueError(f"{fn}: argument sizes disagree")
-    if workspace is not None:
-        _check_workspace(fn, workspace)
     st = (_lib or load()).moe_expert_activation_backward(
         None if pre is None else pre.data_ptr(), grad_out.data_ptr(), expert_offsets.data_ptr(), rows, N, E, act,
         None if grad_pre is None else grad_pre.data_ptr(), None if grad_bias is None else grad_bias.data_ptr(),
@@ -698,12 +698,15 @@ def moe_route_grouped(logits, bias, topk_ids, topk_weights, expert_counts, route
             and expert_counts.dtype is _i32 and expert_counts.get_device() == dev and expert_counts.is_contiguous()
             and routed_tokens.dtype is _i32 and routed_tokens.get_device() == dev and routed_tokens.is_contiguous()
             and loss.dtype is _f32 and loss.get_device() == dev and loss.is_contiguous()
-            and _fits(bias, _f32, dev) and _fits(token_mask, _bool, dev)):
+            and (bias is None or (bias.dtype is _f32 and bias.get_device() == dev and bias.is_contiguous()))
+            and (token_mask is None or _fits(token_mask, _bool, dev))
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
         _check_here(fn, (("logits", logits, logits.dtype), ("topk_ids", topk_ids, torch.int32),
                          ("topk_weights", topk_weights, torch.float32),
                          ("expert_counts", expert_counts, torch.int32),
                          ("routed_tokens", routed_tokens, torch.int32), ("loss", loss, torch.float32),
                          ("bias", bias, torch.float32), ("token_mask", token_mask, torch.bool)))
+        _check_workspace(fn, workspace)
     if bias is not None and bias.numel() != E:
         raise ValueError(f"{fn}: bias has the wrong size")
     if token_mask is not None and token_mask.numel() != T:
@@ -711,8 +714,6 @@ def moe_route_grouped(logits, bias, topk_ids, topk_weights, expert_counts, route
     if topk_ids.numel() != T * K or topk_weights.numel() != T * K or expert_counts.numel() < E \
             or routed_tokens.numel() < 1 or loss.numel() < 1:
         raise ValueError(f"{fn}: output arrays have the wrong size")
-    if workspace is not None:
-        _check_workspace(fn, workspace)
     st = (_lib or load()).moe_route_grouped(
         logits.data_ptr(), bf16, T, E, K, score, None if bias is None else bias.data_ptr(), groups, top_groups,
         group_top, 1 if renormalize else 0, scale, loss_coef, None if token_mask is None else token_mask.data_ptr(),
