@@ -168,3 +168,21 @@ def test_activation_gradient_in_its_own_gradients_place(activation, with_bias):
     want, place = dy.clone(), dy.clone()
     a, b = call(want, dy), call(place, place)
     assert torch.equal(want, place) and (not with_bias or torch.equal(a, b))
+
+
+def test_experts_when_no_token_is_routed():
+    """All ids -1: nothing for the experts, zero gradients, and the shared expert's output alone."""
+    from combine_moe_layout_05_gb300.layer import Experts
+    T, E, H, N = 20, 4, 64, 32
+    leaves = [normal(s, i, 0.1).requires_grad_() for i, s in enumerate(((E, 2 * N, H), (E, H, N), (2 * N, H), (H, N), (T, H)))]
+    ids = torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+    weights = torch.ones((T, 2), device="cuda", requires_grad=True)
+    alone = Experts(leaves[0], leaves[1])(leaves[4], ids, weights)
+    assert not bool(alone.any())
+    out = Experts(leaves[0], leaves[1], shared=(leaves[2], leaves[3]))(leaves[4], ids, weights)
+    out.backward(torch.ones_like(out))
+    assert not bool(leaves[0].grad.any()) and not bool(leaves[1].grad.any()) and not bool(weights.grad.any())
+    a, u = (leaves[4].detach().double() @ leaves[2].detach().double().t()).chunk(2, 1)
+    want = (a * torch.sigmoid(a) * u) @ leaves[3].detach().double().t()
+    assert float((out.detach().double() - want).norm()) <= 3 * 2.0 ** -8 * float(want.norm())
+    assert all(bool(t.grad.isfinite().all()) and bool(t.grad.any()) for t in leaves[2:])
