@@ -106,3 +106,28 @@ def test_biases_at_the_ends_of_fp32(value, scoring):
     bias[8:12] = value
     for top_groups, group_top, K in ((1, 2, 6), (3, 2, 8), (3, 1, 8), (8, 1, 8)):
         check(x, bias, K, scoring, 8, top_groups, group_top)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_scores_below_the_smallest_number(renorm):
+    """Sigmoid scores below 2^-126 are 0: where all of a token's are, so are its weights, its part of the
+    loss and its gradient; the choice goes by the logits, or by the bias."""
+    T, E, K = 6, 64, 4
+    x = -torch.linspace(88, 200, E, device="cuda").repeat(T, 1)
+    x[3:, 7] = 1.0
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, weights = torch.empty((T, K), **i32), torch.empty((T, K), device="cuda")
+    counts, routed, loss = torch.empty(E, **i32), torch.empty(1, **i32), torch.empty(1, device="cuda")
+    ws = torch.empty(moe.moe_route_grouped_workspace_bytes(T, E), dtype=torch.uint8, device="cuda")
+    for bias, rest in ((None, [0, 1, 2, 3]), (torch.linspace(0, 0.5, E, device="cuda"), [63, 62, 61, 60])):
+        moe.moe_route_grouped(x, bias, ids, weights, counts, routed, loss, renormalize=renorm, workspace=ws)
+        assert ids[0].tolist() == rest and ids[5].tolist() == [7] + rest[:3]
+        assert not bool(weights[:3].any()) and not bool(weights[3:, 1:].any()) and routed.item() == T
+        s = 1 / (1 + math.exp(-1.0))
+        assert bool(((weights[3:, 0] - (1.0 if renorm else s)).abs() <= 1e-6).all())
+        want = E * 3 / (K * T) * 3 / T                   # expert 7: chosen three times, all of three tokens' probability
+        assert abs(loss.item() - want) <= 1e-5 * want
+        grad = torch.full_like(x, -9.0)
+        moe.moe_route_grouped_backward(x, ids, counts, routed, torch.ones_like(weights), torch.ones(1, device="cuda"), grad,
+                                       renormalize=renorm)
+        assert not bool(grad[:3].any()) and bool(grad.isfinite().all())
