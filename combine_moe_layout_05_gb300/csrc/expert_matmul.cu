@@ -51,11 +51,16 @@ cudaError_t launch(const void *x, const void *w, const int32_t *offsets, int row
         if (parts > 1) return go(Split<G>{}, parts);
     }
     // By rows an expert, on average.  Narrow and Mid: 7.8 and 10.9 us at 16 rows of one
-    // expert (2048 -> 2048), equal to 3 % with 64 experts to 32 rows, where Narrow
-    // begins to read weights twice (94.1 and 85.4 us at 48).  Mid and Wide, 64 experts,
-    // 2048 -> 2048: 89.6 and 93.2 us at 96 rows each, 106 and 99 at 160, 381 and 338 at
-    // 1024; 512 -> 4096: 51.7 and 52.0 at 96, 59.4 and 57.1 at 160, 251 and 212 at 1024;
-    // skewed (48 experts, 2056 -> 1001): 42 and 48 us at 50 on average, 53 and 51 at 97.
+    // expert (2048 -> 2048), 138 and 140 at 8 rows of 32 (7168 -> 2048), but 83.8 and
+    // 80.7 at 16 rows of 64 (2048 -> 2048), and from 32 rows on Narrow reads weights
+    // twice (93.8 and 83.8 at 48).  The average does not see rows that are a few
+    // experts': 8 of 256 with 512 rows each (2048 -> 2048) 74.6 and 29.4.  Mid and
+    // Wide, even loads: the border is between 128 and 160 rows (64 experts, 2048 ->
+    // 2048: 87.9 and 90.8 at 96, 90.4 and 93.4 at 128, 105 and 96 at 160, 381 and 338 at
+    // 1024; 32, 7168 -> 2048: 150 and 157 at 96, 153 and 161 at 128, 184 and 165 at 160;
+    // 64, 512 -> 4096: 51.3 and 51.7 at 96, 54.7 and 54.5 at 128).  Rows in proportion
+    // to 1 / rank, nearer to what routing gives: 95.1 and 91.8 at 96, 159 and 163 (172
+    // and 161 at 128), 55.7 and 53.7; 48 experts, 2056 -> 1008, 46.6 and 43.7.
     if (rows <= 16 * E) return go(Narrow<G>{}, 1);
     return rows >= 96 * E ? go(Wide<G>{}, 1) : go(Mid<G>{}, 1);
 }

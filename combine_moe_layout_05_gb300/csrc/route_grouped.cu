@@ -16,11 +16,18 @@
 // fetching of its instructions, and the call ends with its slowest block: a
 // choice in 64 bits of all that was open took 10 to 25 us of a call of 25.
 //
-// 16384 x 256 fp32, K = 8, bias, the best 4 of 8 groups: 28.5 us; without groups
-// and bias 24.3 (moe_route, with softmax: 19.0).  Issue slots bound it: 831
-// instructions a token (moe_route 478), of which the groups take 190, the scores
-// and keys 150, the picks 140; 32 warps a multiprocessor (24: 32.3 us, 16 in
-// larger blocks 30.9).  Some 8 us are the two launches.  One token: 4.7 us.
+// 16384 x 256 fp32, K = 8, bias, the best 4 of 8 groups: 28.6 us; without groups
+// and bias 24.3 (moe_route, with softmax: 19.0); some 2 us more where tokens are
+// valued again, 10 to 13 where one is left for settle.  No single thing bounds it.
+// A multiprocessor has a block in 65 % of the kernel's cycles: some 8 us are the two
+// launches, and a warp has 3.37 tokens, so that 37 % of the blocks have a fourth
+// round that the others wait for.  In those cycles 62 % of the issue slots are used,
+// by 882 instructions a token (724 without groups and bias, moe_route 478); the
+// warps wait for one another's slots, for results in a token's chain of dependent
+// steps, and for shared and global memory, about as much for each.  32 warps a
+// multiprocessor (24: 32.3 us, 16 in larger blocks 30.9) leave 64 registers a
+// thread: this form spills 76 bytes of stores and 68 of loads, 1.6 % of its
+// instructions.  One token: 4.9 us.
 #include "activation.cuh"
 #include "route_grouped.cuh"
 #include "route_totals.cuh"

@@ -176,9 +176,15 @@ cudaError_t launch_route_finish(const uint32_t *part, int clusters, int E, int K
 
 // Blocks of one cluster that writes the results itself, or 0 where two
 // launches over all multiprocessors are quicker: by tokens a warp, fewer the
-// wider the rows (one and two launches, a call among others: E = 128, 512
-// tokens 6.7 and 7.9 us; E = 256, 256 tokens 6.1 and 8.7, 512 tokens 8.9 and
-// 7.7; E = 1000, 256 tokens 23.3 and 20.4).
+// wider the rows (moe_route, 16 warps a block, one and two launches, a call among
+// others: E = 128, 512 tokens 6.7 and 7.9 us; E = 256, 256 tokens 6.1 and 8.7, 512
+// tokens 8.9 and 7.7; E = 1000, 256 tokens 23.3 and 20.4).  moe_route_grouped has 8
+// warps and takes longer for a token, so its border is earlier than this rule's
+// (one and two launches, bias and groups: E = 128, 64 tokens 5.1 and 6.8 us, 128
+// 7.0 and 6.8, 256 10.5 and 6.8; E = 256, 64 tokens 6.0 and 7.5, 128 8.2 and 7.6;
+// E = 512, 64 tokens 8.1 and 9.7, 128 11.9 and 10.0; E = 1000, 64 tokens 16.3 and
+// 18.2, where the rule ends): between 65 tokens and the rule's end it costs up to
+// 3.7 us.
 template <int WARPS>
 int single_blocks(int T, int E)
 {

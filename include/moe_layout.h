@@ -452,8 +452,9 @@ MOE_API moe_status_t moe_route_backward(const void *logits, int32_t bf16, int32_
  *
  * Open experts and routed tokens are moe_route's.  With x the logits:
  *
- *   s[t,e]  MOE_SCORE_SIGMOID: 1 / (1 + exp(-x[t,e])); MOE_SCORE_SOFTMAX:
- *           moe_route's p[t,e]; 0 for an expert that is not open
+ *   s[t,e]  MOE_SCORE_SIGMOID: 1 / (1 + exp(-x[t,e])), 0 where that is below
+ *           2^-126 (x below -87.3); MOE_SCORE_SOFTMAX: moe_route's p[t,e]; 0 for an
+ *           expert that is not open
  *   c[t,e]  s[t,e] + bias[e] of an open expert: what the choice goes by
  *   groups  expert e is in group e / (E / groups).  A group's value is the sum of
  *           its group_top (1 or 2) largest c (of its one open expert, the one c);
@@ -462,9 +463,10 @@ MOE_API moe_status_t moe_route_backward(const void *logits, int32_t bf16, int32_
  *   topk_ids[t,:]      the K experts of largest c left, largest first, ties to
  *                      the lowest index; -1 where fewer are open
  *   topk_weights[t,k]  scale * s at topk_ids[t,k], s divided by the sum of the
- *                      token's K first when renormalize == 1; 0 where topk_ids is -1
+ *                      token's K first when renormalize == 1 (all 0 where that is
+ *                      0); 0 where topk_ids is -1
  *   expert_counts, routed_tokens, loss   moe_route's, with p[t,e] = s[t,e] / sum
- *                      over e' of s[t,e']
+ *                      over e' of s[t,e'] (0 where that is 0)
  *
  * The choice is that of exact arithmetic on the given logits and bias, as far as
  * 64 bits tell two values apart (equal ones go by index): where fp32 might order
