@@ -1,5 +1,5 @@
-"""The products are called as the first CUDA work of a thread, as autograd's own
-thread does where a gradient comes straight from the caller: same bits as here."""
+"""The routers' and the experts' calls as the first CUDA work of a thread, as autograd's
+own thread makes them where a gradient comes straight from the caller: same bits as here."""
 import threading
 
 import pytest
@@ -73,3 +73,33 @@ def test_gradient_given_by_the_caller():
     gx, gw = torch.empty_like(x), torch.empty_like(w)
     moe.moe_expert_matmul_backward(g, x.detach(), w.detach(), o, gx, gw)
     assert torch.equal(x.grad, gx) and torch.equal(w.grad, gw)
+
+
+@pytest.mark.parametrize("what", ["route", "route_backward", "activation"])
+@pytest.mark.parametrize("rows", [5, 4000])
+def test_other_calls(what, rows):
+    x, bias = normal((rows, 64), 1).float(), torch.linspace(0, 0.1, 64, device="cuda")
+    o = torch.tensor([0, 3, rows], dtype=torch.int32, device="cuda")
+    pre, dy, dw = normal((rows, 64), 2), normal((rows, 64), 3), torch.ones((rows, 4), device="cuda")
+    route = moe.RouteBuffers(rows, 4, 64).run(x)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    outs = []
+    for _ in range(2):
+        r = moe.RouteBuffers(rows, 4, 64)
+        outs.append(dict(route=[r.topk_ids, r.topk_weights, r.expert_counts, r.routed_tokens, r.loss],
+                         route_backward=[torch.zeros_like(x)],
+                         activation=[torch.zeros_like(pre), torch.zeros((2, 64), device="cuda")])[what])
+        for t in outs[-1]:
+            t.zero_()
+
+    def call(out):
+        if what == "route":
+            moe.moe_route_grouped(x, bias, *out, groups=8, top_groups=4, workspace=ws)
+        elif what == "route_backward":
+            moe.moe_route_grouped_backward(x, route.topk_ids, route.expert_counts, route.routed_tokens, dw, route.loss, *out)
+        else:
+            moe.moe_expert_activation_backward(pre, dy, o, out[0], "silu", grad_bias=out[1], workspace=ws)
+    torch.cuda.synchronize()
+    in_a_thread(lambda: call(outs[1]))
+    call(outs[0])
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and any(bool(t.any()) for t in outs[0])
